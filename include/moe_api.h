@@ -442,6 +442,125 @@ moe_status moe_dispatch_align_noalloc(const moe_config* cfg, int32_t T, const in
                                       int32_t* num_padded, int32_t* expert_counts,
                                       int32_t* num_dropped, int32_t* status_out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The layer on 4-bit experts: residual + RMS norm, routing by scores,
+ * microscaled (MX) 4-bit tensors and the grouped expert FFN on them.
+ *
+ * An MX tensor [rows, K] (K % 32 == 0) is two byte arrays, row-major:
+ *   codes  [rows, K/2]   two e2m1 values a byte, the even element in the low
+ *                        half; sign, 2 exponent bits, 1 mantissa bit:
+ *                        0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *   scales [rows, K/32]  one E8M0 byte b per 32 elements: 2^(b - 127); 255: NaN
+ * A block of 32 converts with the exponent floor(log2(amax)) - 2 of its
+ * largest magnitude amax (at least -127, which an all-zero block takes); each
+ * element is rounded to the nearest value, ties to the even mantissa, and
+ * saturates at 6.  A block that holds an infinity or a NaN gets the scale 255
+ * and zero codes: all its elements read as NaN.
+ * ------------------------------------------------------------------------ */
+
+/* Residual addition, root-mean-square norm and the normalised row in 4 bits:
+ *   v = x + residual (fp32);  residual_out = bf16(v)
+ *   out = bf16(v / sqrt(mean(v^2) + eps) * weight)
+ *   codes, scales = the MX tensor of out (the bf16 values, stored or not)
+ *   x, residual [T, H] bf16 (residual NULL: v = x), weight [H] bf16,
+ *   residual_out [T, H] bf16 or NULL, out [T, H] bf16 or NULL,
+ *   codes [T, H/2] and scales [T, H/32], both or neither; out or codes given.
+ * residual_out may be x or residual itself (each row is read before it is
+ * written), and so may out; no other overlap.  H % 32 == 0, H <= 32768.  The sum of squares
+ * has one order for every T. */
+moe_status moe_add_norm(int32_t T, int32_t H, const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
+                        float eps, uint16_t* residual_out, uint16_t* out, uint8_t* codes, uint8_t* scales,
+                        void* stream);
+
+/* How moe_route_scored scores and selects.  Zero-initialise: zero is the
+ * default of every field. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_GROUP_MAX 0
+#define MOE_GROUP_TOP2_SUM 1
+typedef struct moe_scoring {
+  int32_t score;        /* MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID */
+  int32_t num_groups;   /* groups of N / num_groups consecutive experts; 0, 1: no groups; <= 32 */
+  int32_t top_groups;   /* groups a token may use; 0: all */
+  int32_t group_score;  /* MOE_GROUP_MAX or MOE_GROUP_TOP2_SUM (groups of at least two) */
+  int32_t renormalize;  /* 1: gates divided by the sum of the selected scores */
+  float scale;          /* factor of the gates; 0: 1 */
+} moe_scoring;
+
+/* Checks a scoring against a configuration (token choice; top_k experts have
+ * to fit into top_groups groups). */
+moe_status moe_check_scoring(const moe_config* cfg, const moe_scoring* scoring);
+
+/* Top-k routing by scores, from the logits of every expert (e.g. of
+ * moe_router_logits):
+ *   s = softmax(l) or 1 / (1 + exp(-l));  b = s + score_bias (selection only)
+ *   groups rank by the largest b or the sum of the two largest; the experts
+ *   outside the top_groups best are left out (not scored as zero)
+ *   the k largest b; gate = scale * s, with renormalize scale * s / (sum of the
+ *   selected s in slot order + 1e-20)
+ *   logits [T, N] fp32, score_bias [N] fp32 or NULL
+ *   topk_idx [T, k] int32 out, experts in ascending index; topk_gate [T, k] fp32 out
+ * Ties go to the lower index (of expert and of group); NaN ranks last.  A row
+ * of -inf logits has softmax scores of zero. */
+moe_status moe_route_scored(const moe_config* cfg, const moe_scoring* scoring, int32_t T, const float* logits,
+                            const float* score_bias, int32_t* topk_idx, float* topk_gate, void* stream);
+
+/* x [rows, K] bf16 -> MX tensor. */
+moe_status moe_quantize_mx(int64_t rows, int32_t K, const uint16_t* x, uint8_t* codes, uint8_t* scales,
+                           void* stream);
+/* MX tensor -> out [rows, K] bf16 (exact, but for values past bf16's range). */
+moe_status moe_dequantize_mx(int64_t rows, int32_t K, const uint8_t* codes, const uint8_t* scales, uint16_t* out,
+                             void* stream);
+/* Expert weights as moe_expert_ffn takes them, w [experts, K, F] bf16, to the
+ * K-major MX tensor [experts, F, K] (blocks along K): w13 [N, H, 2I] -> [N,
+ * 2I, H], w2 [N, I, H] -> [N, H, I].  K % 32 == 0, F % 8 == 0. */
+moe_status moe_quantize_weights_mx(int32_t experts, int32_t K, int32_t F, const uint16_t* w, uint8_t* codes,
+                                   uint8_t* scales, void* stream);
+/* Scales of an MX weight tensor [experts, rows, K/32] in the order the GEMMs
+ * read them (same number of bytes; done once, when the weights are loaded).
+ * gate_up = 1 for w13 and w13_shared, 0 for w2 and w2_shared.  rows % 128 ==
+ * 0, K % 128 == 0. */
+moe_status moe_pack_scales_mx(int32_t experts, int32_t rows, int32_t K, int32_t gate_up, const uint8_t* scales,
+                              uint8_t* packed, void* stream);
+
+/* Bytes of workspace of moe_expert_ffn_mx and moe_forward_mx for up to
+ * max_tokens tokens (0 if the configuration is invalid).  The device status
+ * word is at its start, as in moe_workspace_bytes. */
+size_t moe_workspace_bytes_mx(const moe_config* cfg, int32_t max_tokens);
+
+/* moe_expert_ffn on 4-bit operands: for every padded row p with route r of
+ * expert e,
+ *   [g | u] = x[r / S] . W13_e,  a = MX(silu(g) * u),  y_perm[p] = bf16(a . W2_e)
+ * x, W and a MX tensors, fp32 accumulation, silu(g) * u rounded once (fp32 to
+ * e2m1).  With shared_intermediate > 0 y_shared[t] is the shared expert's
+ * output.
+ *   x_codes [T, H/2], x_scales [T, H/32]
+ *   w13 [N, 2I, H/2] (gate rows 0..I-1, up rows I..2I-1), w2 [N, H, I/2], and
+ *   w13_shared [2Is, H/2], w2_shared [H, Is/2] (or NULL): codes; their scales
+ *   as moe_pack_scales_mx writes them
+ *   sorted_route_ids, block_expert, num_padded, y_perm, y_shared: as in moe_expert_ffn
+ * One K order and no split-K: a row does not depend on the batch. */
+moe_status moe_expert_ffn_mx(const moe_config* cfg, int32_t T, const uint8_t* x_codes, const uint8_t* x_scales,
+                             const uint8_t* w13, const uint8_t* w13_scales, const uint8_t* w2,
+                             const uint8_t* w2_scales, const uint8_t* w13_shared, const uint8_t* w13_shared_scales,
+                             const uint8_t* w2_shared, const uint8_t* w2_shared_scales,
+                             const int32_t* sorted_route_ids, const int32_t* block_expert, const int32_t* num_padded,
+                             uint16_t* y_perm, uint16_t* y_shared, void* ws, size_t ws_bytes, void* stream);
+
+/* A pre-norm MoE layer on 4-bit experts:
+ *   v, n, MX(n) = moe_add_norm(x, residual);  logits = moe_router_logits(n)
+ *   moe_route_scored -> moe_dispatch_align -> moe_expert_ffn_mx(MX(n))
+ *   out = moe_combine with h = bf16(v): v + sum of gate * y + y_shared
+ * residual NULL: v = x.  Token choice; the drop policy where a capacity is
+ * set.  Weights as in moe_expert_ffn_mx, w_gate and router_bias as in
+ * moe_route, score_bias as in moe_route_scored; out [T, H] bf16. */
+moe_status moe_forward_mx(const moe_config* cfg, const moe_scoring* scoring, int32_t T, const uint16_t* x,
+                          const uint16_t* residual, const uint16_t* norm_weight, float eps, const uint16_t* w_gate,
+                          const float* router_bias, const float* score_bias, const uint8_t* w13,
+                          const uint8_t* w13_scales, const uint8_t* w2, const uint8_t* w2_scales,
+                          const uint8_t* w13_shared, const uint8_t* w13_shared_scales, const uint8_t* w2_shared,
+                          const uint8_t* w2_shared_scales, uint16_t* out, void* ws, size_t ws_bytes, void* stream);
+
 /* Reads the device status word of `ws` (synchronises `stream`): the whole word
  * in *status_out; MOE_ERR_DEVICE if any bit of MOE_DEV_ERR_MASK is set. */
 moe_status moe_get_device_status(const void* ws, int32_t* status_out, void* stream);

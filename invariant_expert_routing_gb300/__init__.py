@@ -51,6 +51,10 @@ MOE_OVERFLOW_DROP = 0
 MOE_OVERFLOW_REROUTE = 1
 MOE_ROUTING_TOKEN_CHOICE = 0
 MOE_ROUTING_EXPERT_CHOICE = 1
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_GROUP_MAX = 0
+MOE_GROUP_TOP2_SUM = 1
 
 
 class moe_config(ctypes.Structure):
@@ -60,6 +64,12 @@ class moe_config(ctypes.Structure):
                 ("shared_intermediate", ctypes.c_int32), ("overflow_policy", ctypes.c_int32),
                 ("routing", ctypes.c_int32), ("debug_flags", ctypes.c_uint32),
                 ("debug_grid_ctas", ctypes.c_int32), ("debug_wait_ns", ctypes.c_int64)]
+
+
+class moe_scoring(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("num_groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class moe_route_stats(ctypes.Structure):
@@ -78,6 +88,7 @@ class MoEError(RuntimeError):
 
 _vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 _cfgp = ctypes.POINTER(moe_config)
+_scp = ctypes.POINTER(moe_scoring)
 _SIGS = {
     "moe_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "moe_check_config": ([_cfgp], ctypes.c_int),
@@ -103,6 +114,17 @@ _SIGS = {
     "moe_route_expert_choice": ([_cfgp, _i32] + [_vp] * 8 + [_vp, _sz, _vp], ctypes.c_int),
     "moe_routing_stats": ([_cfgp, _i32, _vp, ctypes.c_double, _vp, _vp, _vp], ctypes.c_int),
     "moe_router_margin": ([_cfgp, _i32, _vp, _vp, _vp], ctypes.c_int),
+    "moe_add_norm": ([_i32, _i32] + [_vp] * 3 + [ctypes.c_float] + [_vp] * 5, ctypes.c_int),
+    "moe_check_scoring": ([_cfgp, _scp], ctypes.c_int),
+    "moe_route_scored": ([_cfgp, _scp, _i32] + [_vp] * 5, ctypes.c_int),
+    "moe_quantize_mx": ([ctypes.c_int64, _i32] + [_vp] * 4, ctypes.c_int),
+    "moe_dequantize_mx": ([ctypes.c_int64, _i32] + [_vp] * 4, ctypes.c_int),
+    "moe_quantize_weights_mx": ([_i32, _i32, _i32] + [_vp] * 4, ctypes.c_int),
+    "moe_pack_scales_mx": ([_i32, _i32, _i32, _i32] + [_vp] * 3, ctypes.c_int),
+    "moe_workspace_bytes_mx": ([_cfgp, _i32], _sz),
+    "moe_expert_ffn_mx": ([_cfgp, _i32] + [_vp] * 16 + [_sz, _vp], ctypes.c_int),
+    "moe_forward_mx": ([_cfgp, _scp, _i32] + [_vp] * 3 + [ctypes.c_float] + [_vp] * 13 + [_sz, _vp],
+                       ctypes.c_int),
     "moe_get_device_status": ([_vp, ctypes.POINTER(_i32), _vp], ctypes.c_int),
     "moe_clear_device_status": ([_vp, _vp], ctypes.c_int),
 }
@@ -346,3 +368,176 @@ def moe_get_device_status(ws, stream=None) -> int:
 
 def moe_clear_device_status(ws, stream=None) -> None:
     _check("moe_clear_device_status", _lib.moe_clear_device_status(_ptr(ws), _stream(stream)))
+
+
+# ---- the layer on 4-bit experts (microscaled e2m1 tensors: codes and scales)
+
+def make_scoring(score=MOE_SCORE_SOFTMAX, num_groups=0, top_groups=0, group_score=MOE_GROUP_MAX,
+                 renormalize=False, scale=0.0) -> moe_scoring:
+    return moe_scoring(score, num_groups, top_groups, group_score, int(renormalize), scale)
+
+
+def _scoring(scoring) -> moe_scoring:
+    return scoring if isinstance(scoring, moe_scoring) else make_scoring(**scoring)
+
+
+def _want(name, t, dtype, shape, optional=False):
+    """A contiguous CUDA tensor of this type and shape (the C entry points see pointers only)."""
+    import torch
+    if t is None:
+        if optional:
+            return
+        raise ValueError(f"{name}: a tensor is needed")
+    if t.dtype != getattr(torch, dtype) or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: a contiguous CUDA tensor of {dtype} {tuple(shape)} is needed, got "
+                         f"{t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'} on {t.device}")
+
+
+def _want_at_least(name, t, dtype, n):
+    """A contiguous CUDA tensor of this type with at least n elements."""
+    import torch
+    if t is None or t.dtype != getattr(torch, dtype) or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: a contiguous CUDA tensor of at least {n} {dtype} is needed")
+
+
+def moe_check_scoring(cfg, scoring) -> int:
+    return int(_lib.moe_check_scoring(ctypes.byref(_cfg(cfg)), ctypes.byref(_scoring(scoring))))
+
+
+def moe_add_norm(x, residual, weight, eps, residual_out, out, codes=None, scales=None, stream=None):
+    """x [T, H] bf16 (+ residual) -> residual_out, out [T, H] bf16 and the MX tensor of out;
+    residual, residual_out, out and the pair (codes, scales) may be None."""
+    T, H = x.shape
+    _want("x", x, "bfloat16", (T, H))
+    _want("residual", residual, "bfloat16", (T, H), optional=True)
+    _want("weight", weight, "bfloat16", (H,))
+    _want("residual_out", residual_out, "bfloat16", (T, H), optional=True)
+    _want("out", out, "bfloat16", (T, H), optional=True)
+    _want("codes", codes, "uint8", (T, H // 2), optional=True)
+    _want("scales", scales, "uint8", (T, H // 32), optional=True)
+    _check("moe_add_norm", _lib.moe_add_norm(
+        T, H, _ptr(x), _ptr(residual), _ptr(weight), float(eps), _ptr(residual_out), _ptr(out),
+        _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def moe_route_scored(cfg, scoring, logits, score_bias, topk_idx, topk_gate, stream=None):
+    c = _cfg(cfg)
+    T = logits.shape[0]
+    _want("logits", logits, "float32", (T, c.num_experts))
+    _want("score_bias", score_bias, "float32", (c.num_experts,), optional=True)
+    _want("topk_idx", topk_idx, "int32", (T, c.top_k))
+    _want("topk_gate", topk_gate, "float32", (T, c.top_k))
+    _check("moe_route_scored", _lib.moe_route_scored(
+        ctypes.byref(c), ctypes.byref(_scoring(scoring)), T, _ptr(logits), _ptr(score_bias),
+        _ptr(topk_idx), _ptr(topk_gate), _stream(stream)))
+
+
+def _mx_shape(codes, scales, lead, K):
+    _want("codes", codes, "uint8", (*lead, K // 2))
+    _want("scales", scales, "uint8", (*lead, K // 32))
+
+
+def moe_quantize_mx(x, codes, scales, stream=None):
+    """x [..., K] bf16 -> codes [..., K/2], scales [..., K/32] (uint8)."""
+    *lead, K = x.shape
+    _want("x", x, "bfloat16", x.shape)
+    _mx_shape(codes, scales, lead, K)
+    _check("moe_quantize_mx", _lib.moe_quantize_mx(
+        x.numel() // K if K else 0, K, _ptr(x), _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def moe_dequantize_mx(codes, scales, out, stream=None):
+    """codes [..., K/2], scales [..., K/32] -> out [..., K] bf16."""
+    *lead, K = out.shape
+    _want("out", out, "bfloat16", out.shape)
+    _mx_shape(codes, scales, lead, K)
+    _check("moe_dequantize_mx", _lib.moe_dequantize_mx(
+        out.numel() // K if K else 0, K, _ptr(codes), _ptr(scales), _ptr(out), _stream(stream)))
+
+
+def moe_quantize_weights_mx(w, codes, scales, stream=None):
+    """w [experts, K, F] bf16 -> codes [experts, F, K/2], scales [experts, F, K/32]."""
+    E, K, F = w.shape
+    _want("w", w, "bfloat16", (E, K, F))
+    _mx_shape(codes, scales, (E, F), K)
+    _check("moe_quantize_weights_mx", _lib.moe_quantize_weights_mx(
+        E, K, F, _ptr(w), _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def moe_pack_scales_mx(scales, packed, gate_up, stream=None):
+    """scales [experts, rows, K/32] -> packed, the same shape, in the GEMMs' order."""
+    E, rows, blocks = scales.shape
+    _want("scales", scales, "uint8", scales.shape)
+    _want("packed", packed, "uint8", scales.shape)
+    _check("moe_pack_scales_mx", _lib.moe_pack_scales_mx(
+        E, rows, blocks * 32, int(gate_up), _ptr(scales), _ptr(packed), _stream(stream)))
+
+
+def moe_workspace_bytes_mx(cfg, max_tokens: int) -> int:
+    return int(_lib.moe_workspace_bytes_mx(ctypes.byref(_cfg(cfg)), max_tokens))
+
+
+def workspace_mx(cfg, max_tokens: int, device="cuda"):
+    """A torch uint8 tensor for moe_expert_ffn_mx and moe_forward_mx with up to max_tokens tokens."""
+    import torch
+    n = moe_workspace_bytes_mx(cfg, max_tokens)
+    if n == 0:
+        raise MoEError("moe_workspace_bytes_mx", MOE_ERR_UNSUPPORTED)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _want_experts(c, w13, w13_scales, w2, w2_scales, w13_shared, w13_shared_scales, w2_shared, w2_shared_scales):
+    N, H, I, Is = c.num_experts, c.hidden, c.intermediate, c.shared_intermediate
+    _want("w13", w13, "uint8", (N, 2 * I, H // 2))
+    _want("w13_scales", w13_scales, "uint8", (N, 2 * I, H // 32))
+    _want("w2", w2, "uint8", (N, H, I // 2))
+    _want("w2_scales", w2_scales, "uint8", (N, H, I // 32))
+    if Is > 0:
+        _want_at_least("w13_shared", w13_shared, "uint8", 2 * Is * (H // 2))
+        _want_at_least("w13_shared_scales", w13_shared_scales, "uint8", 2 * Is * (H // 32))
+        _want_at_least("w2_shared", w2_shared, "uint8", H * (Is // 2))
+        _want_at_least("w2_shared_scales", w2_shared_scales, "uint8", H * (Is // 32))
+
+
+def moe_expert_ffn_mx(cfg, x_codes, x_scales, w13, w13_scales, w2, w2_scales, w13_shared,
+                      w13_shared_scales, w2_shared, w2_shared_scales, sorted_route_ids, block_expert,
+                      num_padded, y_perm, y_shared, ws, stream=None):
+    """moe_expert_ffn on MX operands; every *_scales of the weights is packed (moe_pack_scales_mx)."""
+    c = _cfg(cfg)
+    T, H = x_codes.shape[0], c.hidden
+    _want("x_codes", x_codes, "uint8", (T, H // 2))
+    _want("x_scales", x_scales, "uint8", (T, H // 32))
+    _want_experts(c, w13, w13_scales, w2, w2_scales, w13_shared, w13_shared_scales, w2_shared, w2_shared_scales)
+    rows = moe_max_padded_rows(c, T)
+    _want_at_least("sorted_route_ids", sorted_route_ids, "int32", rows)
+    _want_at_least("block_expert", block_expert, "int32", moe_max_blocks(c, T))
+    _want_at_least("num_padded", num_padded, "int32", 1)
+    _want_at_least("y_perm", y_perm, "bfloat16", rows * H)
+    if c.shared_intermediate > 0:
+        _want_at_least("y_shared", y_shared, "bfloat16", T * H)
+    _check("moe_expert_ffn_mx", _lib.moe_expert_ffn_mx(
+        ctypes.byref(c), T, _ptr(x_codes), _ptr(x_scales), _ptr(w13), _ptr(w13_scales), _ptr(w2),
+        _ptr(w2_scales), _ptr(w13_shared), _ptr(w13_shared_scales), _ptr(w2_shared),
+        _ptr(w2_shared_scales), _ptr(sorted_route_ids), _ptr(block_expert), _ptr(num_padded), _ptr(y_perm),
+        _ptr(y_shared), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_forward_mx(cfg, scoring, x, residual, norm_weight, eps, w_gate, router_bias, score_bias, w13,
+                   w13_scales, w2, w2_scales, w13_shared, w13_shared_scales, w2_shared, w2_shared_scales,
+                   out, ws, stream=None):
+    """The pre-norm layer on MX experts: norm, router, dispatch, expert FFN, combine into x + residual."""
+    c = _cfg(cfg)
+    T, H = x.shape[0], c.hidden
+    _want("x", x, "bfloat16", (T, H))
+    _want("residual", residual, "bfloat16", (T, H), optional=True)
+    _want("norm_weight", norm_weight, "bfloat16", (H,))
+    _want("w_gate", w_gate, "bfloat16", (H, c.num_experts))
+    _want("router_bias", router_bias, "float32", (c.num_experts,), optional=True)
+    _want("score_bias", score_bias, "float32", (c.num_experts,), optional=True)
+    _want_experts(c, w13, w13_scales, w2, w2_scales, w13_shared, w13_shared_scales, w2_shared, w2_shared_scales)
+    _want("out", out, "bfloat16", (T, H))
+    _check("moe_forward_mx", _lib.moe_forward_mx(
+        ctypes.byref(c), ctypes.byref(_scoring(scoring)), T, _ptr(x), _ptr(residual), _ptr(norm_weight),
+        float(eps), _ptr(w_gate), _ptr(router_bias), _ptr(score_bias), _ptr(w13), _ptr(w13_scales),
+        _ptr(w2), _ptr(w2_scales), _ptr(w13_shared), _ptr(w13_shared_scales), _ptr(w2_shared),
+        _ptr(w2_shared_scales), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))

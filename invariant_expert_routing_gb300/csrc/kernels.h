@@ -195,4 +195,23 @@ void launch_combine(const uint16_t* h, const float* gates, const uint8_t* route_
                     const int32_t* route_pos, const uint16_t* y_perm, const uint16_t* y_shared,
                     uint16_t* out, int T, int H, int k, int64_t max_rows, cudaStream_t s);
 
+// ---- microscaled 4-bit format (mx.cuh), residual + norm, routing by scores
+void launch_quantize_mx(const uint16_t* x, size_t elements, uint8_t* codes, uint8_t* scales, cudaStream_t s);
+void launch_dequantize_mx(const uint8_t* codes, const uint8_t* scales, size_t elements, uint16_t* out,
+                          cudaStream_t s);
+// w [experts, K, F] -> codes [experts, F, K/2], scales [experts, F, K/32]
+void launch_quantize_weights_mx(const uint16_t* w, int experts, int K, int F, uint8_t* codes, uint8_t* scales,
+                                cudaStream_t s);
+// scales [experts, rows, K/32] -> the grouped GEMM's 512-byte chunks
+void launch_pack_scales_mx(const uint8_t* scales, int experts, int rows, int K, bool gate_up, uint8_t* packed,
+                           cudaStream_t s);
+// residual, residual_out, out, codes and scales may be null
+void launch_add_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps, int T, int H,
+                     uint16_t* residual_out, uint16_t* out, uint8_t* codes, uint8_t* scales, int sms,
+                     cudaStream_t s);
+int route_scored_max_groups();
+void launch_route_scored(const float* logits, const float* bias, int T, int N, int k, bool sigmoid, int groups,
+                         int top_groups, bool top2, bool renormalize, float scale, int32_t* topk_idx,
+                         float* topk_gate, cudaStream_t s);
+
 }  // namespace moe

@@ -11,6 +11,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "api_internal.h"
 #include "kernels.h"
 
 namespace {
@@ -721,12 +722,6 @@ moe_status forward_impl(const moe_config* c, int32_t T, const uint16_t* h, const
   return last_cuda();
 }
 
-#define MOE_TRY(x)                   \
-  do {                               \
-    const moe_status _st = (x);      \
-    if (_st != MOE_OK) return _st;   \
-  } while (0)
-
 moe_status need(const void* p) { return (p && aligned16(p)) ? MOE_OK : MOE_ERR_INVALID_ARG; }
 moe_status opt(const void* p) { return (!p || aligned16(p)) ? MOE_OK : MOE_ERR_INVALID_ARG; }
 
@@ -739,6 +734,25 @@ moe_status check_shared(const moe_config* c, const void* w13s, const void* w2s) 
 }
 
 }  // namespace
+
+namespace moe {
+namespace api {
+
+moe_status check_config(const moe_config* c) { return check_cfg(c); }
+moe_status check_tokens(const moe_config* c, int32_t T) { return check_T(c, T); }
+int32_t capacity(const moe_config* c, int32_t T) { return capacity_of(c, T); }
+int slots(const moe_config* c) { return slots_of(c); }
+int64_t max_rows(const moe_config* c, int32_t T) { return max_rows_of(c, T); }
+int64_t max_blocks(const moe_config* c, int32_t T) { return max_blocks_of(c, T); }
+int64_t max_tiles(const moe_config* c, int32_t T, int tile_rows) { return max_gemm_tiles_of(c, T, tile_rows); }
+int sm_count() { return num_sms(); }
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode() { return encode_fn(); }
+moe_status last_error() { return last_cuda(); }
+moe_status need(const void* p) { return ::need(p); }
+moe_status optional(const void* p) { return ::opt(p); }
+
+}  // namespace api
+}  // namespace moe
 
 extern "C" {
 

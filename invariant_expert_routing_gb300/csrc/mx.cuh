@@ -1,0 +1,164 @@
+// Microscaled (MX) 4-bit format and the block-scaled tcgen05 helpers.
+//
+// MX e2m1: 32 consecutive elements share one E8M0 scale byte (2^(byte - 127),
+// 255 = NaN); each element is sign, 2 exponent bits, 1 mantissa bit: 0, 0.5,
+// 1, 1.5, 2, 3, 4, 6.  Conversion of a block with largest magnitude amax:
+//   byte = max(E - 2, 0), E the biased fp32 exponent of amax, so that
+//   amax / 2^(byte - 127) lies in [4, 8); elements round to nearest even and
+//   saturate at 6.  A block holding an infinity or a NaN gets byte 255 and
+//   zero codes (every element reads as NaN).
+// Two codes a byte, the even element in the low half.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace moe {
+namespace mx {
+
+constexpr int kBlock = 32;                // elements per scale
+constexpr int kSfRows = 128;              // rows of one scale chunk
+constexpr int kSfChunkK = 128;            // reduction elements of one scale chunk (4 scale bytes a row)
+constexpr uint32_t kSfChunkBytes = 512;   // 128 rows x 4 bytes
+
+// Scale byte of a block from the bits of its largest magnitude (sign clear).
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
+  const uint32_t e = amax_bits >> 23;
+  return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+}
+// 2^(127 - byte): what elements are multiplied by before rounding (byte <= 253).
+__device__ __forceinline__ float scale_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// 2^(byte - 127); 255: NaN.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7FFFFFFFu : (byte == 0u ? 0x00400000u : byte << 23));
+}
+
+// Eight values (already scaled) to eight codes, v[0] in the lowest half byte.
+__device__ __forceinline__ uint32_t pack8(const float (&v)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// Byte offset, inside one 512-byte chunk, of row r's four scale bytes (r <
+// 128): the order in which tcgen05.cp 32x128b puts rows r, r + 32, r + 64,
+// r + 96 into four neighbouring TMEM columns of lane r % 32.
+__host__ __device__ constexpr uint32_t sf_row_offset(uint32_t r) { return (r & 31u) * 16u + (r >> 5) * 4u; }
+
+// Codes and scale byte of a block held by four neighbouring lanes, eight bf16
+// elements a lane (full warp converged).  Integer maxima of the magnitudes'
+// bits order every value, infinities and NaN above the finite ones.
+__device__ __forceinline__ uint32_t quantize8(const uint4& x, uint32_t& byte) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  m = max(m & 0xFFFFu, m >> 16);
+  byte = scale_byte(m << 16);
+  if (byte == 255u) return 0u;
+  const float inv = scale_inverse(byte);
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16) * inv;
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
+  }
+  return pack8(v);
+}
+
+// ---------------------------------------------------------------- PTX
+// Untiled bulk copy, global to shared (16-byte aligned, size % 16 == 0).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// Shared-memory descriptor of a 32 x 16-byte matrix stored without swizzle:
+// 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(128u >> 4) << 16;
+  d |= (uint64_t)(128u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  return d;
+}
+
+// 512 bytes of scales into four TMEM columns, the same in all four lane quarters.
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// Instruction descriptor of kind::mxf4: e2m1 A and B (both K-major, 64
+// elements per MMA), E8M0 scales, fp32 D.  Bits: B scale id [4,6); A type
+// [7,10) = 1; B type [10,12) = 1; N >> 3 at [17,23); scale type [23] = 1
+// (E8M0); M >> 7 at [27,29); A scale id [29,31).  The scale id (0 or 2)
+// names the half of a row's four scale bytes that the MMA uses.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int half) {
+  return ((uint32_t)(half * 2) << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(M >> 7) << 27) | ((uint32_t)(half * 2) << 29);
+}
+
+// D[tmem] (+)= (A . sfa) x (B . sfb) over 64 elements of K; single thread.
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// 32 consecutive fp32 columns of the thread's TMEM lane, complete on return
+// (the wait is part of the statement, so no use can be moved before it).
+__device__ __forceinline__ void tmem_load32(uint32_t taddr, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]),
+        "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]),
+        "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+// Two such column ranges.
+__device__ __forceinline__ void tmem_load32x2(uint32_t ta, float (&a)[32], uint32_t tb, float (&b)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3]), "=f"(a[4]), "=f"(a[5]), "=f"(a[6]), "=f"(a[7]),
+        "=f"(a[8]), "=f"(a[9]), "=f"(a[10]), "=f"(a[11]), "=f"(a[12]), "=f"(a[13]), "=f"(a[14]), "=f"(a[15]),
+        "=f"(a[16]), "=f"(a[17]), "=f"(a[18]), "=f"(a[19]), "=f"(a[20]), "=f"(a[21]), "=f"(a[22]),
+        "=f"(a[23]), "=f"(a[24]), "=f"(a[25]), "=f"(a[26]), "=f"(a[27]), "=f"(a[28]), "=f"(a[29]),
+        "=f"(a[30]), "=f"(a[31]),
+        "=f"(b[0]), "=f"(b[1]), "=f"(b[2]), "=f"(b[3]), "=f"(b[4]), "=f"(b[5]), "=f"(b[6]), "=f"(b[7]),
+        "=f"(b[8]), "=f"(b[9]), "=f"(b[10]), "=f"(b[11]), "=f"(b[12]), "=f"(b[13]), "=f"(b[14]), "=f"(b[15]),
+        "=f"(b[16]), "=f"(b[17]), "=f"(b[18]), "=f"(b[19]), "=f"(b[20]), "=f"(b[21]), "=f"(b[22]),
+        "=f"(b[23]), "=f"(b[24]), "=f"(b[25]), "=f"(b[26]), "=f"(b[27]), "=f"(b[28]), "=f"(b[29]),
+        "=f"(b[30]), "=f"(b[31])
+      : "r"(ta), "r"(tb)
+      : "memory");
+}
+
+}  // namespace mx
+}  // namespace moe

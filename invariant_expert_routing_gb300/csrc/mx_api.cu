@@ -1,0 +1,429 @@
+// C ABI of the 4-bit expert path (include/moe_api.h): residual + norm,
+// routing by scores, microscaled 4-bit conversion, the grouped expert FFN on
+// 4-bit operands and the pre-norm block that runs them together.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "api_internal.h"
+#include "kernels.h"
+#include "mx_gemm.h"
+
+namespace {
+
+using moe::GemmTile;
+namespace api = moe::api;
+
+constexpr int kSfBlock = 32;      // elements per scale
+constexpr int kMaxHidden = 32768;
+
+size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Bytes of the scale chunks of `tiles` 128-row tiles with K elements a row.
+size_t sf_bytes(int64_t tiles, int K) { return (size_t)tiles * moe::kMxTileRows * (K / kSfBlock); }
+
+// Workspace regions, each 256-byte aligned; the status word is at offset 0.
+struct Layout {
+  size_t status, tiles, num_tiles, x_perm, x_sf, a, a_sf, x_sh_sf, a_sh, a_sh_sf,
+      // moe_forward_mx alone
+      residual, norm, codes, scales, logits, rpart, topk, gates, kept, pos, rank, tile_count, seg_off, sorted, blocks,
+      num_padded, counts, dropped, y, y_sh, total;
+};
+
+Layout layout_of(const moe_config* c, int32_t T) {
+  const size_t N = c->num_experts, H = c->hidden, I = c->intermediate, Is = c->shared_intermediate;
+  const size_t R = (size_t)T * api::slots(c), rows = (size_t)api::max_rows(c, T);
+  const int64_t tiles = api::max_tiles(c, T, moe::kMxTileRows);
+  const int64_t tiles_t = ((int64_t)T + moe::kMxTileRows - 1) / moe::kMxTileRows;
+  Layout L{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = round_up(off + bytes, 256);
+    return at;
+  };
+  L.status = take(sizeof(int32_t));
+  L.tiles = take(sizeof(GemmTile) * (size_t)tiles);
+  L.num_tiles = take(2 * sizeof(int32_t));
+  // the activations keep one tile of rows of slack so that every tile load stays inside them
+  L.x_perm = take((rows + moe::kMxTileRows) * H / 2);
+  L.x_sf = take(sf_bytes(tiles, (int)H));
+  L.a = take((rows + moe::kMxTileRows) * I / 2);
+  L.a_sf = take(sf_bytes(tiles, (int)I));
+  L.x_sh_sf = take(Is ? sf_bytes(tiles_t, (int)H) : 0);
+  L.a_sh = take(Is ? ((size_t)T + moe::kMxTileRows) * Is / 2 : 0);
+  L.a_sh_sf = take(Is ? sf_bytes(tiles_t, (int)Is) : 0);
+  L.residual = take(2 * (size_t)T * H);
+  L.norm = take(2 * (size_t)T * H);
+  L.codes = take((size_t)T * H / 2);
+  L.scales = take((size_t)T * H / kSfBlock);
+  L.logits = take(sizeof(float) * (size_t)T * N);
+  L.rpart = take(sizeof(float) * moe::chunked_router_part_floats(T, (int)H, (int)N));
+  L.topk = take(sizeof(int32_t) * R);
+  L.gates = take(sizeof(float) * R);
+  L.kept = take(R);
+  L.pos = take(sizeof(int32_t) * R);
+  L.rank = take(sizeof(int32_t) * R);
+  L.tile_count = take(sizeof(int32_t) * ((R + moe::kDispatchTile - 1) / moe::kDispatchTile) * N);
+  L.seg_off = take(sizeof(int32_t) * N);
+  L.sorted = take(sizeof(int32_t) * rows);
+  L.blocks = take(sizeof(int32_t) * (size_t)api::max_blocks(c, T));
+  L.num_padded = take(sizeof(int32_t));
+  L.counts = take(sizeof(int32_t) * N);
+  L.dropped = take(sizeof(int32_t));
+  L.y = take(2 * rows * H);
+  L.y_sh = take(Is ? 2 * (size_t)T * H : 0);
+  L.total = off;
+  return L;
+}
+
+template <class P>
+P* at(void* ws, size_t off) {
+  return reinterpret_cast<P*>(static_cast<char*>(ws) + off);
+}
+
+moe_status check_ws(const moe_config* c, int32_t T, const void* ws, size_t ws_bytes) {
+  MOE_TRY(api::need(ws));
+  return ws_bytes < layout_of(c, T).total ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+moe_status check_scoring(const moe_config* c, const moe_scoring* s) {
+  if (!s) return MOE_ERR_INVALID_ARG;
+  if (s->score != MOE_SCORE_SOFTMAX && s->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (s->group_score != MOE_GROUP_MAX && s->group_score != MOE_GROUP_TOP2_SUM) return MOE_ERR_INVALID_ARG;
+  if (s->renormalize != 0 && s->renormalize != 1) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(s->scale) || s->scale < 0.0f) return MOE_ERR_INVALID_ARG;
+  if (c->routing != MOE_ROUTING_TOKEN_CHOICE) return MOE_ERR_INVALID_ARG;
+  const int N = c->num_experts;
+  const int groups = s->num_groups == 0 ? 1 : s->num_groups;
+  const int top = s->top_groups == 0 ? groups : s->top_groups;
+  if (groups < 1 || top < 1 || top > groups || N % groups) return MOE_ERR_INVALID_ARG;
+  if (groups > moe::route_scored_max_groups()) return MOE_ERR_UNSUPPORTED;
+  if (groups > 1 && s->group_score == MOE_GROUP_TOP2_SUM && N / groups < 2) return MOE_ERR_INVALID_ARG;
+  if (c->top_k > top * (N / groups)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status route_impl(const moe_config* c, const moe_scoring* s, int32_t T, const float* logits,
+                      const float* score_bias, int32_t* idx, float* gate, cudaStream_t st) {
+  const int groups = s->num_groups == 0 ? 1 : s->num_groups;
+  const int top = s->top_groups == 0 ? groups : s->top_groups;
+  moe::launch_route_scored(logits, score_bias, T, c->num_experts, c->top_k, s->score == MOE_SCORE_SIGMOID,
+                           top == groups ? 1 : groups, top, s->group_score == MOE_GROUP_TOP2_SUM, s->renormalize != 0,
+                           s->scale == 0.0f ? 1.0f : s->scale, idx, gate, st);
+  return api::last_error();
+}
+
+// ----------------------------------------------------------------- tensor maps
+// Byte tensors with 128-byte swizzle, 128 bytes (256 elements) of K a box.
+bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+  auto fn = api::tensor_map_encode();
+  if (!fn) return false;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool map_rows(CUtensorMap* m, const void* base, int K, uint64_t rows, uint32_t box_rows) {
+  const cuuint64_t pitch = (cuuint64_t)K / 2;
+  const cuuint64_t dims[2] = {pitch, rows}, strides[1] = {pitch};
+  const cuuint32_t box[2] = {128, box_rows};
+  return encode(m, base, 2, dims, strides, box);
+}
+
+// W13 [N, 2I, K/2]: (byte, row of a 32-feature block, gate/up, block, expert),
+// so that one box holds 32 gate and the same 32 up rows in turns.
+bool map_w13(CUtensorMap* m, const void* base, int K, int I, int N, int tile_features) {
+  const cuuint64_t pitch = (cuuint64_t)K / 2;
+  const cuuint64_t dims[5] = {pitch, 32, 2, (cuuint64_t)I / 32, (cuuint64_t)N};
+  const cuuint64_t strides[4] = {pitch, pitch * I, pitch * 32, pitch * 2 * I};
+  const cuuint32_t box[5] = {128, 32, 2, (cuuint32_t)tile_features / 64, 1};
+  return encode(m, base, 5, dims, strides, box);
+}
+
+// W2 [N, H, I/2]: (byte, row, expert); rows past an expert's last read as zeros.
+bool map_w2(CUtensorMap* m, const void* base, int K, int H, int N, int tile_features) {
+  const cuuint64_t pitch = (cuuint64_t)K / 2;
+  const cuuint64_t dims[3] = {pitch, (cuuint64_t)H, (cuuint64_t)N}, strides[2] = {pitch, pitch * H};
+  const cuuint32_t box[3] = {128, (cuuint32_t)tile_features, 1};
+  return encode(m, base, 3, dims, strides, box);
+}
+
+// ----------------------------------------------------------------- expert FFN
+// The two GEMMs of one set of experts: activations x (codes, tile-order
+// scales) -> a (codes, tile-order scales) -> y.
+moe_status gemms(const moe_config* c, int H, int I, int N, const uint8_t* x, const uint8_t* x_sf, uint64_t x_rows,
+                 const uint8_t* w13, const uint8_t* w13_sf, const uint8_t* w2, const uint8_t* w2_sf, uint8_t* a,
+                 uint8_t* a_sf, uint64_t a_rows, uint16_t* y, const GemmTile* tiles, const int32_t* num_tiles,
+                 int identity_T, int64_t max_tiles, int* status, cudaStream_t s) {
+  const int sms = api::sm_count();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  const int f13 = moe::mx_tile_features(true, 2 * I, max_tiles, sms);
+  const int f2 = moe::mx_tile_features(false, H, max_tiles, sms);
+  CUtensorMap m_w13, m_w2, m_x, m_xs, m_a, m_as;
+  if (!map_w13(&m_w13, w13, H, I, N, f13) || !map_w2(&m_w2, w2, I, H, N, f2) || !map_rows(&m_x, x, H, x_rows, 128) ||
+      !map_rows(&m_xs, x, H, x_rows, 32) || !map_rows(&m_a, a, I, a_rows, 128) || !map_rows(&m_as, a, I, a_rows, 32))
+    return MOE_ERR_CUDA;
+  moe::MxGemmArgs g{};
+  g.K = H;
+  g.features = 2 * I;
+  g.tile_features = f13;
+  g.tiles = tiles;
+  g.num_tiles = num_tiles;
+  g.identity_T = identity_T;
+  g.a_sf = x_sf;
+  g.b_sf = w13_sf;
+  g.out_codes = a;
+  g.out_sf = a_sf;
+  g.out_ld = I;
+  g.status = status;
+  g.wait_ns = (unsigned long long)c->debug_wait_ns;
+  moe::launch_mx_gemm(true, m_w13, m_x, m_xs, g, max_tiles, sms, s);
+  g.K = I;
+  g.features = H;
+  g.tile_features = f2;
+  g.a_sf = a_sf;
+  g.b_sf = w2_sf;
+  g.out = y;
+  g.out_ld = H;
+  moe::launch_mx_gemm(false, m_w2, m_a, m_as, g, max_tiles, sms, s);
+  return api::last_error();
+}
+
+struct Experts {
+  const uint8_t *w13, *w13_sf, *w2, *w2_sf, *w13s, *w13s_sf, *w2s, *w2s_sf;
+};
+
+moe_status check_experts(const moe_config* c, const Experts& w) {
+  MOE_TRY(api::need(w.w13));
+  MOE_TRY(api::need(w.w13_sf));
+  MOE_TRY(api::need(w.w2));
+  MOE_TRY(api::need(w.w2_sf));
+  if (c->shared_intermediate > 0) {
+    MOE_TRY(api::need(w.w13s));
+    MOE_TRY(api::need(w.w13s_sf));
+    MOE_TRY(api::need(w.w2s));
+    MOE_TRY(api::need(w.w2s_sf));
+  }
+  return MOE_OK;
+}
+
+moe_status ffn_impl(const moe_config* c, int32_t T, const uint8_t* codes, const uint8_t* scales, const Experts& w,
+                    const int32_t* sorted, const int32_t* blocks, const int32_t* num_padded, uint16_t* y_perm,
+                    uint16_t* y_shared, void* ws, cudaStream_t s) {
+  const Layout L = layout_of(c, T);
+  const int H = c->hidden, I = c->intermediate, N = c->num_experts, slots = api::slots(c);
+  const int64_t rows = api::max_rows(c, T), max_tiles = api::max_tiles(c, T, moe::kMxTileRows);
+  int* status = at<int>(ws, L.status);
+  GemmTile* tiles = at<GemmTile>(ws, L.tiles);
+  int32_t* num_tiles = at<int32_t>(ws, L.num_tiles);
+  if (!moe::mx_gemm_smem_ok()) return MOE_ERR_CUDA;
+  const moe::TileListOut list{tiles, num_tiles, moe::kMxTileRows, (int)max_tiles, nullptr};
+  moe::launch_tiles_and_rows(blocks, num_padded, sorted, slots, T, N, c->block_size, rows, &list, nullptr, status, 0,
+                             nullptr, nullptr, H, nullptr, s);
+  uint8_t* x_perm = at<uint8_t>(ws, L.x_perm);
+  uint8_t* x_sf = at<uint8_t>(ws, L.x_sf);
+  moe::launch_mx_gather(codes, scales, sorted, slots, T, H, tiles, num_tiles, 0, max_tiles, x_perm, x_sf, s);
+  const uint64_t perm_rows = (uint64_t)rows + moe::kMxTileRows;
+  MOE_TRY(gemms(c, H, I, N, x_perm, x_sf, perm_rows, w.w13, w.w13_sf, w.w2, w.w2_sf, at<uint8_t>(ws, L.a),
+                at<uint8_t>(ws, L.a_sf), perm_rows, y_perm, tiles, num_tiles, 0, max_tiles, status, s));
+  if (c->shared_intermediate > 0) {
+    const int64_t tiles_t = ((int64_t)T + moe::kMxTileRows - 1) / moe::kMxTileRows;
+    uint8_t* xs_sf = at<uint8_t>(ws, L.x_sh_sf);
+    moe::launch_mx_gather(codes, scales, nullptr, 1, T, H, nullptr, nullptr, T, tiles_t, nullptr, xs_sf, s);
+    MOE_TRY(gemms(c, H, c->shared_intermediate, 1, codes, xs_sf, (uint64_t)T, w.w13s, w.w13s_sf, w.w2s, w.w2s_sf,
+                  at<uint8_t>(ws, L.a_sh), at<uint8_t>(ws, L.a_sh_sf), (uint64_t)T + moe::kMxTileRows, y_shared, nullptr,
+                  nullptr, T, tiles_t, status, s));
+  }
+  return api::last_error();
+}
+
+moe_status check_norm(int32_t T, int32_t H, float eps) {
+  if (T < 0 || H <= 0 || !(eps >= 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+  if (H % kSfBlock || H > kMaxHidden || T > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status check_mx(int64_t rows, int32_t K) {
+  if (rows < 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+  if (K % kSfBlock || rows > ((int64_t)1 << 40) / K) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_check_scoring(const moe_config* cfg, const moe_scoring* scoring) {
+  MOE_TRY(api::check_config(cfg));
+  return check_scoring(cfg, scoring);
+}
+
+moe_status moe_route_scored(const moe_config* cfg, const moe_scoring* scoring, int32_t T, const float* logits,
+                            const float* score_bias, int32_t* topk_idx, float* topk_gate, void* stream) {
+  MOE_TRY(api::check_config(cfg));
+  MOE_TRY(api::check_tokens(cfg, T));
+  MOE_TRY(check_scoring(cfg, scoring));
+  if (T == 0) return MOE_OK;
+  MOE_TRY(api::need(logits));
+  MOE_TRY(api::optional(score_bias));
+  MOE_TRY(api::need(topk_idx));
+  MOE_TRY(api::need(topk_gate));
+  return route_impl(cfg, scoring, T, logits, score_bias, topk_idx, topk_gate, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_add_norm(int32_t T, int32_t H, const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
+                        float eps, uint16_t* residual_out, uint16_t* out, uint8_t* codes, uint8_t* scales,
+                        void* stream) {
+  MOE_TRY(check_norm(T, H, eps));
+  if (T == 0) return MOE_OK;
+  MOE_TRY(api::need(x));
+  MOE_TRY(api::optional(residual));
+  MOE_TRY(api::need(weight));
+  MOE_TRY(api::optional(residual_out));
+  MOE_TRY(api::optional(out));
+  MOE_TRY(api::optional(codes));
+  MOE_TRY(api::optional(scales));
+  if ((codes == nullptr) != (scales == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!out && !codes) return MOE_ERR_INVALID_ARG;
+  const int sms = api::sm_count();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  moe::launch_add_norm(x, residual, weight, eps, T, H, residual_out, out, codes, scales, sms,
+                       static_cast<cudaStream_t>(stream));
+  return api::last_error();
+}
+
+moe_status moe_quantize_mx(int64_t rows, int32_t K, const uint16_t* x, uint8_t* codes, uint8_t* scales,
+                           void* stream) {
+  MOE_TRY(check_mx(rows, K));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(api::need(x));
+  MOE_TRY(api::need(codes));
+  MOE_TRY(api::need(scales));
+  moe::launch_quantize_mx(x, (size_t)rows * K, codes, scales, static_cast<cudaStream_t>(stream));
+  return api::last_error();
+}
+
+moe_status moe_dequantize_mx(int64_t rows, int32_t K, const uint8_t* codes, const uint8_t* scales, uint16_t* out,
+                             void* stream) {
+  MOE_TRY(check_mx(rows, K));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(api::need(codes));
+  MOE_TRY(api::need(scales));
+  MOE_TRY(api::need(out));
+  moe::launch_dequantize_mx(codes, scales, (size_t)rows * K, out, static_cast<cudaStream_t>(stream));
+  return api::last_error();
+}
+
+moe_status moe_quantize_weights_mx(int32_t experts, int32_t K, int32_t F, const uint16_t* w, uint8_t* codes,
+                                   uint8_t* scales, void* stream) {
+  if (experts < 0 || F <= 0) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_mx(experts, K));
+  if (F % 8 || F > (1 << 21) || experts > 65535) return MOE_ERR_UNSUPPORTED;
+  if (experts == 0) return MOE_OK;
+  MOE_TRY(api::need(w));
+  MOE_TRY(api::need(codes));
+  MOE_TRY(api::need(scales));
+  moe::launch_quantize_weights_mx(w, experts, K, F, codes, scales, static_cast<cudaStream_t>(stream));
+  return api::last_error();
+}
+
+moe_status moe_pack_scales_mx(int32_t experts, int32_t rows, int32_t K, int32_t gate_up, const uint8_t* scales,
+                              uint8_t* packed, void* stream) {
+  if (experts < 0 || rows <= 0 || K <= 0 || (gate_up != 0 && gate_up != 1)) return MOE_ERR_INVALID_ARG;
+  if (rows % 128 || K % 128 || rows > (1 << 18) || K > (1 << 17) || experts > 65535) return MOE_ERR_UNSUPPORTED;
+  if (experts == 0) return MOE_OK;
+  MOE_TRY(api::need(scales));
+  MOE_TRY(api::need(packed));
+  moe::launch_pack_scales_mx(scales, experts, rows, K, gate_up != 0, packed, static_cast<cudaStream_t>(stream));
+  return api::last_error();
+}
+
+size_t moe_workspace_bytes_mx(const moe_config* cfg, int32_t max_tokens) {
+  if (api::check_config(cfg) != MOE_OK || api::check_tokens(cfg, max_tokens) != MOE_OK) return 0;
+  return layout_of(cfg, max_tokens).total;
+}
+
+moe_status moe_expert_ffn_mx(const moe_config* cfg, int32_t T, const uint8_t* x_codes, const uint8_t* x_scales,
+                             const uint8_t* w13, const uint8_t* w13_scales, const uint8_t* w2,
+                             const uint8_t* w2_scales, const uint8_t* w13_shared, const uint8_t* w13_shared_scales,
+                             const uint8_t* w2_shared, const uint8_t* w2_shared_scales,
+                             const int32_t* sorted_route_ids, const int32_t* block_expert, const int32_t* num_padded,
+                             uint16_t* y_perm, uint16_t* y_shared, void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(api::check_config(cfg));
+  MOE_TRY(api::check_tokens(cfg, T));
+  if (T == 0) return MOE_OK;
+  const Experts w{w13, w13_scales, w2, w2_scales, w13_shared, w13_shared_scales, w2_shared, w2_shared_scales};
+  MOE_TRY(api::need(x_codes));
+  MOE_TRY(api::need(x_scales));
+  MOE_TRY(check_experts(cfg, w));
+  MOE_TRY(api::need(sorted_route_ids));
+  MOE_TRY(api::need(block_expert));
+  MOE_TRY(api::need(num_padded));
+  MOE_TRY(api::need(y_perm));
+  if (cfg->shared_intermediate > 0) MOE_TRY(api::need(y_shared));
+  MOE_TRY(check_ws(cfg, T, ws, ws_bytes));
+  return ffn_impl(cfg, T, x_codes, x_scales, w, sorted_route_ids, block_expert, num_padded, y_perm, y_shared, ws,
+                  static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_forward_mx(const moe_config* cfg, const moe_scoring* scoring, int32_t T, const uint16_t* x,
+                          const uint16_t* residual, const uint16_t* norm_weight, float eps, const uint16_t* w_gate,
+                          const float* router_bias, const float* score_bias, const uint8_t* w13,
+                          const uint8_t* w13_scales, const uint8_t* w2, const uint8_t* w2_scales,
+                          const uint8_t* w13_shared, const uint8_t* w13_shared_scales, const uint8_t* w2_shared,
+                          const uint8_t* w2_shared_scales, uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(api::check_config(cfg));
+  MOE_TRY(api::check_tokens(cfg, T));
+  MOE_TRY(check_scoring(cfg, scoring));
+  MOE_TRY(check_norm(T, cfg->hidden, eps));
+  if (cfg->overflow_policy == MOE_OVERFLOW_REROUTE && cfg->capacity_factor > 0.0) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  const Experts w{w13, w13_scales, w2, w2_scales, w13_shared, w13_shared_scales, w2_shared, w2_shared_scales};
+  MOE_TRY(api::need(x));
+  MOE_TRY(api::optional(residual));
+  MOE_TRY(api::need(norm_weight));
+  MOE_TRY(api::need(w_gate));
+  MOE_TRY(api::optional(router_bias));
+  MOE_TRY(api::optional(score_bias));
+  MOE_TRY(check_experts(cfg, w));
+  MOE_TRY(api::need(out));
+  MOE_TRY(check_ws(cfg, T, ws, ws_bytes));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int sms = api::sm_count();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  const Layout L = layout_of(cfg, T);
+  const int H = cfg->hidden, N = cfg->num_experts;
+  // without a residual the layer's input is its residual stream
+  uint16_t* sum = residual ? at<uint16_t>(ws, L.residual) : nullptr;
+  uint16_t* norm = at<uint16_t>(ws, L.norm);
+  uint8_t* codes = at<uint8_t>(ws, L.codes);
+  uint8_t* scales = at<uint8_t>(ws, L.scales);
+  float* logits = at<float>(ws, L.logits);
+  int32_t* idx = at<int32_t>(ws, L.topk);
+  float* gates = at<float>(ws, L.gates);
+  uint8_t* kept = at<uint8_t>(ws, L.kept);
+  int32_t* pos = at<int32_t>(ws, L.pos);
+  int32_t* sorted = at<int32_t>(ws, L.sorted);
+  int32_t* blocks = at<int32_t>(ws, L.blocks);
+  int32_t* num_padded = at<int32_t>(ws, L.num_padded);
+  uint16_t* y = at<uint16_t>(ws, L.y);
+  uint16_t* y_sh = cfg->shared_intermediate ? at<uint16_t>(ws, L.y_sh) : nullptr;
+  moe::launch_add_norm(x, residual, norm_weight, eps, T, H, sum, norm, codes, scales, sms, s);
+  moe::launch_router_chunked(norm, w_gate, router_bias, at<float>(ws, L.rpart), logits, nullptr, nullptr, T, H, N,
+                             cfg->top_k, s);
+  MOE_TRY(route_impl(cfg, scoring, T, logits, score_bias, idx, gates, s));
+  moe::launch_dispatch(idx, T, N, cfg->top_k, cfg->block_size, api::capacity(cfg, T), kept, pos, sorted, blocks,
+                       num_padded, at<int32_t>(ws, L.counts), at<int32_t>(ws, L.dropped), at<int32_t>(ws, L.rank),
+                       at<int32_t>(ws, L.tile_count), at<int32_t>(ws, L.seg_off), at<int>(ws, L.status), s);
+  MOE_TRY(ffn_impl(cfg, T, codes, scales, w, sorted, blocks, num_padded, y, y_sh, ws, s));
+  moe::launch_combine(sum ? sum : x, gates, kept, pos, y, y_sh, out, T, H, cfg->top_k, api::max_rows(cfg, T), s);
+  return api::last_error();
+}
+
+}  // extern "C"
