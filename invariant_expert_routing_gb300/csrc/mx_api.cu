@@ -37,7 +37,9 @@ Layout layout_of(const moe_config* c, int32_t T) {
   const size_t N = c->num_experts, H = c->hidden, I = c->intermediate, Is = c->shared_intermediate;
   const size_t R = (size_t)T * api::slots(c), rows = (size_t)api::max_rows(c, T);
   const int64_t tiles = api::max_tiles(c, T, moe::kMxTileRows);
-  const int64_t tiles_t = ((int64_t)T + moe::kMxTileRows - 1) / moe::kMxTileRows;
+  // scales of 128-row tiles, an even number of them for every tile of 256 rows
+  const int64_t sf_tiles = 2 * api::max_tiles(c, T, 2 * moe::kMxTileRows);
+  const int64_t tiles_t = 2 * (((int64_t)T + 2 * moe::kMxTileRows - 1) / (2 * moe::kMxTileRows));
   Layout L{};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -50,9 +52,9 @@ Layout layout_of(const moe_config* c, int32_t T) {
   L.num_tiles = take(2 * sizeof(int32_t));
   // the activations keep one tile of rows of slack so that every tile load stays inside them
   L.x_perm = take((rows + moe::kMxTileRows) * H / 2);
-  L.x_sf = take(sf_bytes(tiles, (int)H));
+  L.x_sf = take(sf_bytes(std::max(tiles, sf_tiles), (int)H));
   L.a = take((rows + moe::kMxTileRows) * I / 2);
-  L.a_sf = take(sf_bytes(tiles, (int)I));
+  L.a_sf = take(sf_bytes(std::max(tiles, sf_tiles), (int)I));
   L.x_sh_sf = take(Is ? sf_bytes(tiles_t, (int)H) : 0);
   L.a_sh = take(Is ? ((size_t)T + moe::kMxTileRows) * Is / 2 : 0);
   L.a_sh_sf = take(Is ? sf_bytes(tiles_t, (int)Is) : 0);
@@ -118,40 +120,57 @@ moe_status route_impl(const moe_config* c, const moe_scoring* s, int32_t T, cons
 }
 
 // ----------------------------------------------------------------- tensor maps
-// Byte tensors with 128-byte swizzle, 128 bytes (256 elements) of K a box.
-bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-            const cuuint32_t* box) {
+bool encode(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base, int rank,
+            const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
   auto fn = api::tensor_map_encode();
   if (!fn) return false;
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return fn(m, type, rank, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Bytes with 128-byte swizzle, 128 of them (256 elements of K) a box.
+bool encode_codes(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                  const cuuint32_t* box) {
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, base, rank, dims, strides, box);
+}
+
+// Scale chunks as rows of 512 bytes, two a box.
+bool map_scales(CUtensorMap* m, const void* base, uint64_t chunks) {
+  const cuuint64_t dims[2] = {128, chunks}, strides[1] = {512};
+  const cuuint32_t box[2] = {128, 2};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, base, 2, dims, strides, box);
+}
+
+// bf16 output rows, 32 rows x 64 columns a box.
+bool map_out(CUtensorMap* m, const void* base, uint64_t H, uint64_t rows) {
+  const cuuint64_t dims[2] = {H, rows}, strides[1] = {2 * H};
+  const cuuint32_t box[2] = {64, 32};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, base, 2, dims, strides, box);
 }
 
 bool map_rows(CUtensorMap* m, const void* base, int K, uint64_t rows, uint32_t box_rows) {
   const cuuint64_t pitch = (cuuint64_t)K / 2;
   const cuuint64_t dims[2] = {pitch, rows}, strides[1] = {pitch};
   const cuuint32_t box[2] = {128, box_rows};
-  return encode(m, base, 2, dims, strides, box);
+  return encode_codes(m, base, 2, dims, strides, box);
 }
 
 // W13 [N, 2I, K/2]: (byte, row of a 32-feature block, gate/up, block, expert),
 // so that one box holds 32 gate and the same 32 up rows in turns.
-bool map_w13(CUtensorMap* m, const void* base, int K, int I, int N, int tile_features) {
+bool map_w13(CUtensorMap* m, const void* base, int K, int I, int N, int box_rows) {
   const cuuint64_t pitch = (cuuint64_t)K / 2;
   const cuuint64_t dims[5] = {pitch, 32, 2, (cuuint64_t)I / 32, (cuuint64_t)N};
   const cuuint64_t strides[4] = {pitch, pitch * I, pitch * 32, pitch * 2 * I};
-  const cuuint32_t box[5] = {128, 32, 2, (cuuint32_t)tile_features / 64, 1};
-  return encode(m, base, 5, dims, strides, box);
+  const cuuint32_t box[5] = {128, 32, 2, (cuuint32_t)box_rows / 64, 1};
+  return encode_codes(m, base, 5, dims, strides, box);
 }
 
 // W2 [N, H, I/2]: (byte, row, expert); rows past an expert's last read as zeros.
-bool map_w2(CUtensorMap* m, const void* base, int K, int H, int N, int tile_features) {
+bool map_w2(CUtensorMap* m, const void* base, int K, int H, int N, int box_rows) {
   const cuuint64_t pitch = (cuuint64_t)K / 2;
   const cuuint64_t dims[3] = {pitch, (cuuint64_t)H, (cuuint64_t)N}, strides[2] = {pitch, pitch * H};
-  const cuuint32_t box[3] = {128, (cuuint32_t)tile_features, 1};
-  return encode(m, base, 3, dims, strides, box);
+  const cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1};
+  return encode_codes(m, base, 3, dims, strides, box);
 }
 
 // ----------------------------------------------------------------- expert FFN
@@ -159,19 +178,30 @@ bool map_w2(CUtensorMap* m, const void* base, int K, int H, int N, int tile_feat
 // scales) -> a (codes, tile-order scales) -> y.
 moe_status gemms(const moe_config* c, int H, int I, int N, const uint8_t* x, const uint8_t* x_sf, uint64_t x_rows,
                  const uint8_t* w13, const uint8_t* w13_sf, const uint8_t* w2, const uint8_t* w2_sf, uint8_t* a,
-                 uint8_t* a_sf, uint64_t a_rows, uint16_t* y, const GemmTile* tiles, const int32_t* num_tiles,
-                 int identity_T, int64_t max_tiles, int* status, cudaStream_t s) {
+                 uint8_t* a_sf, uint64_t a_rows, uint16_t* y, uint64_t y_rows, const GemmTile* tiles,
+                 const int32_t* num_tiles, int tile_rows, int identity_T, int64_t max_tiles, int* status,
+                 cudaStream_t s) {
   const int sms = api::sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
-  const int f13 = moe::mx_tile_features(true, 2 * I, max_tiles, sms);
-  const int f2 = moe::mx_tile_features(false, H, max_tiles, sms);
-  CUtensorMap m_w13, m_w2, m_x, m_xs, m_a, m_as;
-  if (!map_w13(&m_w13, w13, H, I, N, f13) || !map_w2(&m_w2, w2, I, H, N, f2) || !map_rows(&m_x, x, H, x_rows, 128) ||
-      !map_rows(&m_xs, x, H, x_rows, 32) || !map_rows(&m_a, a, I, a_rows, 128) || !map_rows(&m_as, a, I, a_rows, 32))
+  const bool pair = tile_rows != moe::kMxTileRows;
+  const int f13 = moe::mx_tile_features(tile_rows, 2 * I, max_tiles, sms);
+  const int f2 = moe::mx_tile_features(tile_rows, H, max_tiles, sms);
+  const uint64_t sf_tiles = (uint64_t)max_tiles * (tile_rows / moe::kMxTileRows);
+  moe::MxMaps m13, m2;
+  // a CTA of a pair loads half of the weight rows of an item
+  if (!map_w13(&m13.w, w13, H, I, N, pair ? f13 / 2 : f13) || !map_rows(&m13.x, x, H, x_rows, 128) ||
+      !map_rows(&m13.x_small, x, H, x_rows, 32) || !map_w2(&m2.w, w2, I, H, N, pair ? f2 / 2 : f2) ||
+      !map_rows(&m2.x, a, I, a_rows, 128) || !map_rows(&m2.x_small, a, I, a_rows, 32))
     return MOE_ERR_CUDA;
+  if (pair && (!map_scales(&m13.sfa, x_sf, sf_tiles * (H / 128)) || !map_scales(&m2.sfa, a_sf, sf_tiles * (I / 128)) ||
+               !map_scales(&m13.sfb, w13_sf, (uint64_t)N * (2 * I / 128) * (H / 128)) ||
+               !map_scales(&m2.sfb, w2_sf, (uint64_t)N * (H / 128) * (I / 128)) || !map_out(&m2.y, y, H, y_rows)))
+    return MOE_ERR_CUDA;
+  if (pair) m13.y = m2.y;
   moe::MxGemmArgs g{};
   g.K = H;
   g.features = 2 * I;
+  g.tile_rows = tile_rows;
   g.tile_features = f13;
   g.tiles = tiles;
   g.num_tiles = num_tiles;
@@ -183,7 +213,7 @@ moe_status gemms(const moe_config* c, int H, int I, int N, const uint8_t* x, con
   g.out_ld = I;
   g.status = status;
   g.wait_ns = (unsigned long long)c->debug_wait_ns;
-  moe::launch_mx_gemm(true, m_w13, m_x, m_xs, g, max_tiles, sms, s);
+  moe::launch_mx_gemm(true, m13, g, max_tiles, sms, s);
   g.K = I;
   g.features = H;
   g.tile_features = f2;
@@ -191,7 +221,7 @@ moe_status gemms(const moe_config* c, int H, int I, int N, const uint8_t* x, con
   g.b_sf = w2_sf;
   g.out = y;
   g.out_ld = H;
-  moe::launch_mx_gemm(false, m_w2, m_a, m_as, g, max_tiles, sms, s);
+  moe::launch_mx_gemm(false, m2, g, max_tiles, sms, s);
   return api::last_error();
 }
 
@@ -218,27 +248,32 @@ moe_status ffn_impl(const moe_config* c, int32_t T, const uint8_t* codes, const 
                     uint16_t* y_shared, void* ws, cudaStream_t s) {
   const Layout L = layout_of(c, T);
   const int H = c->hidden, I = c->intermediate, N = c->num_experts, slots = api::slots(c);
-  const int64_t rows = api::max_rows(c, T), max_tiles = api::max_tiles(c, T, moe::kMxTileRows);
+  const int64_t rows = api::max_rows(c, T);
+  const int tile_rows = moe::mx_tile_rows((int64_t)T * slots, N);
+  const int64_t max_tiles = api::max_tiles(c, T, tile_rows);
   int* status = at<int>(ws, L.status);
   GemmTile* tiles = at<GemmTile>(ws, L.tiles);
   int32_t* num_tiles = at<int32_t>(ws, L.num_tiles);
   if (!moe::mx_gemm_smem_ok()) return MOE_ERR_CUDA;
-  const moe::TileListOut list{tiles, num_tiles, moe::kMxTileRows, (int)max_tiles, nullptr};
+  const moe::TileListOut list{tiles, num_tiles, tile_rows, (int)max_tiles, nullptr};
   moe::launch_tiles_and_rows(blocks, num_padded, sorted, slots, T, N, c->block_size, rows, &list, nullptr, status, 0,
                              nullptr, nullptr, H, nullptr, s);
   uint8_t* x_perm = at<uint8_t>(ws, L.x_perm);
   uint8_t* x_sf = at<uint8_t>(ws, L.x_sf);
-  moe::launch_mx_gather(codes, scales, sorted, slots, T, H, tiles, num_tiles, 0, max_tiles, x_perm, x_sf, s);
+  moe::launch_mx_gather(codes, scales, sorted, slots, T, H, tiles, num_tiles, tile_rows, 0, max_tiles, x_perm, x_sf,
+                        s);
   const uint64_t perm_rows = (uint64_t)rows + moe::kMxTileRows;
   MOE_TRY(gemms(c, H, I, N, x_perm, x_sf, perm_rows, w.w13, w.w13_sf, w.w2, w.w2_sf, at<uint8_t>(ws, L.a),
-                at<uint8_t>(ws, L.a_sf), perm_rows, y_perm, tiles, num_tiles, 0, max_tiles, status, s));
+                at<uint8_t>(ws, L.a_sf), perm_rows, y_perm, (uint64_t)rows, tiles, num_tiles, tile_rows, 0, max_tiles,
+                status, s));
   if (c->shared_intermediate > 0) {
-    const int64_t tiles_t = ((int64_t)T + moe::kMxTileRows - 1) / moe::kMxTileRows;
+    const int rows_t = moe::mx_tile_rows(T, 1);
+    const int64_t tiles_t = ((int64_t)T + rows_t - 1) / rows_t;
     uint8_t* xs_sf = at<uint8_t>(ws, L.x_sh_sf);
-    moe::launch_mx_gather(codes, scales, nullptr, 1, T, H, nullptr, nullptr, T, tiles_t, nullptr, xs_sf, s);
+    moe::launch_mx_gather(codes, scales, nullptr, 1, T, H, nullptr, nullptr, rows_t, T, tiles_t, nullptr, xs_sf, s);
     MOE_TRY(gemms(c, H, c->shared_intermediate, 1, codes, xs_sf, (uint64_t)T, w.w13s, w.w13s_sf, w.w2s, w.w2s_sf,
-                  at<uint8_t>(ws, L.a_sh), at<uint8_t>(ws, L.a_sh_sf), (uint64_t)T + moe::kMxTileRows, y_shared, nullptr,
-                  nullptr, T, tiles_t, status, s));
+                  at<uint8_t>(ws, L.a_sh), at<uint8_t>(ws, L.a_sh_sf), (uint64_t)T + moe::kMxTileRows, y_shared, (uint64_t)T,
+                  nullptr, nullptr, rows_t, T, tiles_t, status, s));
   }
   return api::last_error();
 }

@@ -40,6 +40,7 @@ constexpr int kThreads = (2 + kEpiWarps) * 32;
 constexpr int kStageK = 256;                         // elements of K per stage: one 128-byte row
 constexpr int kSmallRows = 32;                       // token box of a tile with at most 32 routed rows
 constexpr uint32_t kSmemBudget = 226 * 1024;
+constexpr uint32_t kSfUnits = kSfChunkBytes >> 4;    // a scale chunk in descriptor units
 
 template <int BN>
 struct Cfg {
@@ -70,6 +71,7 @@ struct Item {
 // contiguous; inside an expert they run in groups of feature tiles x all of
 // the expert's token tiles, a group sized so that one wave of CTAs shares its
 // weight and token tiles through L2.
+template <int kRows = kMxTileRows>
 __device__ __forceinline__ Item item_of(const MxGemmArgs& a, int item, int num_tiles, int nf) {
   int first = 0, count = num_tiles;
   if (!a.identity_T) {
@@ -87,8 +89,8 @@ __device__ __forceinline__ Item item_of(const MxGemmArgs& a, int item, int num_t
   w.tile = first + lin / gsz;
   if (a.identity_T) {
     w.expert = 0;
-    w.row0 = w.tile * kMxTileRows;
-    w.valid = min(kMxTileRows, a.identity_T - w.row0);
+    w.row0 = w.tile * kRows;
+    w.valid = min(kRows, a.identity_T - w.row0);
   } else {
     const GemmTile g = a.tiles[w.tile];
     w.expert = g.expert;
@@ -98,21 +100,22 @@ __device__ __forceinline__ Item item_of(const MxGemmArgs& a, int item, int num_t
   return w;
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2,
-                                            uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-      "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
-      : "memory");
+__device__ __forceinline__ Item uniform_item(Item w) {
+  w.f = uniform(w.f);
+  w.tile = uniform(w.tile);
+  w.expert = uniform(w.expert);
+  w.row0 = uniform(w.row0);
+  w.valid = uniform(w.valid);
+  return w;
 }
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, int c3,
-                                            int c4, uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
-      "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar), "l"(policy)
-      : "memory");
+
+// Waits of a converged warp (every lane polls): false as soon as one lane gave up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit));
+}
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort,
+                                                  uint64_t limit) {
+  return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort, limit));
 }
 
 // a = silu(g) * u of 32 neighbouring features of one token, quantised:
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tempty0 = tfull0 + 16;
   const uint32_t drain = tempty0 + 16;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const int kchunks = args.K / kSfChunkK;
   const int ksteps = (args.K + kStageK - 1) / kStageK;
   const int nf = (args.features + BN - 1) / BN;
@@ -203,42 +206,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem_base;
+  const uint32_t tmem = (uint32_t)uniform((int)s_tmem_base);
   pdl_wait();
   pdl_trigger();
   const int num_tiles =
-      args.identity_T ? (args.identity_T + kMxTileRows - 1) / kMxTileRows : *args.num_tiles;
+      uniform(args.identity_T ? (args.identity_T + kMxTileRows - 1) / kMxTileRows : *args.num_tiles);
   const int total = num_tiles * nf;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      const uint64_t pol_w = policy_evict_normal();
-      const uint64_t pol_x = policy_evict_last();
-      int stage = 0;
-      uint32_t phase = 0;
-      int armed = 0;
-      bool ok = true;
-      for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-        const Item w = item_of(args, item, num_tiles, nf);
-        const bool small = w.valid <= kSmallRows;
-        const uint32_t a_tx = (small ? kSmallRows : kMxTileRows) * 128u;
-        // scale tiles of B that exist (the last item of an odd number of 128-row tiles has one)
-        const int sft0 = w.f * BN / kSfRows;
-        const int sft = min(C::kSfbTiles, args.features / kSfRows - sft0);
-        const uint8_t* sfa = args.a_sf + (size_t)w.tile * kchunks * kSfChunkBytes;
-        const uint8_t* sfb =
-            args.b_sf + ((size_t)w.expert * (args.features / kSfRows) + sft0) * kchunks * kSfChunkBytes;
-        for (int ks = 0; ks < ksteps; ++ks) {
-          if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, &s_abort, wlim)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sA = smem_u32(smem + stage * C::kStageBytes);
-          const uint32_t sB = sA + C::kABytes;
-          const uint32_t sFa = sB + C::kBBytes, sFb = sFa + C::kSfaBytes;
-          const uint32_t fb = full0 + 8 * stage;
-          const uint32_t sf_bytes = (uint32_t)min(2, kchunks - 2 * ks) * kSfChunkBytes;
+    const uint64_t pol_w = policy_evict_normal();
+    const uint64_t pol_x = policy_evict_last();
+    const uint32_t s0 = smem_u32(smem);
+    int stage = 0;
+    uint32_t phase = 0;
+    int armed = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+      const Item w = uniform_item(item_of(args, item, num_tiles, nf));
+      const bool small = w.valid <= kSmallRows;
+      const uint32_t a_tx = (small ? kSmallRows : kMxTileRows) * 128u;
+      // scale tiles of B that exist (the last item of an odd number of 128-row tiles has one)
+      const int sft0 = w.f * BN / kSfRows;
+      const int sft = min(C::kSfbTiles, args.features / kSfRows - sft0);
+      const uint8_t* sfa = args.a_sf + (size_t)w.tile * kchunks * kSfChunkBytes;
+      const uint8_t* sfb = args.b_sf + ((size_t)w.expert * (args.features / kSfRows) + sft0) * kchunks * kSfChunkBytes;
+      for (int ks = 0; ks < ksteps; ++ks) {
+        if (!warp_wait(empty0 + 8 * stage, phase ^ 1u, &s_abort, wlim)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sA = s0 + stage * C::kStageBytes;
+        const uint32_t sB = sA + C::kABytes;
+        const uint32_t sFa = sB + C::kBBytes, sFb = sFa + C::kSfaBytes;
+        const uint32_t fb = full0 + 8 * stage;
+        const uint32_t sf_bytes = (uint32_t)min(2, kchunks - 2 * ks) * kSfChunkBytes;
+        if (elect_one()) {
           mbar_arrive_expect_tx(fb, a_tx + C::kBBytes + sf_bytes * (1 + sft));
           if (kW13)
             tma_load_5d(sB, &w_map, ks * 128, 0, 0, w.f * (BN / 64), w.expert, fb, pol_w);
@@ -246,99 +249,116 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(sB, &w_map, ks * 128, w.f * BN, w.expert, fb, pol_w);
           tma_load_2d(sA, small ? &x_map_small : &x_map, ks * 128, w.row0, fb, pol_x);
           bulk_load(sFa, sfa + (size_t)(2 * ks) * kSfChunkBytes, sf_bytes, fb);
-          for (int t = 0; t < sft; ++t)
-            bulk_load(sFb + t * 2 * kSfChunkBytes, sfb + ((size_t)t * kchunks + 2 * ks) * kSfChunkBytes, sf_bytes, fb);
-          armed = min(armed + 1, C::kStages);
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          bulk_load(sFb, sfb + (size_t)(2 * ks) * kSfChunkBytes, sf_bytes, fb);
+          if (C::kSfbTiles > 1 && sft > 1)
+            bulk_load(sFb + 2 * kSfChunkBytes, sfb + ((size_t)kchunks + 2 * ks) * kSfChunkBytes, sf_bytes, fb);
+        }
+        __syncwarp();
+        armed = min(armed + 1, C::kStages);
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok) {
-        s_abort = 1;
-        atomicOr(args.status, kDevErrTimeout);
-      }
-      if (s_abort) {
-        // let the copies already issued land before exit
-        volatile int no_abort = 0;
-        int s = stage;
-        uint32_t ph = phase;
-        for (int i = 0; i < armed; ++i) {
-          if (--s < 0) {
-            s = C::kStages - 1;
-            ph ^= 1u;
-          }
-          mbar_wait(full0 + 8 * s, ph, &no_abort);
+    }
+    if (!ok) {
+      s_abort = 1;
+      if (lane == 0) atomicOr(args.status, kDevErrTimeout);
+    }
+    if (s_abort && lane == 0) {
+      // let the copies already issued land before exit
+      volatile int no_abort = 0;
+      int s = stage;
+      uint32_t ph = phase;
+      for (int i = 0; i < armed; ++i) {
+        if (--s < 0) {
+          s = C::kStages - 1;
+          ph ^= 1u;
         }
+        mbar_wait(full0 + 8 * s, ph, &no_abort);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int acc = 0;
-      uint32_t acc_phase = 0;
-      bool ok = true;
-      for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-        if (!mbar_wait(tempty0 + 8 * acc, acc_phase ^ 1u, &s_abort, wlim)) {
+    int stage = 0;
+    uint32_t phase = 0;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    // descriptors of stage 0, built once; soff is the stage's offset in their 16-byte units
+    const uint32_t s0 = smem_u32(smem);
+    const uint64_t adesc0 = sdesc_sw128(s0, 16, 1024), bdesc0 = sdesc_sw128(s0 + C::kABytes, 16, 1024);
+    const uint64_t fadesc0 = sdesc_scales(s0 + C::kABytes + C::kBBytes);
+    const uint64_t fbdesc0 = sdesc_scales(s0 + C::kABytes + C::kBBytes + C::kSfaBytes);
+    constexpr uint32_t kI0 = idesc_mxf4(kMxTileRows, BN, 0), kI1 = idesc_mxf4(kMxTileRows, BN, 1);
+    uint32_t soff = 0;
+    for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+      // an item narrower than a scale tile takes its columns of it
+      const int f = (BN < kSfRows) ? uniform(item_of(args, item, num_tiles, nf).f) : 0;
+      const uint32_t sfb_skip = (BN < kSfRows) ? (uint32_t)(f * BN % kSfRows) / 32u : 0u;
+      if (!warp_wait(tempty0 + 8 * acc, acc_phase ^ 1u, &s_abort, wlim)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d0 = tmem + acc * BN;
+      for (int ks = 0; ks < ksteps; ++ks) {
+        if (!warp_wait(full0 + 8 * stage, phase, &s_abort, wlim)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        // an item narrower than a scale tile takes its columns of it
-        const int f = (BN < kSfRows) ? item_of(args, item, num_tiles, nf).f : 0;
-        const uint32_t sfb_skip = (BN < kSfRows) ? (uint32_t)(f * BN % kSfRows) / 32u : 0u;
-        const uint32_t d0 = tmem + acc * BN;
-        for (int ks = 0; ks < ksteps; ++ks) {
-          if (!mbar_wait(full0 + 8 * stage, phase, &s_abort, wlim)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sA = smem_u32(smem + stage * C::kStageBytes);
-          const uint32_t sB = sA + C::kABytes;
-          const uint32_t sFa = sB + C::kBBytes, sFb = sFa + C::kSfaBytes;
-          const uint32_t ta = tmem + C::kSfCol0 + stage * C::kSfCols, tb = ta + 8;
-          const int chunks = min(2, kchunks - 2 * ks);
-          // scales: chunk c of A in columns ta + 4c, of B's tile t in tb + (c kSfbTiles + t) 4
-          for (int c = 0; c < chunks; ++c) {
-            cp_scales(ta + 4 * c, sdesc_scales(sFa + c * kSfChunkBytes));
+        const uint32_t ta = tmem + C::kSfCol0 + stage * C::kSfCols, tb = ta + 8;
+        const uint64_t ad = adesc0 + soff, bd = bdesc0 + soff, fa = fadesc0 + soff, fbd = fbdesc0 + soff;
+        // chunk c of 128 elements: scales (A's in columns ta + 4c, those of
+        // B's tile t in tb + (c kSfbTiles + t) 4), then two MMAs
+        auto scales = [&](int c) {
+          cp_scales(ta + 4 * c, fa + c * kSfUnits);
 #pragma unroll
-            for (int t = 0; t < C::kSfbTiles; ++t)
-              cp_scales(tb + 4 * (c * C::kSfbTiles + t), sdesc_scales(sFb + (2 * t + c) * kSfChunkBytes));
-          }
-          const uint64_t ad = sdesc_sw128(sA, 16, 1024), bd = sdesc_sw128(sB, 16, 1024);
-          for (int c = 0; c < chunks; ++c) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-              mma_mxf4(d0, ad + (2 * c + half) * 2, bd + (2 * c + half) * 2, idesc_mxf4(kMxTileRows, BN, half),
-                       ta + 4 * c, tb + 4 * c * C::kSfbTiles + sfb_skip, (ks | c | half) != 0 ? 1u : 0u);
+          for (int t = 0; t < C::kSfbTiles; ++t)
+            cp_scales(tb + 4 * (c * C::kSfbTiles + t), fbd + (2 * t + c) * kSfUnits);
+        };
+        auto mmas = [&](int c, uint32_t accumulate) {
+          const uint32_t sb = tb + 4 * c * C::kSfbTiles + sfb_skip;
+          mma_mxf4(d0, ad + 4 * c, bd + 4 * c, kI0, ta + 4 * c, sb, accumulate);
+          mma_mxf4(d0, ad + 4 * c + 2, bd + 4 * c + 2, kI1, ta + 4 * c, sb, 1u);
+        };
+        if (elect_one()) {
+          scales(0);
+          if (2 * ks + 1 < kchunks) {
+            scales(1);
+            mmas(0, ks != 0 ? 1u : 0u);
+            mmas(1, 1u);
+          } else {
+            mmas(0, ks != 0 ? 1u : 0u);
           }
           mma_commit(empty0 + 8 * stage);
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (ks == ksteps - 1) mma_commit(tfull0 + 8 * acc);
         }
-        if (!ok) break;
-        mma_commit(tfull0 + 8 * acc);
-        if (++acc == C::kNumAcc) {
-          acc = 0;
-          acc_phase ^= 1u;
+        __syncwarp();
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+          soff = 0;
+        } else {
+          soff += C::kStageBytes >> 4;
         }
       }
-      if (!ok) {
-        s_abort = 1;
-        atomicOr(args.status, kDevErrTimeout);
+      if (++acc == C::kNumAcc) {
+        acc = 0;
+        acc_phase ^= 1u;
       }
-      // all issued MMAs must be complete before TMEM is released
-      mma_commit(drain);
-      volatile int no_abort = 0;
-      mbar_wait(drain, 0, &no_abort);
     }
+    if (!ok) {
+      s_abort = 1;
+      if (lane == 0) atomicOr(args.status, kDevErrTimeout);
+    }
+    // all issued MMAs must be complete before TMEM is released
+    if (elect_one()) mma_commit(drain);
+    __syncwarp();
+    volatile int no_abort = 0;
+    mbar_wait(drain, 0, &no_abort);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
@@ -399,9 +419,380 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
+// ------------------------------------------------------------------ CTA pairs
+// The same GEMMs on pairs of CTAs (a cluster of two on two SMs, one
+// cta_group::2 MMA of 256 token rows x 256 weight rows): each CTA loads its
+// own 128 token rows and half of the weight rows, which halves the operand
+// bytes an SM reads per MMA (8 KB against 12 KB per 64 cycles, where shared
+// memory gives 128 bytes a cycle), and holds the result of its 128 rows.
+//
+// TMEM (512 columns): the stages' scales (24 columns each) and two accumulators
+// of 256 columns that share what is missing, 120 of them.  The epilogue reads
+// the shared columns first; from then on the next tile's MMAs run beside the
+// rest of it.
+//
+// W2 rows leave through shared memory as 32-row x 64-column tiled stores (a
+// lane's direct 16-byte stores touch one line per row); a lane quarter with
+// padding rows stores directly, so that padding is never written.
+constexpr int kPairRowsMx = 2 * kMxTileRows;
+constexpr int kPairN = 256;
+
+template <bool kW13>
+struct PairCfgMx {
+  static constexpr uint32_t kABytes = kMxTileRows * 128;
+  static constexpr uint32_t kBBytes = (kPairN / 2) * 128;
+  static constexpr uint32_t kSfaBytes = 2 * kSfChunkBytes;
+  static constexpr uint32_t kSfbBytes = 2 * 2 * kSfChunkBytes;
+  static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
+  static constexpr uint32_t kOutBytes = kW13 ? 0 : kEpiWarps * 32 * 128;
+  static constexpr uint32_t kBarBytes = 512;
+  static constexpr int kStages = 5;
+  static constexpr uint32_t kSmemBytes = kStages * kStageBytes + kOutBytes + kBarBytes + 1024;
+  static constexpr uint32_t kSfCols = 24;
+  static constexpr uint32_t kSfCol0 = 512 - kStages * kSfCols;
+  static_assert(kSmemBytes <= kSmemBudget, "stages fit");
+  static constexpr uint32_t kAcc1 = kSfCol0 - kPairN;   // first column of the second accumulator
+  static_assert(kStageBytes % 1024 == 0, "stages stay aligned to the swizzle atom");
+  static_assert(kPairN - kAcc1 <= 128, "the shared columns lie in the blocks that the epilogue reads first");
+};
+
+template <bool kW13>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
+                        const __grid_constant__ CUtensorMap sfa_map, const __grid_constant__ CUtensorMap sfb_map,
+                        const __grid_constant__ CUtensorMap y_map, const MxGemmArgs args) {
+  using C = PairCfgMx<kW13>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem_base;
+  __shared__ volatile int s_abort;
+
+  const uint32_t rank = cluster_ctarank();   // 0: issues the MMAs
+  const bool lead = rank == 0;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_out = smem + C::kStages * C::kStageBytes;
+  const uint32_t full0 = smem_u32(s_out + C::kOutBytes);
+  const uint32_t empty0 = full0 + 8 * C::kStages;
+  const uint32_t tfull0 = empty0 + 8 * C::kStages;
+  const uint32_t tshare = tfull0 + 16;   // shared accumulator columns read
+  const uint32_t drain = tshare + 8;
+
+  const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  const int kchunks = args.K / kSfChunkK;
+  const int ksteps = (args.K + kStageK - 1) / kStageK;
+  const int nf = (args.features + kPairN - 1) / kPairN;
+  const int pair0 = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
+  const uint64_t wlim = args.wait_ns ? args.wait_ns : kWaitLimitNs;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) mbar_init(tfull0 + 8 * b, 1);
+    mbar_init(tshare, 2 * kEpiWarps);
+    mbar_init(drain, 1);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&s_tmem_base), 512);
+    tmem_relinquish_pair();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&w_map);
+    prefetch_tmap(&x_map);
+    prefetch_tmap(&sfa_map);
+    prefetch_tmap(&sfb_map);
+    if (!kW13) prefetch_tmap(&y_map);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers exist before either signals the other
+  tc_fence_after();
+  const uint32_t tmem = (uint32_t)uniform((int)s_tmem_base);
+  pdl_wait();
+  pdl_trigger();
+  const int num_tiles =
+      uniform(args.identity_T ? (args.identity_T + kPairRowsMx - 1) / kPairRowsMx : *args.num_tiles);
+  const int total = num_tiles * nf;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (both CTAs)
+    const uint64_t pol_w = policy_evict_normal();
+    const uint64_t pol_x = policy_evict_last();
+    const uint32_t s0 = smem_u32(smem);
+    const int me = uniform((int)rank);
+    const uint32_t full_lead = mapa_shared(full0, 0);   // the even CTA's full barriers
+    int stage = 0;
+    uint32_t phase = 0;
+    int armed = 0;
+    bool ok = true;
+    for (int item = pair0; item < total && ok; item += pairs) {
+      const Item w = uniform_item(item_of<kPairRowsMx>(args, item, num_tiles, nf));
+      const int arow = w.row0 + me * kMxTileRows;
+      const int sfa_row = (2 * w.tile + me) * kchunks;
+      const int sfb_row = (w.expert * (args.features / kSfRows) + 2 * w.f) * kchunks;
+      for (int ks = 0; ks < ksteps; ++ks) {
+        if (!warp_wait_cluster(empty0 + 8 * stage, phase ^ 1u, &s_abort, wlim)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sA = s0 + stage * C::kStageBytes;
+        const uint32_t sB = sA + C::kABytes;
+        const uint32_t sFa = sB + C::kBBytes, sFb = sFa + C::kSfaBytes;
+        const uint32_t fb = full_lead + 8 * stage;
+        if (elect_one()) {
+          if (lead) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * C::kStageBytes);
+          if (kW13)
+            tma_load_5d_pair(sB, &w_map, ks * 128, 0, 0, w.f * 4 + 2 * me, w.expert, fb, pol_w);
+          else
+            tma_load_3d_pair(sB, &w_map, ks * 128, w.f * kPairN + me * (kPairN / 2), w.expert, fb, pol_w);
+          tma_load_2d_pair(sA, &x_map, ks * 128, arow, fb, pol_x);
+          // scale chunks of this stage's 256 elements (a last odd chunk brings its
+          // neighbour's along; the MMAs stop at K)
+          tma_load_2d_pair(sFa, &sfa_map, 0, sfa_row + 2 * ks, fb, pol_x);
+          tma_load_2d_pair(sFb, &sfb_map, 0, sfb_row + 2 * ks, fb, pol_w);
+          tma_load_2d_pair(sFb + 2 * kSfChunkBytes, &sfb_map, 0, sfb_row + kchunks + 2 * ks, fb, pol_w);
+        }
+        __syncwarp();
+        armed = min(armed + 1, C::kStages);
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok) {
+      s_abort = 1;
+      if (lane == 0) atomicOr(args.status, kDevErrTimeout);
+    }
+    if (s_abort && lane == 0) {
+      if (lead) {
+        // copies already issued (ours and the odd CTA's) complete on our full barriers
+        volatile int no_abort = 0;
+        int s = stage;
+        uint32_t ph = phase;
+        for (int i = 0; i < armed; ++i) {
+          if (--s < 0) {
+            s = C::kStages - 1;
+            ph ^= 1u;
+          }
+          mbar_wait_cluster(full0 + 8 * s, ph, &no_abort);
+        }
+      } else {
+        // the odd CTA's copies complete on the even CTA's barriers: give any
+        // still in flight time to land in our shared memory
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 200000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (lead) {
+      int stage = 0;
+      uint32_t phase = 0;
+      const uint32_t s0 = smem_u32(smem);
+      const uint64_t adesc0 = sdesc_sw128(s0, 16, 1024), bdesc0 = sdesc_sw128(s0 + C::kABytes, 16, 1024);
+      const uint64_t fadesc0 = sdesc_scales(s0 + C::kABytes + C::kBBytes);
+      const uint64_t fbdesc0 = sdesc_scales(s0 + C::kABytes + C::kBBytes + C::kSfaBytes);
+      constexpr uint32_t kI0 = idesc_mxf4(kPairRowsMx, kPairN, 0), kI1 = idesc_mxf4(kPairRowsMx, kPairN, 1);
+      uint32_t soff = 0;
+      int n = 0;
+      bool ok = true;
+      for (int item = pair0; item < total && ok; item += pairs, ++n) {
+        // the previous tile's shared columns are read (which implies that
+        // the tile before it, in this accumulator, is read altogether)
+        if (n > 0 && !warp_wait_cluster(tshare, (uint32_t)(n - 1) & 1u, &s_abort, wlim)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d0 = tmem + (n & 1) * C::kAcc1;
+        for (int ks = 0; ks < ksteps; ++ks) {
+          if (!warp_wait_cluster(full0 + 8 * stage, phase, &s_abort, wlim)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t ta = tmem + C::kSfCol0 + stage * C::kSfCols, tb = ta + 8;
+          const uint64_t ad = adesc0 + soff, bd = bdesc0 + soff, fa = fadesc0 + soff, fbd = fbdesc0 + soff;
+          auto scales = [&](int c) {
+            cp_scales_pair(ta + 4 * c, fa + c * kSfUnits);
+            cp_scales_pair(tb + 8 * c, fbd + c * kSfUnits);
+            cp_scales_pair(tb + 8 * c + 4, fbd + (2 + c) * kSfUnits);
+          };
+          auto mmas = [&](int c, uint32_t accumulate) {
+            mma_mxf4_pair(d0, ad + 4 * c, bd + 4 * c, kI0, ta + 4 * c, tb + 8 * c, accumulate);
+            mma_mxf4_pair(d0, ad + 4 * c + 2, bd + 4 * c + 2, kI1, ta + 4 * c, tb + 8 * c, 1u);
+          };
+          if (elect_one()) {
+            scales(0);
+            if (2 * ks + 1 < kchunks) {
+              scales(1);
+              mmas(0, ks != 0 ? 1u : 0u);
+              mmas(1, 1u);
+            } else {
+              mmas(0, ks != 0 ? 1u : 0u);
+            }
+            mma_commit_pair(empty0 + 8 * stage, 0x3);
+            if (ks == ksteps - 1) mma_commit_pair(tfull0 + 8 * (n & 1), 0x3);
+          }
+          __syncwarp();
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+            soff = 0;
+          } else {
+            soff += C::kStageBytes >> 4;
+          }
+        }
+      }
+      if (!ok) {
+        s_abort = 1;
+        if (lane == 0) atomicOr(args.status, kDevErrTimeout);
+      }
+      if (elect_one()) mma_commit_pair(drain, 0x1);
+      __syncwarp();
+      volatile int no_abort = 0;
+      mbar_wait(drain, 0, &no_abort);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int quarter = warp & 3;              // TMEM lanes this warp may access
+    const int half = (warp - 2) / 4;           // its 64-column blocks: half and half + 2
+    const int r = quarter * 32 + lane;         // token row of the CTA's 128
+    uint8_t* buf = s_out + (warp - 2) * (32 * 128);
+    const uint32_t sbuf = smem_u32(buf);
+    int n = 0;
+    for (int item = pair0; item < total; item += pairs, ++n) {
+      const Item w = item_of<kPairRowsMx>(args, item, num_tiles, nf);
+      const int acc = n & 1;
+      int got = 1;
+      if (lane == 0) got = mbar_wait_cluster(tfull0 + 8 * acc, (uint32_t)(n >> 1) & 1u, &s_abort, wlim) ? 1 : 0;
+      got = __shfl_sync(0xffffffffu, got, 0);
+      if (!got) {
+        if (lane == 0) {
+          s_abort = 1;
+          atomicOr(args.status, kDevErrTimeout);
+        }
+        break;
+      }
+      tc_fence_after();
+      const uint32_t tbase = tmem + ((uint32_t)(quarter * 32) << 16) + acc * C::kAcc1;
+      const int valid = w.valid - (int)rank * kMxTileRows;       // of this CTA's rows
+      const size_t row = (size_t)w.row0 + rank * kMxTileRows + r;
+      const bool work = quarter * 32 < valid;
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        // the shared columns are the last of accumulator 0 and the first of
+        // accumulator 1: the two blocks that the warps read first hold them
+        const int b = half + 2 * (acc == 0 ? 1 - i : i);
+        float p[32], q[32];
+        if (work) tmem_load32x2(tbase + b * 64, p, tbase + b * 64 + 32, q);
+        if (i == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(mapa_shared(tshare, 0));
+        }
+        if (!work) continue;
+        if (kW13) {
+          const int feat = w.f * (kPairN / 2) + b * 32;
+          if (r < valid)
+            store_swiglu_block(p, q, args.out_codes + (row * args.out_ld + feat) / 2,
+                               args.out_sf +
+                                   ((size_t)(2 * w.tile + rank) * (args.out_ld / kSfChunkK) + feat / kSfChunkK) * kSfChunkBytes +
+                                   sf_row_offset(r) + (feat % kSfChunkK) / kBlock);
+        } else {
+          const int feat = w.f * kPairN + b * 64;
+          if (feat >= args.features) continue;
+          if (quarter * 32 + 32 <= valid) {
+            // 128 bytes a row in the 128-byte swizzle: 16-byte piece j of row l at j ^ (l & 7)
+            if (lane == 0) tma_store_wait_read();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int c = (8 * j + 2 * e) & 31;
+                const __nv_bfloat162 v = j < 4 ? __floats2bfloat162_rn(p[c], p[c + 1]) : __floats2bfloat162_rn(q[c], q[c + 1]);
+                o[e] = *reinterpret_cast<const uint32_t*>(&v);
+              }
+              *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tma_store_2d(&y_map, sbuf, feat, w.row0 + (int)rank * kMxTileRows + quarter * 32);
+          } else if (r < valid) {
+            store_bf16_block(p, args.out + row * args.out_ld + feat);
+            store_bf16_block(q, args.out + row * args.out_ld + feat + 32);
+          }
+        }
+      }
+    }
+    if (!kW13 && lane == 0) tma_store_wait();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // nothing of either CTA still targets the other's shared memory
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// Pairs of CTAs that can be resident at once, looked up once per device and kernel.
+template <bool kW13>
+int resident_pairs_mx(int sms) {
+  static int cache[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
+  int n = 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (unsigned)(sms / 2), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = PairCfgMx<kW13>::kSmemBytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, mx_gemm_pair_kernel<kW13>, &cfg) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    n = sms / 2;
+  }
+  n = n < sms / 2 ? n : sms / 2;
+  if (dev >= 0 && dev < 64) cache[dev] = n;
+  return n;
+}
+
+template <bool kW13>
+void launch_pair_mx(const MxMaps& m, MxGemmArgs a, int64_t max_tiles, int sms, cudaStream_t s) {
+  auto kernel = mx_gemm_pair_kernel<kW13>;
+  constexpr int smem = (int)PairCfgMx<kW13>::kSmemBytes;
+  static bool attr_set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  const int64_t items = max_tiles * ((a.features + kPairN - 1) / kPairN);
+  if (items <= 0) return;
+  const int cap = resident_pairs_mx<kW13>(sms);
+  const int pairs = (int)(items < cap ? items : cap);
+  a.concurrent = pairs;
+  launch_pdl(kernel, dim3(2 * pairs), dim3(kThreads), smem, s, m.w, m.x, m.sfa, m.sfb, m.y, a);
+}
+
 template <bool kW13, int BN>
-void launch(const CUtensorMap& w_map, const CUtensorMap& x_map, const CUtensorMap& x_small, MxGemmArgs a,
-            int64_t max_tiles, int sms, cudaStream_t s) {
+void launch(const MxMaps& m, MxGemmArgs a, int64_t max_tiles, int sms, cudaStream_t s) {
   auto kernel = mx_gemm_kernel<kW13, BN>;
   constexpr int smem = (int)Cfg<BN>::kSmemBytes;
   static bool attr_set[64] = {false};
@@ -415,7 +806,7 @@ void launch(const CUtensorMap& w_map, const CUtensorMap& x_map, const CUtensorMa
   if (items <= 0) return;
   const int grid = (int)(items < sms ? items : sms);
   a.concurrent = grid;
-  launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, s, w_map, x_map, x_small, a);
+  launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, s, m.w, m.x, m.x_small, a);
 }
 
 // Routed rows in tile order: a warp a row (16 bytes of codes a lane, then one
@@ -423,18 +814,18 @@ void launch(const CUtensorMap& w_map, const CUtensorMap& x_map, const CUtensorMa
 constexpr int kGatherWarps = 8;
 __global__ void __launch_bounds__(32 * kGatherWarps) mx_gather_kernel(
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, const int32_t* __restrict__ sorted, int slots,
-    int T, int H, const GemmTile* __restrict__ tiles, const int32_t* __restrict__ num_tiles, int identity_T,
+    int T, int H, const GemmTile* __restrict__ tiles, const int32_t* __restrict__ num_tiles, int tile_rows, int identity_T,
     uint8_t* __restrict__ x_perm, uint8_t* __restrict__ x_sf) {
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = identity_T ? (identity_T + kMxTileRows - 1) / kMxTileRows : *num_tiles;
+  const int n = identity_T ? (identity_T + tile_rows - 1) / tile_rows : *num_tiles;
   const int kchunks = H / kSfChunkK;
   const long long R = (long long)T * slots;
-  const long long rows = (long long)n * kMxTileRows;
+  const long long rows = (long long)n * tile_rows;
   const long long step = (long long)gridDim.x * kGatherWarps;
   for (long long i = (long long)blockIdx.x * kGatherWarps + warp; i < rows; i += step) {
-    const int tile = (int)(i / kMxTileRows), r = (int)(i % kMxTileRows);
+    const int tile = (int)(i / tile_rows), r = (int)(i % tile_rows);
     long long token;
     size_t row = (size_t)i;
     if (identity_T) {
@@ -452,7 +843,8 @@ __global__ void __launch_bounds__(32 * kGatherWarps) mx_gather_kernel(
     }
     const uint32_t* ssrc = reinterpret_cast<const uint32_t*>(scales + token * (H / kBlock));
     for (int c = lane; c < kchunks; c += 32)
-      *reinterpret_cast<uint32_t*>(x_sf + ((size_t)tile * kchunks + c) * kSfChunkBytes + sf_row_offset(r)) = __ldg(ssrc + c);
+      *reinterpret_cast<uint32_t*>(x_sf + ((size_t)(i / kSfRows) * kchunks + c) * kSfChunkBytes + sf_row_offset(r % kSfRows)) =
+          __ldg(ssrc + c);
   }
 }
 
@@ -462,37 +854,46 @@ bool mx_gemm_smem_ok() {
   int dev = 0, optin = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-  return optin >= (int)Cfg<256>::kSmemBytes && optin >= (int)Cfg<64>::kSmemBytes;
+  return optin >= (int)Cfg<256>::kSmemBytes && optin >= (int)Cfg<64>::kSmemBytes &&
+         optin >= (int)PairCfgMx<true>::kSmemBytes && optin >= (int)PairCfgMx<false>::kSmemBytes;
 }
 
-int mx_tile_features(bool w13, int features, int64_t max_tiles, int sms) {
-  (void)w13;
+int mx_tile_rows(int64_t rows, int experts) {
+  return rows >= (int64_t)kPairRowsMx * experts ? kPairRowsMx : kMxTileRows;
+}
+
+int mx_tile_features(int tile_rows, int features, int64_t max_tiles, int sms) {
+  if (tile_rows == kPairRowsMx) return kPairN;
   const int64_t wide = max_tiles * ((features + 255) / 256);
   return wide >= 2 * sms ? 256 : 64;
 }
 
-void launch_mx_gemm(bool w13, const CUtensorMap& w_map, const CUtensorMap& x_map, const CUtensorMap& x_small,
-                    const MxGemmArgs& a, int64_t max_tiles, int sms, cudaStream_t s) {
-  if (a.tile_features == 256) {
+void launch_mx_gemm(bool w13, const MxMaps& m, const MxGemmArgs& a, int64_t max_tiles, int sms, cudaStream_t s) {
+  if (a.tile_rows == kPairRowsMx) {
     if (w13)
-      launch<true, 256>(w_map, x_map, x_small, a, max_tiles, sms, s);
+      launch_pair_mx<true>(m, a, max_tiles, sms, s);
     else
-      launch<false, 256>(w_map, x_map, x_small, a, max_tiles, sms, s);
+      launch_pair_mx<false>(m, a, max_tiles, sms, s);
+  } else if (a.tile_features == 256) {
+    if (w13)
+      launch<true, 256>(m, a, max_tiles, sms, s);
+    else
+      launch<false, 256>(m, a, max_tiles, sms, s);
   } else {
     if (w13)
-      launch<true, 64>(w_map, x_map, x_small, a, max_tiles, sms, s);
+      launch<true, 64>(m, a, max_tiles, sms, s);
     else
-      launch<false, 64>(w_map, x_map, x_small, a, max_tiles, sms, s);
+      launch<false, 64>(m, a, max_tiles, sms, s);
   }
 }
 
 void launch_mx_gather(const uint8_t* codes, const uint8_t* scales, const int32_t* sorted_route_ids, int slots,
-                      int T, int H, const GemmTile* tiles, const int32_t* num_tiles, int identity_T,
+                      int T, int H, const GemmTile* tiles, const int32_t* num_tiles, int tile_rows, int identity_T,
                       int64_t max_tiles, uint8_t* x_perm, uint8_t* x_sf, cudaStream_t s) {
-  const int64_t blocks = max_tiles * kMxTileRows / kGatherWarps;
+  const int64_t blocks = max_tiles * tile_rows / kGatherWarps;
   const int grid = (int)(blocks < 152 * 8 ? blocks : 152 * 8);
   launch_pdl(mx_gather_kernel, dim3(grid), dim3(32 * kGatherWarps), 0, s, codes, scales, sorted_route_ids, slots, T, H,
-             tiles, num_tiles, identity_T, x_perm, x_sf);
+             tiles, num_tiles, tile_rows, identity_T, x_perm, x_sf);
 }
 
 }  // namespace moe

@@ -365,14 +365,16 @@ def test_expert_ffn_nan_and_zero_rows(moe):
     assert (np.abs(got[[0, 2]] - ref) <= tol).all()
 
 
-def test_expert_ffn_rows_do_not_depend_on_the_batch(moe):
-    """A token alone (narrow work items) and in a batch of many tiles (wide ones): the same bits."""
+@pytest.mark.parametrize("N", [32, 16])
+def test_expert_ffn_rows_do_not_depend_on_the_batch(moe, N):
+    """A token alone (narrow work items) and in a batch of many tiles (wide ones; with 16
+    experts CTA pairs): the same bits."""
     torch = torch_()
     rng = np.random.default_rng(11)
-    L = Layer(moe, 768, 32, 4, 640, 16, Is=256, seed=6)
+    L = Layer(moe, 768, N, 4, 640, 16, Is=256, seed=6)
     T = 1600
     c, s = (torch.from_numpy(v).cuda() for v in _tokens(rng, T, 768))
-    idx = torch.from_numpy(np.sort(np.argsort(rng.random((T, 32)), axis=1)[:, :4], axis=1).astype(np.int32)).cuda()
+    idx = torch.from_numpy(np.sort(np.argsort(rng.random((T, N)), axis=1)[:, :4], axis=1).astype(np.int32)).cuda()
     d = L.dispatch(idx)
     y, ysh = L.ffn(c, s, d)
     for t in (0, 3, 801, 1599):
