@@ -497,7 +497,7 @@ moe_status moe_check_scoring(const moe_config* cfg, const moe_scoring* scoring);
  *   groups rank by the largest b or the sum of the two largest; the experts
  *   outside the top_groups best are left out (not scored as zero)
  *   the k largest b; gate = scale * s, with renormalize scale * s / (sum of the
- *   selected s in slot order + 1e-20)
+ *   selected s + 1e-20), the sum in one order for every T
  *   logits [T, N] fp32, score_bias [N] fp32 or NULL
  *   topk_idx [T, k] int32 out, experts in ascending index; topk_gate [T, k] fp32 out
  * Ties go to the lower index (of expert and of group); NaN ranks last.  A row

@@ -158,7 +158,9 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle where torch offers it: building a Stream object costs about as much as a launch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -382,22 +384,25 @@ def _scoring(scoring) -> moe_scoring:
 
 
 def _want(name, t, dtype, shape, optional=False):
-    """A contiguous CUDA tensor of this type and shape (the C entry points see pointers only)."""
+    """The address of a contiguous CUDA tensor of this type and shape (the C entry points see
+    pointers only); None for an optional one that is absent."""
     import torch
     if t is None:
         if optional:
-            return
+            return None
         raise ValueError(f"{name}: a tensor is needed")
-    if t.dtype != getattr(torch, dtype) or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype is not getattr(torch, dtype) or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: a contiguous CUDA tensor of {dtype} {tuple(shape)} is needed, got "
                          f"{t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'} on {t.device}")
+    return t.data_ptr()
 
 
 def _want_at_least(name, t, dtype, n):
-    """A contiguous CUDA tensor of this type with at least n elements."""
+    """The address of a contiguous CUDA tensor of this type with at least n elements."""
     import torch
-    if t is None or t.dtype != getattr(torch, dtype) or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
+    if t is None or t.dtype is not getattr(torch, dtype) or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: a contiguous CUDA tensor of at least {n} {dtype} is needed")
+    return t.data_ptr()
 
 
 def moe_check_scoring(cfg, scoring) -> int:
@@ -407,70 +412,58 @@ def moe_check_scoring(cfg, scoring) -> int:
 def moe_add_norm(x, residual, weight, eps, residual_out, out, codes=None, scales=None, stream=None):
     """x [T, H] bf16 (+ residual) -> residual_out, out [T, H] bf16 and the MX tensor of out;
     residual, residual_out, out and the pair (codes, scales) may be None."""
-    T, H = x.shape
-    _want("x", x, "bfloat16", (T, H))
-    _want("residual", residual, "bfloat16", (T, H), optional=True)
-    _want("weight", weight, "bfloat16", (H,))
-    _want("residual_out", residual_out, "bfloat16", (T, H), optional=True)
-    _want("out", out, "bfloat16", (T, H), optional=True)
-    _want("codes", codes, "uint8", (T, H // 2), optional=True)
-    _want("scales", scales, "uint8", (T, H // 32), optional=True)
+    shape = T, H = x.shape
     _check("moe_add_norm", _lib.moe_add_norm(
-        T, H, _ptr(x), _ptr(residual), _ptr(weight), float(eps), _ptr(residual_out), _ptr(out),
-        _ptr(codes), _ptr(scales), _stream(stream)))
+        T, H, _want("x", x, "bfloat16", shape), _want("residual", residual, "bfloat16", shape, True),
+        _want("weight", weight, "bfloat16", (H,)), eps,
+        _want("residual_out", residual_out, "bfloat16", shape, True), _want("out", out, "bfloat16", shape, True),
+        _want("codes", codes, "uint8", (T, H // 2), True), _want("scales", scales, "uint8", (T, H // 32), True),
+        _stream(stream)))
 
 
 def moe_route_scored(cfg, scoring, logits, score_bias, topk_idx, topk_gate, stream=None):
     c = _cfg(cfg)
     T = logits.shape[0]
-    _want("logits", logits, "float32", (T, c.num_experts))
-    _want("score_bias", score_bias, "float32", (c.num_experts,), optional=True)
-    _want("topk_idx", topk_idx, "int32", (T, c.top_k))
-    _want("topk_gate", topk_gate, "float32", (T, c.top_k))
     _check("moe_route_scored", _lib.moe_route_scored(
-        ctypes.byref(c), ctypes.byref(_scoring(scoring)), T, _ptr(logits), _ptr(score_bias),
-        _ptr(topk_idx), _ptr(topk_gate), _stream(stream)))
+        ctypes.byref(c), ctypes.byref(_scoring(scoring)), T, _want("logits", logits, "float32", (T, c.num_experts)),
+        _want("score_bias", score_bias, "float32", (c.num_experts,), True),
+        _want("topk_idx", topk_idx, "int32", (T, c.top_k)), _want("topk_gate", topk_gate, "float32", (T, c.top_k)),
+        _stream(stream)))
 
 
-def _mx_shape(codes, scales, lead, K):
-    _want("codes", codes, "uint8", (*lead, K // 2))
-    _want("scales", scales, "uint8", (*lead, K // 32))
+def _mx(codes, scales, lead, K):
+    return _want("codes", codes, "uint8", (*lead, K // 2)), _want("scales", scales, "uint8", (*lead, K // 32))
 
 
 def moe_quantize_mx(x, codes, scales, stream=None):
     """x [..., K] bf16 -> codes [..., K/2], scales [..., K/32] (uint8)."""
-    *lead, K = x.shape
-    _want("x", x, "bfloat16", x.shape)
-    _mx_shape(codes, scales, lead, K)
+    shape = *lead, K = x.shape
     _check("moe_quantize_mx", _lib.moe_quantize_mx(
-        x.numel() // K if K else 0, K, _ptr(x), _ptr(codes), _ptr(scales), _stream(stream)))
+        x.numel() // K if K else 0, K, _want("x", x, "bfloat16", shape), *_mx(codes, scales, lead, K),
+        _stream(stream)))
 
 
 def moe_dequantize_mx(codes, scales, out, stream=None):
     """codes [..., K/2], scales [..., K/32] -> out [..., K] bf16."""
-    *lead, K = out.shape
-    _want("out", out, "bfloat16", out.shape)
-    _mx_shape(codes, scales, lead, K)
+    shape = *lead, K = out.shape
     _check("moe_dequantize_mx", _lib.moe_dequantize_mx(
-        out.numel() // K if K else 0, K, _ptr(codes), _ptr(scales), _ptr(out), _stream(stream)))
+        out.numel() // K if K else 0, K, *_mx(codes, scales, lead, K), _want("out", out, "bfloat16", shape),
+        _stream(stream)))
 
 
 def moe_quantize_weights_mx(w, codes, scales, stream=None):
     """w [experts, K, F] bf16 -> codes [experts, F, K/2], scales [experts, F, K/32]."""
-    E, K, F = w.shape
-    _want("w", w, "bfloat16", (E, K, F))
-    _mx_shape(codes, scales, (E, F), K)
+    shape = E, K, F = w.shape
     _check("moe_quantize_weights_mx", _lib.moe_quantize_weights_mx(
-        E, K, F, _ptr(w), _ptr(codes), _ptr(scales), _stream(stream)))
+        E, K, F, _want("w", w, "bfloat16", shape), *_mx(codes, scales, (E, F), K), _stream(stream)))
 
 
 def moe_pack_scales_mx(scales, packed, gate_up, stream=None):
     """scales [experts, rows, K/32] -> packed, the same shape, in the GEMMs' order."""
-    E, rows, blocks = scales.shape
-    _want("scales", scales, "uint8", scales.shape)
-    _want("packed", packed, "uint8", scales.shape)
+    shape = E, rows, blocks = scales.shape
     _check("moe_pack_scales_mx", _lib.moe_pack_scales_mx(
-        E, rows, blocks * 32, int(gate_up), _ptr(scales), _ptr(packed), _stream(stream)))
+        E, rows, blocks * 32, int(gate_up), _want("scales", scales, "uint8", shape),
+        _want("packed", packed, "uint8", shape), _stream(stream)))
 
 
 def moe_workspace_bytes_mx(cfg, max_tokens: int) -> int:
@@ -515,6 +508,7 @@ def moe_expert_ffn_mx(cfg, x_codes, x_scales, w13, w13_scales, w2, w2_scales, w1
     _want_at_least("y_perm", y_perm, "bfloat16", rows * H)
     if c.shared_intermediate > 0:
         _want_at_least("y_shared", y_shared, "bfloat16", T * H)
+    _want_at_least("ws", ws, "uint8", 1)
     _check("moe_expert_ffn_mx", _lib.moe_expert_ffn_mx(
         ctypes.byref(c), T, _ptr(x_codes), _ptr(x_scales), _ptr(w13), _ptr(w13_scales), _ptr(w2),
         _ptr(w2_scales), _ptr(w13_shared), _ptr(w13_shared_scales), _ptr(w2_shared),
@@ -536,6 +530,7 @@ def moe_forward_mx(cfg, scoring, x, residual, norm_weight, eps, w_gate, router_b
     _want("score_bias", score_bias, "float32", (c.num_experts,), optional=True)
     _want_experts(c, w13, w13_scales, w2, w2_scales, w13_shared, w13_shared_scales, w2_shared, w2_shared_scales)
     _want("out", out, "bfloat16", (T, H))
+    _want_at_least("ws", ws, "uint8", 1)
     _check("moe_forward_mx", _lib.moe_forward_mx(
         ctypes.byref(c), ctypes.byref(_scoring(scoring)), T, _ptr(x), _ptr(residual), _ptr(norm_weight),
         float(eps), _ptr(w_gate), _ptr(router_bias), _ptr(score_bias), _ptr(w13), _ptr(w13_scales),

@@ -7,7 +7,7 @@
 //
 // The sum of squares has one order for every batch and thread count: eight
 // elements in turn, the 32 groups of a 256-element chunk by a fixed tree,
-// then the chunks in ascending order.  How many warps share a row is thus
+// then the chunks by another.  How many warps share a row is thus
 // free to follow the batch.
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -82,8 +82,16 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const uint16_t* __restri
   }
   __syncthreads();
   float total = 0.0f;
-  for (int c = 0; c < chunks; ++c) total += s_sum[c];
-  const float inv = 1.0f / sqrtf(total / (float)H + eps);
+#pragma unroll
+  for (int c = 0; c < kNormMaxChunks; c += 64) {
+    float u = c + lane < chunks ? s_sum[c + lane] : 0.0f;
+    if (c + 32 + lane < chunks) u += s_sum[c + 32 + lane];
+    total += u;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  const float root = sqrtf(total / (float)H + eps), inv = 1.0f / root;
+  const bool finite = root <= 3.402823466e38f;   // no correction of a quotient by infinity
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (warp + i * warps) * kNormChunk + lane * 8;
@@ -92,7 +100,12 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const uint16_t* __restri
     float w[8], n[8];
     unpack8(wv[i], w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) n[j] = v[i][j] * inv * w[j];
+    for (int j = 0; j < 8; ++j) {
+      // v / root with one correction: the product alone rounds twice, which
+      // turns a bf16 rounding (and a 4-bit one behind it) twice as often
+      const float q = v[i][j] * inv;
+      n[j] = (finite ? fmaf(fmaf(-q, root, v[i][j]), inv, q) : q) * w[j];
+    }
     const uint4 nb = pack_bf16(n);
     if (in && out) *reinterpret_cast<uint4*>(out + row + c) = nb;
     if (codes) {

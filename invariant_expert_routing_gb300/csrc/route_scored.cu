@@ -1,7 +1,7 @@
 // Routing by scores (sigmoid or softmax) with a selection bias, expert groups
 // and renormalised, scaled gates.
 //
-// Per token, one warp, expert e = lane + 32 s in register s of a lane:
+// Per token, one warp:
 //   score_e = 1 / (1 + exp(-l_e))  or  exp(l_e - m) / sum_i exp(l_i - m)
 //   b_e = score_e + bias_e                       (selection only)
 //   groups of N / G consecutive experts rank by the largest b or by the sum
@@ -9,9 +9,16 @@
 //   the k largest b of the experts that stay; slots in ascending expert order
 //   gate_j = scale * score_j [/ (sum of the selected scores + 1e-20)]
 // Ties go to the lower index, NaN ranks last.  Values are ranked through
-// order-preserving 32-bit keys, so that the warp-wide maximum is one redux
-// instruction and a round of the top-k two (largest key, then the lowest
-// expert among the lanes that hold it).
+// order-preserving 32-bit keys, so that the warp-wide maximum of a round of
+// the top-k is one redux instruction.
+//
+// Two kernels, by N and the groups alone.  Where a lane can hold 4 or 8
+// consecutive experts of one group, each lane sorts its four best keys (keys
+// only, 16 compare-exchanges); group scores are a merge of the lanes' first two,
+// and a round is a redux, a ballot and a shift of the winner's list, without a
+// scan of the lane's experts.  Any other shape takes experts lane + 32 s and
+// scans.  Bound by instruction issue; the scores alone (an exponential and a
+// reciprocal per expert) are a fifth of it.
 #include <cmath>
 #include <cstdint>
 
@@ -37,8 +44,198 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
 }
 
+__device__ __forceinline__ float sigmoid(float l) {
+  // accurate exponential; the reciprocal is off by one unit at most, 0 for an infinite argument
+  return __fdividef(1.0f, 1.0f + expf(-l));
+}
+
+__device__ __forceinline__ void order(uint32_t& a, uint32_t& b) {   // a >= b
+  const uint32_t x = max(a, b);
+  b = min(a, b);
+  a = x;
+}
+__device__ __forceinline__ void sort4(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  order(a, b);
+  order(c, d);
+  order(a, c);
+  order(b, d);
+  order(b, c);
+}
+
+// The four largest of a lane's E keys, descending.
+template <int E>
+__device__ __forceinline__ void best_four(const uint32_t (&key)[E], uint32_t (&top)[4]) {
+  uint32_t lo[4] = {key[0], key[1], key[2], key[3]};
+  sort4(lo[0], lo[1], lo[2], lo[3]);
+  if (E == 8) {
+    uint32_t hi[4] = {key[E - 4], key[E - 3], key[E - 2], key[E - 1]};
+    sort4(hi[0], hi[1], hi[2], hi[3]);
+    // the larger of lo[i] and hi[3 - i] are the four largest, a bitonic sequence
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lo[i] = max(lo[i], hi[3 - i]);
+    order(lo[0], lo[2]);
+    order(lo[1], lo[3]);
+    order(lo[0], lo[1]);
+    order(lo[2], lo[3]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top[i] = lo[i];
+}
+
+// A lane's `count` largest keys are taken, the last of them `last`: their bits
+// (equal keys: the lower index first); they leave the keys.
+template <int E>
+__device__ __forceinline__ uint32_t take(uint32_t (&key)[E], int count, uint32_t last) {
+  uint32_t bits = 0;
+  int equal = count;
+#pragma unroll
+  for (int s = 0; s < E; ++s) equal -= count > 0 && key[s] > last ? 1 : 0;
+#pragma unroll
+  for (int s = 0; s < E; ++s) {
+    const bool eq = key[s] == last && equal > 0;
+    const bool hit = count > 0 && (key[s] > last || eq);
+    equal -= eq ? 1 : 0;
+    bits |= hit ? 1u << s : 0u;
+    key[s] = hit ? 0u : key[s];
+  }
+  return bits;
+}
+
+// E consecutive experts a lane; groups of whole lanes, a power of two of them.
+template <int E>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
+    const float* __restrict__ logits, const float* __restrict__ bias, int T, int N, int k, int sigmoids, int groups,
+    int top_groups, int top2, int renormalize, float scale, int32_t* __restrict__ idx_out,
+    float* __restrict__ gate_out) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long t = (long long)blockIdx.x * kRouteWarps + warp;
+  constexpr uint32_t kAll = 0xffffffffu;
+  const bool in = lane * E < N;   // N % E == 0: a lane's experts exist or do not together
+  pdl_wait();
+  pdl_trigger();
+  if (t >= T) return;
+  float sc[E];
+  uint32_t key[E];
+#pragma unroll
+  for (int q = 0; q < E / 4; ++q) {
+    const float4 v = in ? __ldcs(reinterpret_cast<const float4*>(logits + t * N + lane * E) + q)
+                        : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    sc[4 * q] = v.x;
+    sc[4 * q + 1] = v.y;
+    sc[4 * q + 2] = v.z;
+    sc[4 * q + 3] = v.w;
+  }
+  if (sigmoids) {
+#pragma unroll
+    for (int s = 0; s < E; ++s) sc[s] = sigmoid(sc[s]);
+  } else {
+    float m = sc[0];
+#pragma unroll
+    for (int s = 1; s < E; ++s) m = fmaxf(m, sc[s]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
+    if (m == -INFINITY) m = 0.0f;   // every logit is -inf (or NaN): scores 0 (NaN)
+    float sum = 0.0f;
+#pragma unroll
+    for (int s = 0; s < E; ++s) {
+      sc[s] = expf(sc[s] - m);
+      sum += sc[s];
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
+    const float inv = sum == 0.0f ? 1.0f : 1.0f / sum;
+#pragma unroll
+    for (int s = 0; s < E; ++s) sc[s] *= inv;
+  }
+  if (bias && in) {
+#pragma unroll
+    for (int q = 0; q < E / 4; ++q) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(bias + lane * E) + q);
+      key[4 * q] = key_of(sc[4 * q] + v.x);
+      key[4 * q + 1] = key_of(sc[4 * q + 1] + v.y);
+      key[4 * q + 2] = key_of(sc[4 * q + 2] + v.z);
+      key[4 * q + 3] = key_of(sc[4 * q + 3] + v.w);
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < E; ++s) key[s] = in ? key_of(sc[s]) : 0u;
+  }
+  uint32_t top[4];
+  best_four<E>(key, top);
+
+  if (groups > 1) {
+    const int lanes = N / groups / E;   // of one group
+    uint32_t a = top[0], b = top[1];
+    for (int off = 1; off < lanes; off <<= 1) {
+      const uint32_t oa = __shfl_xor_sync(kAll, a, off), ob = __shfl_xor_sync(kAll, b, off);
+      b = max(min(a, oa), max(b, ob));
+      a = max(a, oa);
+    }
+    const uint32_t gkey = top2 ? key_of(value_of(a) + value_of(b)) : a;
+    const int mine = lane / lanes;
+    int better = 0;
+    for (int g = 0; g < groups; ++g) {
+      const uint32_t o = __shfl_sync(kAll, gkey, g * lanes);
+      better += (o > gkey || (o == gkey && g < mine)) ? 1 : 0;
+    }
+    if (better >= top_groups) {
+#pragma unroll
+      for (int s = 0; s < E; ++s) key[s] = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top[i] = 0u;
+    }
+  }
+
+  uint32_t chosen = 0, last = 0;   // bit s: expert lane * E + s is selected
+  int count = 0;
+  for (int j = 0; j < k; ++j) {
+    const uint32_t best = __reduce_max_sync(kAll, top[0]);
+    const unsigned who = __ballot_sync(kAll, top[0] == best);
+    if (lane == __ffs(who) - 1) {   // the lowest lane: the lowest expert of equal keys
+      ++count;
+      last = best;
+      top[0] = top[1];
+      top[1] = top[2];
+      top[2] = top[3];
+      top[3] = 0u;
+    }
+    if (E > 4 && __any_sync(kAll, count == 4)) {   // a lane's list has run out: its next four
+      if (count == 4) {
+        chosen |= take<E>(key, count, last);
+        best_four<E>(key, top);
+        count = 0;
+      }
+    }
+  }
+  chosen |= take<E>(key, count, last);
+
+  float sum = 0.0f;
+  if (renormalize) {
+#pragma unroll
+    for (int s = 0; s < E; ++s) sum += (chosen >> s) & 1u ? sc[s] : 0.0f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
+  }
+  const float factor = renormalize ? scale / (sum + 1e-20f) : scale;
+  // slots: the selected experts of lower lanes come first
+  const int n = __popc(chosen);
+  int base = 0;
+#pragma unroll
+  for (int bit = 0; bit < 4; ++bit)
+    base += __popc(__ballot_sync(kAll, (n >> bit) & 1) & ((1u << lane) - 1u)) << bit;
+  int32_t* io = idx_out + t * k + base;
+  float* go = gate_out + t * k + base;
+#pragma unroll
+  for (int s = 0; s < E; ++s) {
+    if ((chosen >> s) & 1u) {
+      *io++ = lane * E + s;
+      *go++ = sc[s] * factor;
+    }
+  }
+}
+
 __global__ void __launch_bounds__(32 * kRouteWarps) route_scored_kernel(
-    const float* __restrict__ logits, const float* __restrict__ bias, int T, int N, int k, int sigmoid, int groups,
+    const float* __restrict__ logits, const float* __restrict__ bias, int T, int N, int k, int sigmoids, int groups,
     int top_groups, int top2, int renormalize, float scale, int32_t* __restrict__ idx_out,
     float* __restrict__ gate_out) {
   __shared__ uint32_t s_key[kRouteWarps][32 * kSlots];
@@ -53,9 +250,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scored_kernel(
   uint32_t key[kSlots];
 #pragma unroll
   for (int s = 0; s < kSlots; ++s) sc[s] = lane + 32 * s < N ? __ldg(row + lane + 32 * s) : -INFINITY;
-  if (sigmoid) {
+  if (sigmoids) {
 #pragma unroll
-    for (int s = 0; s < kSlots; ++s) sc[s] = 1.0f / (1.0f + expf(-sc[s]));
+    for (int s = 0; s < kSlots; ++s) sc[s] = sigmoid(sc[s]);
   } else {
     float m = sc[0];
 #pragma unroll
@@ -160,9 +357,21 @@ int route_scored_max_groups() { return kMaxGroups; }
 void launch_route_scored(const float* logits, const float* bias, int T, int N, int k, bool sigmoid, int groups,
                          int top_groups, bool top2, bool renormalize, float scale, int32_t* topk_idx,
                          float* topk_gate, cudaStream_t s) {
-  launch_pdl(route_scored_kernel, dim3((T + kRouteWarps - 1) / kRouteWarps), dim3(32 * kRouteWarps), 0, s, logits,
-             bias, T, N, k, sigmoid ? 1 : 0, groups, top_groups, top2 ? 1 : 0, renormalize ? 1 : 0, scale, topk_idx,
-             topk_gate);
+  // a lane's experts lie in one group, and a group is a power of two of lanes
+  auto lanes_ok = [&](int e) {
+    if (N % e || N > 32 * e) return false;
+    if (groups == 1) return true;
+    const int size = N / groups;
+    return size % e == 0 && (size / e & (size / e - 1)) == 0;
+  };
+  const dim3 grid((T + kRouteWarps - 1) / kRouteWarps), block(32 * kRouteWarps);
+  if (lanes_ok(4) || lanes_ok(8)) {
+    launch_pdl(lanes_ok(4) ? route_lanes_kernel<4> : route_lanes_kernel<8>, grid, block, 0, s, logits, bias, T, N, k,
+               sigmoid ? 1 : 0, groups, top_groups, top2 ? 1 : 0, renormalize ? 1 : 0, scale, topk_idx, topk_gate);
+    return;
+  }
+  launch_pdl(route_scored_kernel, grid, block, 0, s, logits, bias, T, N, k, sigmoid ? 1 : 0,
+             groups, top_groups, top2 ? 1 : 0, renormalize ? 1 : 0, scale, topk_idx, topk_gate);
 }
 
 }  // namespace moe

@@ -165,6 +165,11 @@ ROUTES = [  # T, N, k, sigmoid, bias, groups, top_groups, top2, renorm
     (17, 250, 3, True, True, 25, 2, False, True),
     (9, 64, 4, False, False, 32, 7, True, True),
     (300, 96, 7, True, True, 3, 1, True, True),
+    (70, 256, 16, False, True, 1, 1, False, True),
+    (70, 128, 6, True, True, 32, 9, True, True),
+    (70, 224, 12, True, False, 7, 2, False, False),     # a lane's list runs out (16 lanes, 12 slots)
+    (90, 256, 16, True, True, 32, 2, True, True),       # every expert of two lanes
+    (40, 16, 11, False, False, 2, 2, True, True),
 ]
 
 
@@ -230,6 +235,18 @@ def test_route_masked_and_non_finite_logits(moe):
     # softmax of a row with a NaN or +inf: no answer but NaN; the indices stay in range and distinct
     got_idx, _ = _route(moe, l[[3, 4, 5]], None, 4, False, 4, 2, True, True)
     assert ((got_idx >= 0) & (got_idx < 32)).all() and (np.diff(got_idx, axis=1) > 0).all()
+
+
+def test_route_takes_many_experts_of_one_lane(moe):
+    """Ascending and descending runs: the best of a row sit next to each other, with and without ties."""
+    base = np.linspace(-2, 2, 256)
+    l = np.stack([base, base[::-1], np.repeat(np.linspace(2, -2, 32), 8), np.repeat(np.linspace(-2, 2, 64), 4)])
+    for k in (5, 8, 13, 16):
+        for sigmoid in (True, False):
+            idx, gate, _ = mx_ref.route(l, None, k, sigmoid, renorm=True)
+            got_idx, got_gate = _route(moe, l, None, k, sigmoid, 1, 1, False, True)
+            np.testing.assert_array_equal(got_idx, idx)
+            np.testing.assert_allclose(got_gate, gate, rtol=2e-6)
 
 
 def test_route_rows_do_not_depend_on_the_batch(moe):
