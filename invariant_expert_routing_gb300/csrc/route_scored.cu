@@ -8,17 +8,16 @@
 //   of the two largest; the best `top_groups` stay
 //   the k largest b of the experts that stay; slots in ascending expert order
 //   gate_j = scale * score_j [/ (sum of the selected scores + 1e-20)]
-// Ties go to the lower index, NaN ranks last.  Values are ranked through
-// order-preserving 32-bit keys, so that the warp-wide maximum of a round of
-// the top-k is one redux instruction.
+// Ties go to the lower index, NaN ranks last.
 //
 // Two kernels, by N and the groups alone.  Where a lane can hold 4 or 8
-// consecutive experts of one group, each lane sorts its four best keys (keys
-// only, 16 compare-exchanges); group scores are a merge of the lanes' first two,
-// and a round is a redux, a ballot and a shift of the winner's list, without a
-// scan of the lane's experts.  Any other shape takes experts lane + 32 s and
-// scans.  Bound by instruction issue; the scores alone (an exponential and a
-// reciprocal per expert) are a fifth of it.
+// consecutive experts of one group, each lane sorts its four best values (16
+// compare-exchanges, no indices); group scores are a merge of the lanes' first
+// two, and a round of the top-k is a redux, a ballot and a shift of the
+// winner's list, without a scan of the lane's experts.  Any other shape, and
+// a row with an infinite or NaN value, takes experts lane + 32 s and scans,
+// ranking through order-preserving integer keys.  Bound by instruction issue;
+// the scores alone (an exponential and a reciprocal per expert) are a fifth.
 #include <cmath>
 #include <cstdint>
 
@@ -46,232 +45,52 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 
 __device__ __forceinline__ float sigmoid(float l) {
   // accurate exponential; the reciprocal is off by one unit at most, 0 for an infinite argument
-  return __fdividef(1.0f, 1.0f + expf(-l));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-l)));
+  return r;
 }
 
-__device__ __forceinline__ void order(uint32_t& a, uint32_t& b) {   // a >= b
-  const uint32_t x = max(a, b);
-  b = min(a, b);
-  a = x;
-}
-__device__ __forceinline__ void sort4(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
-  order(a, b);
-  order(c, d);
-  order(a, c);
-  order(b, d);
-  order(b, c);
-}
-
-// The four largest of a lane's E keys, descending.
+// Scores of a lane's E experts from its logits (absent experts: -inf).
 template <int E>
-__device__ __forceinline__ void best_four(const uint32_t (&key)[E], uint32_t (&top)[4]) {
-  uint32_t lo[4] = {key[0], key[1], key[2], key[3]};
-  sort4(lo[0], lo[1], lo[2], lo[3]);
-  if (E == 8) {
-    uint32_t hi[4] = {key[E - 4], key[E - 3], key[E - 2], key[E - 1]};
-    sort4(hi[0], hi[1], hi[2], hi[3]);
-    // the larger of lo[i] and hi[3 - i] are the four largest, a bitonic sequence
-#pragma unroll
-    for (int i = 0; i < 4; ++i) lo[i] = max(lo[i], hi[3 - i]);
-    order(lo[0], lo[2]);
-    order(lo[1], lo[3]);
-    order(lo[0], lo[1]);
-    order(lo[2], lo[3]);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) top[i] = lo[i];
-}
-
-// A lane's `count` largest keys are taken, the last of them `last`: their bits
-// (equal keys: the lower index first); they leave the keys.
-template <int E>
-__device__ __forceinline__ uint32_t take(uint32_t (&key)[E], int count, uint32_t last) {
-  uint32_t bits = 0;
-  int equal = count;
-#pragma unroll
-  for (int s = 0; s < E; ++s) equal -= count > 0 && key[s] > last ? 1 : 0;
-#pragma unroll
-  for (int s = 0; s < E; ++s) {
-    const bool eq = key[s] == last && equal > 0;
-    const bool hit = count > 0 && (key[s] > last || eq);
-    equal -= eq ? 1 : 0;
-    bits |= hit ? 1u << s : 0u;
-    key[s] = hit ? 0u : key[s];
-  }
-  return bits;
-}
-
-// E consecutive experts a lane; groups of whole lanes, a power of two of them.
-template <int E>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
-    const float* __restrict__ logits, const float* __restrict__ bias, int T, int N, int k, int sigmoids, int groups,
-    int top_groups, int top2, int renormalize, float scale, int32_t* __restrict__ idx_out,
-    float* __restrict__ gate_out) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long t = (long long)blockIdx.x * kRouteWarps + warp;
+__device__ __forceinline__ void scores_of(float (&sc)[E], int sigmoids) {
   constexpr uint32_t kAll = 0xffffffffu;
-  const bool in = lane * E < N;   // N % E == 0: a lane's experts exist or do not together
-  pdl_wait();
-  pdl_trigger();
-  if (t >= T) return;
-  float sc[E];
-  uint32_t key[E];
-#pragma unroll
-  for (int q = 0; q < E / 4; ++q) {
-    const float4 v = in ? __ldcs(reinterpret_cast<const float4*>(logits + t * N + lane * E) + q)
-                        : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    sc[4 * q] = v.x;
-    sc[4 * q + 1] = v.y;
-    sc[4 * q + 2] = v.z;
-    sc[4 * q + 3] = v.w;
-  }
   if (sigmoids) {
 #pragma unroll
     for (int s = 0; s < E; ++s) sc[s] = sigmoid(sc[s]);
-  } else {
-    float m = sc[0];
-#pragma unroll
-    for (int s = 1; s < E; ++s) m = fmaxf(m, sc[s]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
-    if (m == -INFINITY) m = 0.0f;   // every logit is -inf (or NaN): scores 0 (NaN)
-    float sum = 0.0f;
-#pragma unroll
-    for (int s = 0; s < E; ++s) {
-      sc[s] = expf(sc[s] - m);
-      sum += sc[s];
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
-    const float inv = sum == 0.0f ? 1.0f : 1.0f / sum;
-#pragma unroll
-    for (int s = 0; s < E; ++s) sc[s] *= inv;
+    return;
   }
-  if (bias && in) {
+  float m = sc[0];
 #pragma unroll
-    for (int q = 0; q < E / 4; ++q) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(bias + lane * E) + q);
-      key[4 * q] = key_of(sc[4 * q] + v.x);
-      key[4 * q + 1] = key_of(sc[4 * q + 1] + v.y);
-      key[4 * q + 2] = key_of(sc[4 * q + 2] + v.z);
-      key[4 * q + 3] = key_of(sc[4 * q + 3] + v.w);
-    }
-  } else {
+  for (int s = 1; s < E; ++s) m = fmaxf(m, sc[s]);
 #pragma unroll
-    for (int s = 0; s < E; ++s) key[s] = in ? key_of(sc[s]) : 0u;
-  }
-  uint32_t top[4];
-  best_four<E>(key, top);
-
-  if (groups > 1) {
-    const int lanes = N / groups / E;   // of one group
-    uint32_t a = top[0], b = top[1];
-    for (int off = 1; off < lanes; off <<= 1) {
-      const uint32_t oa = __shfl_xor_sync(kAll, a, off), ob = __shfl_xor_sync(kAll, b, off);
-      b = max(min(a, oa), max(b, ob));
-      a = max(a, oa);
-    }
-    const uint32_t gkey = top2 ? key_of(value_of(a) + value_of(b)) : a;
-    const int mine = lane / lanes;
-    int better = 0;
-    for (int g = 0; g < groups; ++g) {
-      const uint32_t o = __shfl_sync(kAll, gkey, g * lanes);
-      better += (o > gkey || (o == gkey && g < mine)) ? 1 : 0;
-    }
-    if (better >= top_groups) {
-#pragma unroll
-      for (int s = 0; s < E; ++s) key[s] = 0u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top[i] = 0u;
-    }
-  }
-
-  uint32_t chosen = 0, last = 0;   // bit s: expert lane * E + s is selected
-  int count = 0;
-  for (int j = 0; j < k; ++j) {
-    const uint32_t best = __reduce_max_sync(kAll, top[0]);
-    const unsigned who = __ballot_sync(kAll, top[0] == best);
-    if (lane == __ffs(who) - 1) {   // the lowest lane: the lowest expert of equal keys
-      ++count;
-      last = best;
-      top[0] = top[1];
-      top[1] = top[2];
-      top[2] = top[3];
-      top[3] = 0u;
-    }
-    if (E > 4 && __any_sync(kAll, count == 4)) {   // a lane's list has run out: its next four
-      if (count == 4) {
-        chosen |= take<E>(key, count, last);
-        best_four<E>(key, top);
-        count = 0;
-      }
-    }
-  }
-  chosen |= take<E>(key, count, last);
-
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
+  if (m == -INFINITY) m = 0.0f;   // every logit is -inf (or NaN): scores 0 (NaN)
   float sum = 0.0f;
-  if (renormalize) {
-#pragma unroll
-    for (int s = 0; s < E; ++s) sum += (chosen >> s) & 1u ? sc[s] : 0.0f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
-  }
-  const float factor = renormalize ? scale / (sum + 1e-20f) : scale;
-  // slots: the selected experts of lower lanes come first
-  const int n = __popc(chosen);
-  int base = 0;
-#pragma unroll
-  for (int bit = 0; bit < 4; ++bit)
-    base += __popc(__ballot_sync(kAll, (n >> bit) & 1) & ((1u << lane) - 1u)) << bit;
-  int32_t* io = idx_out + t * k + base;
-  float* go = gate_out + t * k + base;
 #pragma unroll
   for (int s = 0; s < E; ++s) {
-    if ((chosen >> s) & 1u) {
-      *io++ = lane * E + s;
-      *go++ = sc[s] * factor;
-    }
+    sc[s] = expf(sc[s] - m);
+    sum += sc[s];
   }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
+  const float inv = sum == 0.0f ? 1.0f : 1.0f / sum;
+#pragma unroll
+  for (int s = 0; s < E; ++s) sc[s] *= inv;
 }
 
-__global__ void __launch_bounds__(32 * kRouteWarps) route_scored_kernel(
-    const float* __restrict__ logits, const float* __restrict__ bias, int T, int N, int k, int sigmoids, int groups,
-    int top_groups, int top2, int renormalize, float scale, int32_t* __restrict__ idx_out,
-    float* __restrict__ gate_out) {
-  __shared__ uint32_t s_key[kRouteWarps][32 * kSlots];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long t = (long long)blockIdx.x * kRouteWarps + warp;
-  pdl_wait();
-  pdl_trigger();
-  if (t >= T) return;
+// One token by a warp, experts lane + 32 s, any groups and any values.
+// s_key: 256 words of the warp.
+__device__ __noinline__ void route_row(const float* __restrict__ row, const float* __restrict__ bias, int N, int k,
+                                       int sigmoids, int groups, int top_groups, int top2, int renormalize,
+                                       float scale, uint32_t* s_key, int32_t* __restrict__ idx_out,
+                                       float* __restrict__ gate_out) {
+  const int lane = threadIdx.x & 31;
   constexpr uint32_t kAll = 0xffffffffu;
-  const float* row = logits + t * N;
   float sc[kSlots];
   uint32_t key[kSlots];
 #pragma unroll
   for (int s = 0; s < kSlots; ++s) sc[s] = lane + 32 * s < N ? __ldg(row + lane + 32 * s) : -INFINITY;
-  if (sigmoids) {
-#pragma unroll
-    for (int s = 0; s < kSlots; ++s) sc[s] = sigmoid(sc[s]);
-  } else {
-    float m = sc[0];
-#pragma unroll
-    for (int s = 1; s < kSlots; ++s) m = fmaxf(m, sc[s]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
-    if (m == -INFINITY) m = 0.0f;   // every logit is -inf (or NaN): scores 0 (NaN)
-    float sum = 0.0f;
-#pragma unroll
-    for (int s = 0; s < kSlots; ++s) {
-      sc[s] = expf(sc[s] - m);
-      sum += sc[s];
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
-    if (sum == 0.0f) sum = 1.0f;
-#pragma unroll
-    for (int s = 0; s < kSlots; ++s) sc[s] = sc[s] / sum;
-  }
+  scores_of<kSlots>(sc, sigmoids);
 #pragma unroll
   for (int s = 0; s < kSlots; ++s) {
     const int e = lane + 32 * s;
@@ -282,13 +101,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scored_kernel(
     // lane g: the two best of group g, then its rank among the groups
     const int size = N / groups;
 #pragma unroll
-    for (int s = 0; s < kSlots; ++s) s_key[warp][lane + 32 * s] = key[s];
+    for (int s = 0; s < kSlots; ++s) s_key[lane + 32 * s] = key[s];
     __syncwarp();
     uint32_t gkey = 0;
     if (lane < groups) {
       uint32_t a = 0, b = 0;
       for (int i = 0; i < size; ++i) {
-        const uint32_t q = s_key[warp][lane * size + i];
+        const uint32_t q = s_key[lane * size + i];
         b = max(b, min(a, q));
         a = max(a, q);
       }
@@ -343,11 +162,205 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scored_kernel(
   for (int s = 0; s < kSlots; ++s) {
     if ((chosen >> s) & 1u) {
       const int slot = base + __popc(mask[s] & ((1u << lane) - 1u));
-      idx_out[t * k + slot] = lane + 32 * s;
-      gate_out[t * k + slot] = scale * (sc[s] / div);
+      idx_out[slot] = lane + 32 * s;
+      gate_out[slot] = scale * (sc[s] / div);
     }
     base += __popc(mask[s]);
   }
+}
+
+__device__ __forceinline__ void order(float& a, float& b) {   // a >= b
+  const float x = fmaxf(a, b);
+  b = fminf(a, b);
+  a = x;
+}
+__device__ __forceinline__ void sort4(float& a, float& b, float& c, float& d) {
+  order(a, b);
+  order(c, d);
+  order(a, c);
+  order(b, d);
+  order(b, c);
+}
+
+// The four largest of a lane's E values, descending.
+template <int E>
+__device__ __forceinline__ void best_four(const float (&v)[E], float (&top)[4]) {
+  float lo[4] = {v[0], v[1], v[2], v[3]};
+  sort4(lo[0], lo[1], lo[2], lo[3]);
+  if (E == 8) {
+    float hi[4] = {v[E - 4], v[E - 3], v[E - 2], v[E - 1]};
+    sort4(hi[0], hi[1], hi[2], hi[3]);
+    // the larger of lo[i] and hi[3 - i] are the four largest, a bitonic sequence
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lo[i] = fmaxf(lo[i], hi[3 - i]);
+    order(lo[0], lo[2]);
+    order(lo[1], lo[3]);
+    order(lo[0], lo[1]);
+    order(lo[2], lo[3]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top[i] = lo[i];
+}
+
+// Bits of a lane's `count` largest values, the last of them `last` (equal
+// values: the lower index first); +inf and 0: none.
+template <int E>
+__device__ __forceinline__ uint32_t taken(const float (&v)[E], int count, float last) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int s = 0; s < E; ++s) bits |= v[s] >= last ? 1u << s : 0u;
+  if (__any_sync(0xffffffffu, __popc(bits) != count)) {   // more equal values than taken
+    int equal = count;
+#pragma unroll
+    for (int s = 0; s < E; ++s) equal -= v[s] > last ? 1 : 0;
+#pragma unroll
+    for (int s = 0; s < E; ++s) {
+      if (v[s] == last && --equal < 0) bits &= ~(1u << s);
+    }
+  }
+  return bits;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// E consecutive experts a lane; groups of whole lanes, a power of two of them.
+// Finite values alone: a row with an infinite or NaN value is left to
+// route_row, which ranks every float.
+template <int E>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
+    const float* __restrict__ logits, const float* __restrict__ bias, int T, int N, int k, int sigmoids, int groups,
+    int top_groups, int top2, int renormalize, float scale, int32_t* __restrict__ idx_out,
+    float* __restrict__ gate_out) {
+  __shared__ uint32_t s_key[kRouteWarps][32 * kSlots];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long t = (long long)blockIdx.x * kRouteWarps + warp;
+  constexpr uint32_t kAll = 0xffffffffu;
+  const bool in = lane * E < N;   // N % E == 0: a lane's experts exist or do not together
+  pdl_wait();
+  pdl_trigger();
+  if (t >= T) return;
+  float sc[E], b[E];
+#pragma unroll
+  for (int q = 0; q < E / 4; ++q) {
+    const float4 v = in ? __ldcs(reinterpret_cast<const float4*>(logits + t * N + lane * E) + q)
+                        : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    sc[4 * q] = v.x;
+    sc[4 * q + 1] = v.y;
+    sc[4 * q + 2] = v.z;
+    sc[4 * q + 3] = v.w;
+  }
+  scores_of<E>(sc, sigmoids);
+#pragma unroll
+  for (int q = 0; q < E / 4; ++q) {
+    const float4 v = bias && in ? __ldg(reinterpret_cast<const float4*>(bias + lane * E) + q)
+                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    b[4 * q] = sc[4 * q] + v.x;
+    b[4 * q + 1] = sc[4 * q + 1] + v.y;
+    b[4 * q + 2] = sc[4 * q + 2] + v.z;
+    b[4 * q + 3] = sc[4 * q + 3] + v.w;
+  }
+  float check = 0.0f;
+#pragma unroll
+  for (int s = 0; s < E; ++s) check += fabsf(b[s]);
+  if (__any_sync(kAll, !(check < INFINITY))) {
+    route_row(logits + t * N, bias, N, k, sigmoids, groups, top_groups, top2, renormalize, scale, s_key[warp],
+              idx_out + t * k, gate_out + t * k);
+    return;
+  }
+  float top[4];
+  best_four<E>(b, top);
+  if (!in) top[0] = top[1] = top[2] = top[3] = -INFINITY;
+
+  if (groups > 1) {
+    const int lanes = N / groups / E;   // of one group
+    float x = top[0], y = top[1];
+    for (int off = 1; off < lanes; off <<= 1) {
+      const float ox = __shfl_xor_sync(kAll, x, off), oy = __shfl_xor_sync(kAll, y, off);
+      y = fmaxf(fminf(x, ox), fmaxf(y, oy));
+      x = fmaxf(x, ox);
+    }
+    // the group's rank: its lanes share the comparisons with the other groups
+    const float mine = top2 ? x + y : x;
+    const int group = lane / lanes;
+    int better = 0;
+    for (int g0 = 0; g0 < groups; g0 += lanes) {
+      const int g = g0 + lane % lanes;
+      const float o = __shfl_sync(kAll, mine, g * lanes & 31);
+      better += g < groups && (o > mine || (o == mine && g < group)) ? 1 : 0;
+    }
+    for (int off = 1; off < lanes; off <<= 1) better += __shfl_xor_sync(kAll, better, off);
+    if (better >= top_groups) top[0] = top[1] = top[2] = top[3] = -INFINITY;
+  }
+
+  uint32_t chosen = 0;          // bit s: expert lane * E + s is selected
+  float last = INFINITY;        // the last value this lane gave up
+  int count = 0;
+  const uint32_t below = (1u << lane) - 1u;
+  for (int j = 0; j < k; ++j) {
+    const float best = warp_max(top[0]);
+    const bool eq = top[0] == best;
+    const unsigned who = __ballot_sync(kAll, eq);
+    if (eq && (who & below) == 0u) {   // the lowest lane: the lowest expert of equal values
+      ++count;
+      last = best;
+      top[0] = top[1];
+      top[1] = top[2];
+      top[2] = top[3];
+      top[3] = -INFINITY;
+    }
+    if (E > 4 && j >= 3 && __any_sync(kAll, count == 4)) {
+      // a lane's list has run out: what it gave leaves its values, and the next four come
+      const bool mine = count == 4;
+      const uint32_t bits = taken<E>(b, mine ? 4 : 0, mine ? last : INFINITY);
+      chosen |= bits;
+#pragma unroll
+      for (int s = 0; s < E; ++s) b[s] = (bits >> s) & 1u ? -INFINITY : b[s];
+      if (mine) {
+        best_four<E>(b, top);
+        count = 0;
+        last = INFINITY;
+      }
+    }
+  }
+  chosen |= taken<E>(b, count, last);
+
+  // slots: the selected experts of lower lanes come first
+  const int n = __popc(chosen);
+  int slot = 0;
+#pragma unroll
+  for (int bit = 0; bit < 4; ++bit) slot += __popc(__ballot_sync(kAll, (n >> bit) & 1) & below) << bit;
+  uint2* out = reinterpret_cast<uint2*>(s_key[warp]) + slot;   // k <= 16 slots
+#pragma unroll
+  for (int s = 0; s < E; ++s)
+    if ((chosen >> s) & 1u) *out++ = make_uint2(lane * E + s, __float_as_uint(sc[s]));
+  __syncwarp();
+  const uint2 mine = lane < k ? reinterpret_cast<const uint2*>(s_key[warp])[lane] : make_uint2(0, 0);
+  float gate = __uint_as_float(mine.y), sum = gate;
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);   // the 16 slots
+  gate = scale * (renormalize ? gate / (sum + 1e-20f) : gate);
+  if (lane < k) {
+    idx_out[t * k + lane] = (int32_t)mine.x;
+    gate_out[t * k + lane] = gate;
+  }
+}
+
+__global__ void __launch_bounds__(32 * kRouteWarps) route_scored_kernel(
+    const float* __restrict__ logits, const float* __restrict__ bias, int T, int N, int k, int sigmoids, int groups,
+    int top_groups, int top2, int renormalize, float scale, int32_t* __restrict__ idx_out,
+    float* __restrict__ gate_out) {
+  __shared__ uint32_t s_key[kRouteWarps][32 * kSlots];
+  const int warp = threadIdx.x >> 5;
+  const long long t = (long long)blockIdx.x * kRouteWarps + warp;
+  pdl_wait();
+  pdl_trigger();
+  if (t >= T) return;
+  route_row(logits + t * N, bias, N, k, sigmoids, groups, top_groups, top2, renormalize, scale, s_key[warp],
+            idx_out + t * k, gate_out + t * k);
 }
 
 }  // namespace
