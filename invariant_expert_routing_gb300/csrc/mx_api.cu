@@ -141,11 +141,11 @@ bool map_scales(CUtensorMap* m, const void* base, uint64_t chunks) {
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, base, 2, dims, strides, box);
 }
 
-// bf16 output rows, 32 rows x 64 columns a box.
+// bf16 output rows, 32 rows x 32 columns a box.
 bool map_out(CUtensorMap* m, const void* base, uint64_t H, uint64_t rows) {
   const cuuint64_t dims[2] = {H, rows}, strides[1] = {2 * H};
-  const cuuint32_t box[2] = {64, 32};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, base, 2, dims, strides, box);
+  const cuuint32_t box[2] = {32, 32};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_64B, base, 2, dims, strides, box);
 }
 
 bool map_rows(CUtensorMap* m, const void* base, int K, uint64_t rows, uint32_t box_rows) {
@@ -156,12 +156,13 @@ bool map_rows(CUtensorMap* m, const void* base, int K, uint64_t rows, uint32_t b
 }
 
 // W13 [N, 2I, K/2]: (byte, row of a 32-feature block, gate/up, block, expert),
-// so that one box holds 32 gate and the same 32 up rows in turns.
+// so that one box holds 32 gate and the same 32 up rows in turns (box_rows 32:
+// one such run).
 bool map_w13(CUtensorMap* m, const void* base, int K, int I, int N, int box_rows) {
   const cuuint64_t pitch = (cuuint64_t)K / 2;
   const cuuint64_t dims[5] = {pitch, 32, 2, (cuuint64_t)I / 32, (cuuint64_t)N};
   const cuuint64_t strides[4] = {pitch, pitch * I, pitch * 32, pitch * 2 * I};
-  const cuuint32_t box[5] = {128, 32, 2, (cuuint32_t)box_rows / 64, 1};
+  const cuuint32_t box[5] = {128, 32, box_rows == 32 ? 1u : 2u, box_rows == 32 ? 1u : (cuuint32_t)box_rows / 64, 1};
   return encode_codes(m, base, 5, dims, strides, box);
 }
 
@@ -189,7 +190,7 @@ moe_status gemms(const moe_config* c, int H, int I, int N, const uint8_t* x, con
   const uint64_t sf_tiles = (uint64_t)max_tiles * (tile_rows / moe::kMxTileRows);
   moe::MxMaps m13, m2;
   // a CTA of a pair loads half of the weight rows of an item
-  if (!map_w13(&m13.w, w13, H, I, N, pair ? f13 / 2 : f13) || !map_rows(&m13.x, x, H, x_rows, 128) ||
+  if (!map_w13(&m13.w, w13, H, I, N, pair ? 32 : f13) || !map_rows(&m13.x, x, H, x_rows, 128) ||
       !map_rows(&m13.x_small, x, H, x_rows, 32) || !map_w2(&m2.w, w2, I, H, N, pair ? f2 / 2 : f2) ||
       !map_rows(&m2.x, a, I, a_rows, 128) || !map_rows(&m2.x_small, a, I, a_rows, 32))
     return MOE_ERR_CUDA;

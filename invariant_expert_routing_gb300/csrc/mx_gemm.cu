@@ -14,15 +14,17 @@
 // and columns of an MMA are independent sums, so a token's row does not
 // depend on the batch or on the column width of the work item.
 //
-// Persistent kernel, one CTA per SM, 10 warps:
+// Persistent kernel, one CTA per SM:
 //   warp 0      TMA producer: codes (tensor maps) and scales (512-byte chunks)
-//   warp 1      TMEM allocation; one thread copies the stage's scales into
-//               TMEM (tcgen05.cp) and issues the MMAs
-//   warps 2..9  epilogue (two warps per TMEM lane quarter)
+//   warp 1      TMEM allocation; copies the stage's scales into TMEM
+//               (tcgen05.cp) and issues the MMAs
+//   warp 2      scheduler: looks the work items up ahead of the others
+//   warps 4..11 epilogue (two warps per TMEM lane quarter)
 // Each stage has TMEM columns of its own for its scales: they are rewritten
 // only after the commit of the MMAs that read them released the stage.
 #include <cuda_bf16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "kernels.h"
 #include "mx.cuh"
@@ -36,7 +38,8 @@ namespace {
 using namespace mx;
 
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = (2 + kEpiWarps) * 32;
+constexpr int kRoleWarps = 4;                        // producer, MMA issuer, scheduler, none: the epilogue starts at a lane quarter of 0
+constexpr int kThreads = (kRoleWarps + kEpiWarps) * 32;
 constexpr int kStageK = 256;                         // elements of K per stage: one 128-byte row
 constexpr int kSmallRows = 32;                       // token box of a tile with at most 32 routed rows
 constexpr uint32_t kSmemBudget = 226 * 1024;
@@ -100,14 +103,13 @@ __device__ __forceinline__ Item item_of(const MxGemmArgs& a, int item, int num_t
   return w;
 }
 
-__device__ __forceinline__ Item uniform_item(Item w) {
-  w.f = uniform(w.f);
-  w.tile = uniform(w.tile);
-  w.expert = uniform(w.expert);
-  w.row0 = uniform(w.row0);
-  w.valid = uniform(w.valid);
-  return w;
-}
+// Items reach the warps of a CTA through a ring in shared memory, filled by a
+// warp of its own: looking one up takes two dependent loads and five
+// divisions (about 2000 cycles), as long as the MMAs of a short tile.
+constexpr int kRing = 4;
+struct RingSlot {
+  int more, f, tile, expert, row0, valid, pad[2];
+};
 
 // Waits of a converged warp (every lane polls): false as soon as one lane gave up.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit) {
@@ -116,6 +118,56 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort,
                                                   uint64_t limit) {
   return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort, limit));
+}
+
+// The scheduler warp (lane 0): items first, first + step, ... below total, then
+// a slot without one.
+template <int kRows>
+__device__ __forceinline__ void schedule(const MxGemmArgs& args, RingSlot* ring, uint32_t ifull0, uint32_t iempty0,
+                                         int first, int step, int total, int num_tiles, int nf, volatile int* abort,
+                                         uint64_t limit) {
+  int item = first;
+  for (int n = 0;; ++n, item += step) {
+    const int slot = n % kRing;
+    RingSlot v{};
+    if (item < total) {
+      const Item w = item_of<kRows>(args, item, num_tiles, nf);
+      v.more = 1;
+      v.f = w.f;
+      v.tile = w.tile;
+      v.expert = w.expert;
+      v.row0 = w.row0;
+      v.valid = w.valid;
+    }
+    if (!mbar_wait(iempty0 + 8 * slot, ((uint32_t)(n / kRing) & 1u) ^ 1u, abort, limit)) {
+      *abort = 1;
+      atomicOr(args.status, kDevErrTimeout);
+      return;
+    }
+    ring[slot] = v;
+    mbar_arrive(ifull0 + 8 * slot);
+    if (!v.more) return;
+  }
+}
+
+// The n-th item, for a converged warp; false when there is none or a wait
+// gave up (then *ok is false).
+__device__ __forceinline__ bool next_item(const RingSlot* ring, uint32_t ifull0, uint32_t iempty0, int n, Item& w,
+                                          bool& ok, volatile int* abort, uint64_t limit) {
+  const int slot = n % kRing;
+  if (!warp_wait(ifull0 + 8 * slot, (uint32_t)(n / kRing) & 1u, abort, limit)) {
+    ok = false;
+    return false;
+  }
+  const RingSlot v = ring[slot];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(iempty0 + 8 * slot);
+  w.f = uniform(v.f);
+  w.tile = uniform(v.tile);
+  w.expert = uniform(v.expert);
+  w.row0 = uniform(v.row0);
+  w.valid = uniform(v.valid);
+  return uniform(v.more) != 0;
 }
 
 // a = silu(g) * u of 32 neighbouring features of one token, quantised:
@@ -167,6 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem_base;
   __shared__ volatile int s_abort;
+  __shared__ __align__(8) uint64_t s_ibar[2 * kRing];   // the ring's full, then empty barriers
+  __shared__ __align__(16) RingSlot s_ring[kRing];
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t full0 = smem_u32(smem + C::kStages * C::kStageBytes);
@@ -174,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tfull0 = empty0 + 8 * C::kStages;
   const uint32_t tempty0 = tfull0 + 16;
   const uint32_t drain = tempty0 + 16;
+  const uint32_t ifull0 = smem_u32(s_ibar), iempty0 = ifull0 + 8 * kRing;
 
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const int kchunks = args.K / kSfChunkK;
@@ -191,6 +246,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(tempty0 + 8 * b, kEpiWarps);
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(ifull0 + 8 * i, 1);
+      mbar_init(iempty0 + 8 * i, 2 + kEpiWarps);
+    }
     s_abort = 0;
     fence_mbar_init();
   }
@@ -222,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     int armed = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-      const Item w = uniform_item(item_of(args, item, num_tiles, nf));
+    Item w;
+    for (int n = 0; ok && next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim); ++n) {
       const bool small = w.valid <= kSmallRows;
       const uint32_t a_tx = (small ? kSmallRows : kMxTileRows) * 128u;
       // scale tiles of B that exist (the last item of an odd number of 128-row tiles has one)
@@ -293,50 +352,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t fbdesc0 = sdesc_scales(s0 + C::kABytes + C::kBBytes + C::kSfaBytes);
     constexpr uint32_t kI0 = idesc_mxf4(kMxTileRows, BN, 0), kI1 = idesc_mxf4(kMxTileRows, BN, 1);
     uint32_t soff = 0;
-    for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+    bool ready = false;   // peeked a stage ahead
+    Item w;
+    for (int n = 0; ok && next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim); ++n) {
       // an item narrower than a scale tile takes its columns of it
-      const int f = (BN < kSfRows) ? uniform(item_of(args, item, num_tiles, nf).f) : 0;
-      const uint32_t sfb_skip = (BN < kSfRows) ? (uint32_t)(f * BN % kSfRows) / 32u : 0u;
+      const uint32_t sfb_skip = (BN < kSfRows) ? (uint32_t)(w.f * BN % kSfRows) / 32u : 0u;
       if (!warp_wait(tempty0 + 8 * acc, acc_phase ^ 1u, &s_abort, wlim)) {
         ok = false;
         break;
       }
-      tc_fence_after();
       const uint32_t d0 = tmem + acc * BN;
-      for (int ks = 0; ks < ksteps; ++ks) {
-        if (!warp_wait(full0 + 8 * stage, phase, &s_abort, wlim)) {
-          ok = false;
-          break;
-        }
+      // one stage: chunks of 128 elements, for each the scales (A's in columns
+      // ta + 4c, those of B's tile t in tb + (c kSfbTiles + t) 4), then two MMAs
+      auto step = [&](auto two, bool first, bool last) -> bool {
+        if (!__all_sync(0xffffffffu, ready) && !warp_wait(full0 + 8 * stage, phase, &s_abort, wlim)) return false;
         tc_fence_after();
         const uint32_t ta = tmem + C::kSfCol0 + stage * C::kSfCols, tb = ta + 8;
         const uint64_t ad = adesc0 + soff, bd = bdesc0 + soff, fa = fadesc0 + soff, fbd = fbdesc0 + soff;
-        // chunk c of 128 elements: scales (A's in columns ta + 4c, those of
-        // B's tile t in tb + (c kSfbTiles + t) 4), then two MMAs
-        auto scales = [&](int c) {
-          cp_scales(ta + 4 * c, fa + c * kSfUnits);
-#pragma unroll
-          for (int t = 0; t < C::kSfbTiles; ++t)
-            cp_scales(tb + 4 * (c * C::kSfbTiles + t), fbd + (2 * t + c) * kSfUnits);
-        };
-        auto mmas = [&](int c, uint32_t accumulate) {
-          const uint32_t sb = tb + 4 * c * C::kSfbTiles + sfb_skip;
-          mma_mxf4(d0, ad + 4 * c, bd + 4 * c, kI0, ta + 4 * c, sb, accumulate);
-          mma_mxf4(d0, ad + 4 * c + 2, bd + 4 * c + 2, kI1, ta + 4 * c, sb, 1u);
-        };
-        if (elect_one()) {
-          scales(0);
-          if (2 * ks + 1 < kchunks) {
-            scales(1);
-            mmas(0, ks != 0 ? 1u : 0u);
-            mmas(1, 1u);
-          } else {
-            mmas(0, ks != 0 ? 1u : 0u);
-          }
-          mma_commit(empty0 + 8 * stage);
-          if (ks == ksteps - 1) mma_commit(tfull0 + 8 * acc);
-        }
-        __syncwarp();
+        const uint32_t done = empty0 + 8 * stage;
         if (++stage == C::kStages) {
           stage = 0;
           phase ^= 1u;
@@ -344,7 +377,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           soff += C::kStageBytes >> 4;
         }
-      }
+        ready = mbar_test(full0 + 8 * stage, phase);
+        if (elect_one()) {
+          constexpr int kChunks = decltype(two)::value ? 2 : 1;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            cp_scales(ta + 4 * c, fa + c * kSfUnits);
+#pragma unroll
+            for (int t = 0; t < C::kSfbTiles; ++t)
+              cp_scales(tb + 4 * (c * C::kSfbTiles + t), fbd + (2 * t + c) * kSfUnits);
+          }
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            const uint32_t sb = tb + 4 * c * C::kSfbTiles + sfb_skip;
+            mma_mxf4(d0, ad + 4 * c, bd + 4 * c, kI0, ta + 4 * c, sb, (c > 0 || !first) ? 1u : 0u);
+            mma_mxf4(d0, ad + 4 * c + 2, bd + 4 * c + 2, kI1, ta + 4 * c, sb, 1u);
+          }
+          mma_commit(done);
+          if (last) mma_commit(tfull0 + 8 * acc);
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int ks = 0; ok && ks < kchunks / 2; ++ks) ok = step(std::true_type{}, ks == 0, 2 * ks + 2 == kchunks);
+      if (ok && (kchunks & 1)) ok = step(std::false_type{}, kchunks == 1, true);
       if (++acc == C::kNumAcc) {
         acc = 0;
         acc_phase ^= 1u;
@@ -360,17 +416,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int no_abort = 0;
     mbar_wait(drain, 0, &no_abort);
     __syncwarp();
+  } else if (warp < kRoleWarps) {
+    // ------------------------------------------------------------ scheduler
+    if (warp == 2 && lane == 0)
+      schedule<kMxTileRows>(args, s_ring, ifull0, iempty0, blockIdx.x, gridDim.x, total, num_tiles, nf, &s_abort, wlim);
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;              // TMEM lanes this warp may access
-    const int half = (warp - 2) / 4;           // which blocks of columns
+    const int half = (warp - kRoleWarps) / 4;  // which blocks of columns
     const int r = quarter * 32 + lane;         // token row of the tile
     constexpr int kBlockCols = kW13 ? 64 : 32; // columns of one block (W13: 32 gate, 32 up)
     constexpr int kBlocks = BN / kBlockCols;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int item = blockIdx.x; item < total; item += gridDim.x) {
-      const Item w = item_of(args, item, num_tiles, nf);
+    Item w;
+    bool ok = true;
+    for (int n = 0; next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim); ++n) {
       int got = 1;
       if (lane == 0) got = mbar_wait(tfull0 + 8 * acc, acc_phase, &s_abort, wlim) ? 1 : 0;
       got = __shfl_sync(0xffffffffu, got, 0);
@@ -411,6 +473,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc_phase ^= 1u;
       }
     }
+    if (!ok) {
+      s_abort = 1;
+      if (lane == 0) atomicOr(args.status, kDevErrTimeout);
+    }
   }
 
   tc_fence_before();
@@ -421,21 +487,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ CTA pairs
 // The same GEMMs on pairs of CTAs (a cluster of two on two SMs, one
-// cta_group::2 MMA of 256 token rows x 256 weight rows): each CTA loads its
-// own 128 token rows and half of the weight rows, which halves the operand
-// bytes an SM reads per MMA (8 KB against 12 KB per 64 cycles, where shared
-// memory gives 128 bytes a cycle), and holds the result of its 128 rows.
+// cta_group::2 MMA of 256 token rows x 192 weight rows): each CTA loads its
+// own 128 token rows and half of the weight rows and holds the result of its
+// 128 rows.  192 columns, because two accumulators and the scale columns then
+// fit into TMEM: with 256 the accumulators have to share columns, and each
+// tile's first MMA waits for the last one's epilogue to begin (about 1800
+// cycles, where a tile of K = 768 has 1700 cycles of MMAs).
 //
-// TMEM (512 columns): the stages' scales (24 columns each) and two accumulators
-// of 256 columns that share what is missing, 120 of them.  The epilogue reads
-// the shared columns first; from then on the next tile's MMAs run beside the
-// rest of it.
+// TMEM (512 columns): accumulators at 0 and 192, five slots of scale columns
+// behind them.  Shared memory holds one stage more than there are slots: a
+// slot is rewritten once the commit of the step that used it last has arrived.
 //
-// W2 rows leave through shared memory as 32-row x 64-column tiled stores (a
-// lane's direct 16-byte stores touch one line per row); a lane quarter with
-// padding rows stores directly, so that padding is never written.
+// Twelve epilogue warps, one per lane quarter and 64-column block.  W2 rows
+// leave through shared memory as 32-row x 32-column tiled stores (a lane's
+// direct 16-byte stores touch one line per row); a lane quarter with padding
+// rows stores directly, so that padding is never written.
 constexpr int kPairRowsMx = 2 * kMxTileRows;
-constexpr int kPairN = 256;
+constexpr int kPairN = 192;
+constexpr int kPairEpiWarps = 12;
+constexpr int kPairThreads = (kRoleWarps + kPairEpiWarps) * 32;
+constexpr int kSfSlots = 5;
 
 template <bool kW13>
 struct PairCfgMx {
@@ -444,20 +515,19 @@ struct PairCfgMx {
   static constexpr uint32_t kSfaBytes = 2 * kSfChunkBytes;
   static constexpr uint32_t kSfbBytes = 2 * 2 * kSfChunkBytes;
   static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
-  static constexpr uint32_t kOutBytes = kW13 ? 0 : kEpiWarps * 32 * 128;
+  static constexpr uint32_t kOutBytes = kW13 ? 0 : kPairEpiWarps * 32 * 64;
   static constexpr uint32_t kBarBytes = 512;
-  static constexpr int kStages = 5;
+  static constexpr int kStages = kW13 ? 7 : 6;
   static constexpr uint32_t kSmemBytes = kStages * kStageBytes + kOutBytes + kBarBytes + 1024;
   static constexpr uint32_t kSfCols = 24;
-  static constexpr uint32_t kSfCol0 = 512 - kStages * kSfCols;
+  static constexpr uint32_t kSfCol0 = 2 * kPairN;
   static_assert(kSmemBytes <= kSmemBudget, "stages fit");
-  static constexpr uint32_t kAcc1 = kSfCol0 - kPairN;   // first column of the second accumulator
+  static_assert(kSfCol0 + kSfSlots * kSfCols <= 512, "accumulators and scales fit in TMEM");
   static_assert(kStageBytes % 1024 == 0, "stages stay aligned to the swizzle atom");
-  static_assert(kPairN - kAcc1 <= 128, "the shared columns lie in the blocks that the epilogue reads first");
 };
 
 template <bool kW13>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
                         const __grid_constant__ CUtensorMap sfa_map, const __grid_constant__ CUtensorMap sfb_map,
                         const __grid_constant__ CUtensorMap y_map, const MxGemmArgs args) {
@@ -465,6 +535,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem_base;
   __shared__ volatile int s_abort;
+  __shared__ __align__(8) uint64_t s_ibar[2 * kRing];   // the ring's full, then empty barriers
+  __shared__ __align__(16) RingSlot s_ring[kRing];
 
   const uint32_t rank = cluster_ctarank();   // 0: issues the MMAs
   const bool lead = rank == 0;
@@ -473,8 +545,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t full0 = smem_u32(s_out + C::kOutBytes);
   const uint32_t empty0 = full0 + 8 * C::kStages;
   const uint32_t tfull0 = empty0 + 8 * C::kStages;
-  const uint32_t tshare = tfull0 + 16;   // shared accumulator columns read
-  const uint32_t drain = tshare + 8;
+  const uint32_t tempty0 = tfull0 + 16;
+  const uint32_t drain = tempty0 + 16;
+  const uint32_t ifull0 = smem_u32(s_ibar), iempty0 = ifull0 + 8 * kRing;
 
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const int kchunks = args.K / kSfChunkK;
@@ -488,9 +561,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
     }
-    for (int b = 0; b < 2; ++b) mbar_init(tfull0 + 8 * b, 1);
-    mbar_init(tshare, 2 * kEpiWarps);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull0 + 8 * b, 1);
+      mbar_init(tempty0 + 8 * b, 2 * kPairEpiWarps);
+    }
     mbar_init(drain, 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(ifull0 + 8 * i, 1);
+      mbar_init(iempty0 + 8 * i, (lead ? 2 : 1) + kPairEpiWarps);
+    }
     s_abort = 0;
     fence_mbar_init();
   }
@@ -527,11 +606,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     int armed = 0;
     bool ok = true;
-    for (int item = pair0; item < total && ok; item += pairs) {
-      const Item w = uniform_item(item_of<kPairRowsMx>(args, item, num_tiles, nf));
+    Item w;
+    for (int n = 0; ok && next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim); ++n) {
       const int arow = w.row0 + me * kMxTileRows;
       const int sfa_row = (2 * w.tile + me) * kchunks;
-      const int sfb_row = (w.expert * (args.features / kSfRows) + 2 * w.f) * kchunks;
+      // the 128-row scale tiles that hold the item's rows (from the middle of
+      // the first one on for an odd item)
+      const int sfb_row = (w.expert * (args.features / kSfRows) + w.f * kPairN / kSfRows) * kchunks;
       for (int ks = 0; ks < ksteps; ++ks) {
         if (!warp_wait_cluster(empty0 + 8 * stage, phase ^ 1u, &s_abort, wlim)) {
           ok = false;
@@ -543,10 +624,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t fb = full_lead + 8 * stage;
         if (elect_one()) {
           if (lead) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * C::kStageBytes);
-          if (kW13)
-            tma_load_5d_pair(sB, &w_map, ks * 128, 0, 0, w.f * 4 + 2 * me, w.expert, fb, pol_w);
-          else
+          if (kW13) {
+            // 96 of the item's 192 rows: three runs of 32, gate and up in turns
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              const int run = 3 * me + i;
+              tma_load_5d_pair(sB + i * 32 * 128, &w_map, ks * 128, 0, run & 1, w.f * 3 + (run >> 1), w.expert, fb, pol_w);
+            }
+          } else {
             tma_load_3d_pair(sB, &w_map, ks * 128, w.f * kPairN + me * (kPairN / 2), w.expert, fb, pol_w);
+          }
           tma_load_2d_pair(sA, &x_map, ks * 128, arow, fb, pol_x);
           // scale chunks of this stage's 256 elements (a last odd chunk brings its
           // neighbour's along; the MMAs stop at K)
@@ -593,53 +680,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lead) {
       int stage = 0;
       uint32_t phase = 0;
+      int old = 0;                   // the stage of the step kSfSlots before the next one
+      uint32_t old_phase = 0;
+      int slot = 0, steps = 0;
       const uint32_t s0 = smem_u32(smem);
       const uint64_t adesc0 = sdesc_sw128(s0, 16, 1024), bdesc0 = sdesc_sw128(s0 + C::kABytes, 16, 1024);
       const uint64_t fadesc0 = sdesc_scales(s0 + C::kABytes + C::kBBytes);
       const uint64_t fbdesc0 = sdesc_scales(s0 + C::kABytes + C::kBBytes + C::kSfaBytes);
       constexpr uint32_t kI0 = idesc_mxf4(kPairRowsMx, kPairN, 0), kI1 = idesc_mxf4(kPairRowsMx, kPairN, 1);
       uint32_t soff = 0;
-      int n = 0;
       bool ok = true;
-      for (int item = pair0; item < total && ok; item += pairs, ++n) {
-        // the previous tile's shared columns are read (which implies that
-        // the tile before it, in this accumulator, is read altogether)
-        if (n > 0 && !warp_wait_cluster(tshare, (uint32_t)(n - 1) & 1u, &s_abort, wlim)) {
+      Item w;
+      // The next stage's barrier, and that of the step whose MMAs read the
+      // scale slot it will rewrite, are looked at while this stage's
+      // instructions are issued: the issue of a stage then stays below its 384
+      // cycles of MMAs (a wait in place costs about 80).
+      bool ready = false, slot_free = true;
+      for (int n = 0; ok && next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim); ++n) {
+        const int acc = n & 1;
+        const uint32_t sfb_skip = (uint32_t)(w.f * kPairN % kSfRows) / 32u;
+        if (!warp_wait_cluster(tempty0 + 8 * acc, ((uint32_t)(n >> 1) & 1u) ^ 1u, &s_abort, wlim)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        const uint32_t d0 = tmem + (n & 1) * C::kAcc1;
-        for (int ks = 0; ks < ksteps; ++ks) {
-          if (!warp_wait_cluster(full0 + 8 * stage, phase, &s_abort, wlim)) {
-            ok = false;
-            break;
+        const uint32_t d0 = tmem + acc * kPairN;
+        auto step = [&](auto two, bool first, bool last) -> bool {
+          if (!__all_sync(0xffffffffu, ready && slot_free)) {
+            if (!warp_wait_cluster(full0 + 8 * stage, phase, &s_abort, wlim)) return false;
+            if (steps >= kSfSlots && !warp_wait_cluster(empty0 + 8 * old, old_phase, &s_abort, wlim)) return false;
           }
           tc_fence_after();
-          const uint32_t ta = tmem + C::kSfCol0 + stage * C::kSfCols, tb = ta + 8;
+          const uint32_t ta = tmem + C::kSfCol0 + slot * C::kSfCols, tb = ta + 8;
           const uint64_t ad = adesc0 + soff, bd = bdesc0 + soff, fa = fadesc0 + soff, fbd = fbdesc0 + soff;
-          auto scales = [&](int c) {
-            cp_scales_pair(ta + 4 * c, fa + c * kSfUnits);
-            cp_scales_pair(tb + 8 * c, fbd + c * kSfUnits);
-            cp_scales_pair(tb + 8 * c + 4, fbd + (2 + c) * kSfUnits);
-          };
-          auto mmas = [&](int c, uint32_t accumulate) {
-            mma_mxf4_pair(d0, ad + 4 * c, bd + 4 * c, kI0, ta + 4 * c, tb + 8 * c, accumulate);
-            mma_mxf4_pair(d0, ad + 4 * c + 2, bd + 4 * c + 2, kI1, ta + 4 * c, tb + 8 * c, 1u);
-          };
-          if (elect_one()) {
-            scales(0);
-            if (2 * ks + 1 < kchunks) {
-              scales(1);
-              mmas(0, ks != 0 ? 1u : 0u);
-              mmas(1, 1u);
-            } else {
-              mmas(0, ks != 0 ? 1u : 0u);
-            }
-            mma_commit_pair(empty0 + 8 * stage, 0x3);
-            if (ks == ksteps - 1) mma_commit_pair(tfull0 + 8 * (n & 1), 0x3);
-          }
-          __syncwarp();
+          const uint32_t done = empty0 + 8 * stage;
+          if (++slot == kSfSlots) slot = 0;
           if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1u;
@@ -647,7 +721,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           } else {
             soff += C::kStageBytes >> 4;
           }
-        }
+          if (++steps > kSfSlots && ++old == C::kStages) {
+            old = 0;
+            old_phase ^= 1u;
+          }
+          ready = mbar_test(full0 + 8 * stage, phase);
+          if (steps >= kSfSlots) slot_free = mbar_test(empty0 + 8 * old, old_phase);
+          if (elect_one()) {
+            constexpr int kChunks = decltype(two)::value ? 2 : 1;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              cp_scales_pair(ta + 4 * c, fa + c * kSfUnits);
+              cp_scales_pair(tb + 8 * c, fbd + c * kSfUnits);
+              cp_scales_pair(tb + 8 * c + 4, fbd + (2 + c) * kSfUnits);
+            }
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              const uint32_t sb = tb + 8 * c + sfb_skip;
+              mma_mxf4_pair(d0, ad + 4 * c, bd + 4 * c, kI0, ta + 4 * c, sb, (c > 0 || !first) ? 1u : 0u);
+              mma_mxf4_pair(d0, ad + 4 * c + 2, bd + 4 * c + 2, kI1, ta + 4 * c, sb, 1u);
+            }
+            mma_commit_pair(done, 0x3);
+            if (last) mma_commit_pair(tfull0 + 8 * acc, 0x3);
+          }
+          __syncwarp();
+          return true;
+        };
+        for (int ks = 0; ok && ks < kchunks / 2; ++ks) ok = step(std::true_type{}, ks == 0, 2 * ks + 2 == kchunks);
+        if (ok && (kchunks & 1)) ok = step(std::false_type{}, kchunks == 1, true);
       }
       if (!ok) {
         s_abort = 1;
@@ -659,16 +760,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_wait(drain, 0, &no_abort);
     }
     __syncwarp();
+  } else if (warp < kRoleWarps) {
+    // ------------------------------------------------------------ scheduler (both CTAs)
+    if (warp == 2 && lane == 0)
+      schedule<kPairRowsMx>(args, s_ring, ifull0, iempty0, pair0, pairs, total, num_tiles, nf, &s_abort, wlim);
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int quarter = warp & 3;              // TMEM lanes this warp may access
-    const int half = (warp - 2) / 4;           // its 64-column blocks: half and half + 2
+    const int b = (warp - kRoleWarps) / 4;     // its 64-column block
     const int r = quarter * 32 + lane;         // token row of the CTA's 128
-    uint8_t* buf = s_out + (warp - 2) * (32 * 128);
+    uint8_t* buf = s_out + (warp - kRoleWarps) * (32 * 64);
     const uint32_t sbuf = smem_u32(buf);
-    int n = 0;
-    for (int item = pair0; item < total; item += pairs, ++n) {
-      const Item w = item_of<kPairRowsMx>(args, item, num_tiles, nf);
+    Item w;
+    bool ok = true;
+    for (int n = 0; next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim); ++n) {
       const int acc = n & 1;
       int got = 1;
       if (lane == 0) got = mbar_wait_cluster(tfull0 + 8 * acc, (uint32_t)(n >> 1) & 1u, &s_abort, wlim) ? 1 : 0;
@@ -681,57 +787,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t tbase = tmem + ((uint32_t)(quarter * 32) << 16) + acc * C::kAcc1;
+      const uint32_t tbase = tmem + ((uint32_t)(quarter * 32) << 16) + acc * kPairN + b * 64;
       const int valid = w.valid - (int)rank * kMxTileRows;       // of this CTA's rows
       const size_t row = (size_t)w.row0 + rank * kMxTileRows + r;
-      const bool work = quarter * 32 < valid;
-#pragma unroll 1
-      for (int i = 0; i < 2; ++i) {
-        // the shared columns are the last of accumulator 0 and the first of
-        // accumulator 1: the two blocks that the warps read first hold them
-        const int b = half + 2 * (acc == 0 ? 1 - i : i);
-        float p[32], q[32];
-        if (work) tmem_load32x2(tbase + b * 64, p, tbase + b * 64 + 32, q);
-        if (i == 0) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(mapa_shared(tshare, 0));
-        }
-        if (!work) continue;
-        if (kW13) {
-          const int feat = w.f * (kPairN / 2) + b * 32;
-          if (r < valid)
-            store_swiglu_block(p, q, args.out_codes + (row * args.out_ld + feat) / 2,
-                               args.out_sf +
-                                   ((size_t)(2 * w.tile + rank) * (args.out_ld / kSfChunkK) + feat / kSfChunkK) * kSfChunkBytes +
-                                   sf_row_offset(r) + (feat % kSfChunkK) / kBlock);
-        } else {
-          const int feat = w.f * kPairN + b * 64;
-          if (feat >= args.features) continue;
-          if (quarter * 32 + 32 <= valid) {
-            // 128 bytes a row in the 128-byte swizzle: 16-byte piece j of row l at j ^ (l & 7)
+      // weight rows past an expert's last (the last item of it) are not stored
+      const bool work = quarter * 32 < valid && w.f * kPairN + b * 64 < args.features;
+      float p[32], q[32];
+      if (work) tmem_load32x2(tbase, p, tbase + 32, q);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(mapa_shared(tempty0 + 8 * acc, 0));
+      if (!work) continue;
+      if (kW13) {
+        const int feat = w.f * (kPairN / 2) + b * 32;
+        if (r < valid)
+          store_swiglu_block(p, q, args.out_codes + (row * args.out_ld + feat) / 2,
+                             args.out_sf +
+                                 ((size_t)(2 * w.tile + rank) * (args.out_ld / kSfChunkK) + feat / kSfChunkK) * kSfChunkBytes +
+                                 sf_row_offset(r) + (feat % kSfChunkK) / kBlock);
+      } else {
+        const int feat = w.f * kPairN + b * 64;
+        if (quarter * 32 + 32 <= valid) {
+          // 64 bytes a row in the 64-byte swizzle: 16-byte piece j of row l at j ^ ((l >> 1) & 3)
+          auto store = [&](const float (&v)[32], int col) {
             if (lane == 0) tma_store_wait_read();
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 4; ++j) {
               uint32_t o[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const int c = (8 * j + 2 * e) & 31;
-                const __nv_bfloat162 v = j < 4 ? __floats2bfloat162_rn(p[c], p[c + 1]) : __floats2bfloat162_rn(q[c], q[c + 1]);
-                o[e] = *reinterpret_cast<const uint32_t*>(&v);
+                const __nv_bfloat162 x = __floats2bfloat162_rn(v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
+                o[e] = *reinterpret_cast<const uint32_t*>(&x);
               }
-              *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) tma_store_2d(&y_map, sbuf, feat, w.row0 + (int)rank * kMxTileRows + quarter * 32);
-          } else if (r < valid) {
-            store_bf16_block(p, args.out + row * args.out_ld + feat);
-            store_bf16_block(q, args.out + row * args.out_ld + feat + 32);
-          }
+            if (lane == 0) tma_store_2d(&y_map, sbuf, col, w.row0 + (int)rank * kMxTileRows + quarter * 32);
+          };
+          store(p, feat);
+          store(q, feat + 32);
+        } else if (r < valid) {
+          store_bf16_block(p, args.out + row * args.out_ld + feat);
+          store_bf16_block(q, args.out + row * args.out_ld + feat + 32);
         }
       }
+    }
+    if (!ok) {
+      s_abort = 1;
+      if (lane == 0) atomicOr(args.status, kDevErrTimeout);
     }
     if (!kW13 && lane == 0) tma_store_wait();
     __syncwarp();
@@ -754,7 +859,7 @@ int resident_pairs_mx(int sms) {
   int n = 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (unsigned)(sms / 2), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(kPairThreads, 1, 1);
   cfg.dynamicSmemBytes = PairCfgMx<kW13>::kSmemBytes;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -788,7 +893,7 @@ void launch_pair_mx(const MxMaps& m, MxGemmArgs a, int64_t max_tiles, int sms, c
   const int cap = resident_pairs_mx<kW13>(sms);
   const int pairs = (int)(items < cap ? items : cap);
   a.concurrent = pairs;
-  launch_pdl(kernel, dim3(2 * pairs), dim3(kThreads), smem, s, m.w, m.x, m.sfa, m.sfb, m.y, a);
+  launch_pdl(kernel, dim3(2 * pairs), dim3(kPairThreads), smem, s, m.w, m.x, m.sfa, m.sfb, m.y, a);
 }
 
 template <bool kW13, int BN>
