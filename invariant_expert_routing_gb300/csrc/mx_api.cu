@@ -141,11 +141,11 @@ bool map_scales(CUtensorMap* m, const void* base, uint64_t chunks) {
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, base, 2, dims, strides, box);
 }
 
-// bf16 output rows, 32 rows x 32 columns a box.
+// bf16 output rows, 32 rows x 64 columns a box.
 bool map_out(CUtensorMap* m, const void* base, uint64_t H, uint64_t rows) {
   const cuuint64_t dims[2] = {H, rows}, strides[1] = {2 * H};
-  const cuuint32_t box[2] = {32, 32};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_64B, base, 2, dims, strides, box);
+  const cuuint32_t box[2] = {64, 32};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, base, 2, dims, strides, box);
 }
 
 bool map_rows(CUtensorMap* m, const void* base, int K, uint64_t rows, uint32_t box_rows) {

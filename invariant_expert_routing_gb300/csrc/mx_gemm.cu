@@ -495,11 +495,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // cycles, where a tile of K = 768 has 1700 cycles of MMAs).
 //
 // TMEM (512 columns): accumulators at 0 and 192, five slots of scale columns
-// behind them.  Shared memory holds one stage more than there are slots: a
-// slot is rewritten once the commit of the step that used it last has arrived.
+// behind them.  W13's shared memory holds two stages more than there are slots:
+// a slot is rewritten once the commit of the step that used it last has arrived.
 //
 // Twelve epilogue warps, one per lane quarter and 64-column block.  W2 rows
-// leave through shared memory as 32-row x 32-column tiled stores (a lane's
+// leave through shared memory as 32-row x 64-column tiled stores (a lane's
 // direct 16-byte stores touch one line per row); a lane quarter with padding
 // rows stores directly, so that padding is never written.
 constexpr int kPairRowsMx = 2 * kMxTileRows;
@@ -515,9 +515,9 @@ struct PairCfgMx {
   static constexpr uint32_t kSfaBytes = 2 * kSfChunkBytes;
   static constexpr uint32_t kSfbBytes = 2 * 2 * kSfChunkBytes;
   static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
-  static constexpr uint32_t kOutBytes = kW13 ? 0 : kPairEpiWarps * 32 * 64;
+  static constexpr uint32_t kOutBytes = kW13 ? 0 : kPairEpiWarps * 32 * 128;
   static constexpr uint32_t kBarBytes = 512;
-  static constexpr int kStages = kW13 ? 7 : 6;
+  static constexpr int kStages = kW13 ? 7 : 5;
   static constexpr uint32_t kSmemBytes = kStages * kStageBytes + kOutBytes + kBarBytes + 1024;
   static constexpr uint32_t kSfCols = 24;
   static constexpr uint32_t kSfCol0 = 2 * kPairN;
@@ -707,7 +707,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         auto step = [&](auto two, bool first, bool last) -> bool {
           if (!__all_sync(0xffffffffu, ready && slot_free)) {
             if (!warp_wait_cluster(full0 + 8 * stage, phase, &s_abort, wlim)) return false;
-            if (steps >= kSfSlots && !warp_wait_cluster(empty0 + 8 * old, old_phase, &s_abort, wlim)) return false;
+            if (C::kStages > kSfSlots && steps >= kSfSlots && !warp_wait_cluster(empty0 + 8 * old, old_phase, &s_abort, wlim)) return false;
           }
           tc_fence_after();
           const uint32_t ta = tmem + C::kSfCol0 + slot * C::kSfCols, tb = ta + 8;
@@ -726,7 +726,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             old_phase ^= 1u;
           }
           ready = mbar_test(full0 + 8 * stage, phase);
-          if (steps >= kSfSlots) slot_free = mbar_test(empty0 + 8 * old, old_phase);
+          if (C::kStages > kSfSlots && steps >= kSfSlots) slot_free = mbar_test(empty0 + 8 * old, old_phase);
           if (elect_one()) {
             constexpr int kChunks = decltype(two)::value ? 2 : 1;
 #pragma unroll
@@ -770,7 +770,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int quarter = warp & 3;              // TMEM lanes this warp may access
     const int b = (warp - kRoleWarps) / 4;     // its 64-column block
     const int r = quarter * 32 + lane;         // token row of the CTA's 128
-    uint8_t* buf = s_out + (warp - kRoleWarps) * (32 * 64);
+    uint8_t* buf = s_out + (warp - kRoleWarps) * (32 * 128);
     const uint32_t sbuf = smem_u32(buf);
     Item w;
     bool ok = true;
@@ -808,10 +808,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       } else {
         const int feat = w.f * kPairN + b * 64;
         if (quarter * 32 + 32 <= valid) {
-          // 64 bytes a row in the 64-byte swizzle: 16-byte piece j of row l at j ^ ((l >> 1) & 3)
-          auto store = [&](const float (&v)[32], int col) {
-            if (lane == 0) tma_store_wait_read();
-            __syncwarp();
+          // 128 bytes a row in the 128-byte swizzle: 16-byte piece j of row l at j ^ (l & 7)
+          if (lane == 0) tma_store_wait_read();
+          __syncwarp();
+          auto pieces = [&](const float (&v)[32], int j0) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               uint32_t o[4];
@@ -820,14 +820,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const __nv_bfloat162 x = __floats2bfloat162_rn(v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
                 o[e] = *reinterpret_cast<const uint32_t*>(&x);
               }
-              *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(buf + lane * 128 + (((j0 + j) ^ (lane & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tma_store_2d(&y_map, sbuf, col, w.row0 + (int)rank * kMxTileRows + quarter * 32);
           };
-          store(p, feat);
-          store(q, feat + 32);
+          pieces(p, 0);
+          pieces(q, 4);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tma_store_2d(&y_map, sbuf, feat, w.row0 + (int)rank * kMxTileRows + quarter * 32);
         } else if (r < valid) {
           store_bf16_block(p, args.out + row * args.out_ld + feat);
           store_bf16_block(q, args.out + row * args.out_ld + feat + 32);
