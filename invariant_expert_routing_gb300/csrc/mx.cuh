@@ -110,6 +110,13 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(p));
   return p != 0;
 }
+// Arrival on another CTA's mbarrier without ordering the thread's memory
+// accesses.  It reports that accumulator columns have been read, which
+// tcgen05.wait::ld has completed; a release at cluster scope would first wait
+// for the global stores of the tile before to land (1100 to 3500 cycles).
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // Whether the phase of `parity` is complete, without waiting (try_wait may suspend the thread).
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;

@@ -796,7 +796,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (work) tmem_load32x2(tbase, p, tbase + 32, q);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(mapa_shared(tempty0 + 8 * acc, 0));
+      if (lane == 0) mbar_arrive_remote_relaxed(mapa_shared(tempty0 + 8 * acc, 0));
       if (!work) continue;
       if (kW13) {
         const int feat = w.f * (kPairN / 2) + b * 32;
