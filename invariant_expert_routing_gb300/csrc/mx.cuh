@@ -49,6 +49,18 @@ __device__ __forceinline__ uint32_t pack8(const float (&v)[8]) {
   return r;
 }
 
+// Two values to one byte, x in the low half.
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, z;\n\t"
+      "mov.b16 {z, _}, 0;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "mov.b32 %0, {b0, z, z, z};\n\t}"
+      : "=r"(r)
+      : "f"(x), "f"(y));
+  return r;
+}
+
 // Byte offset, inside one 512-byte chunk, of row r's four scale bytes (r <
 // 128): the order in which tcgen05.cp 32x128b puts rows r, r + 32, r + 64,
 // r + 96 into four neighbouring TMEM columns of lane r % 32.
@@ -223,6 +235,41 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Named barriers of `threads` threads; the second returns the AND of `pred`.
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool bar_and(int id, int threads, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred q, p;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "bar.red.and.pred p, %2, %3, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(pred ? 1 : 0), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
+// The largest magnitude in a warp; NaN if any lane holds one.
+__device__ __forceinline__ float warp_amax(float v) {
+  float r;
+  asm("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// 16 consecutive columns of the thread's lane (32 below).
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
 // 32 consecutive fp32 columns of the thread's TMEM lane, complete on return
 // (the wait is part of the statement, so no use can be moved before it).
 __device__ __forceinline__ void tmem_load32(uint32_t taddr, float (&v)[32]) {

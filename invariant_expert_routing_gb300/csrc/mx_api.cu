@@ -25,6 +25,9 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // Bytes of the scale chunks of `tiles` 128-row tiles with K elements a row.
 size_t sf_bytes(int64_t tiles, int K) { return (size_t)tiles * moe::kMxTileRows * (K / kSfBlock); }
 
+// 128-row scale tiles under a tile of the list.
+int64_t scale_tiles(int tile_rows) { return tile_rows > moe::kMxTileRows ? tile_rows / moe::kMxTileRows : 1; }
+
 // Workspace regions, each 256-byte aligned; the status word is at offset 0.
 struct Layout {
   size_t status, tiles, num_tiles, x_perm, x_sf, a, a_sf, x_sh_sf, a_sh, a_sh_sf,
@@ -36,9 +39,12 @@ struct Layout {
 Layout layout_of(const moe_config* c, int32_t T) {
   const size_t N = c->num_experts, H = c->hidden, I = c->intermediate, Is = c->shared_intermediate;
   const size_t R = (size_t)T * api::slots(c), rows = (size_t)api::max_rows(c, T);
-  const int64_t tiles = api::max_tiles(c, T, moe::kMxTileRows);
-  // scales of 128-row tiles, an even number of them for every tile of 256 rows
-  const int64_t sf_tiles = 2 * api::max_tiles(c, T, 2 * moe::kMxTileRows);
+  // The tile height follows the number of routes; the regions hold the list
+  // and the scale tiles of any height that up to T tokens may take, so that a
+  // workspace for T serves every smaller call.
+  const int32_t t_swap = (int32_t)std::min<int64_t>(T, moe::mx_swap_max_rows((int)N) / api::slots(c));
+  const int64_t tiles = std::max(api::max_tiles(c, t_swap, 32), api::max_tiles(c, T, moe::kMxTileRows));
+  const int64_t sf_tiles = std::max(tiles, 2 * api::max_tiles(c, T, 2 * moe::kMxTileRows));
   const int64_t tiles_t = 2 * (((int64_t)T + 2 * moe::kMxTileRows - 1) / (2 * moe::kMxTileRows));
   Layout L{};
   size_t off = 0;
@@ -52,9 +58,9 @@ Layout layout_of(const moe_config* c, int32_t T) {
   L.num_tiles = take(2 * sizeof(int32_t));
   // the activations keep one tile of rows of slack so that every tile load stays inside them
   L.x_perm = take((rows + moe::kMxTileRows) * H / 2);
-  L.x_sf = take(sf_bytes(std::max(tiles, sf_tiles), (int)H));
+  L.x_sf = take(sf_bytes(sf_tiles, (int)H));
   L.a = take((rows + moe::kMxTileRows) * I / 2);
-  L.a_sf = take(sf_bytes(std::max(tiles, sf_tiles), (int)I));
+  L.a_sf = take(sf_bytes(sf_tiles, (int)I));
   L.x_sh_sf = take(Is ? sf_bytes(tiles_t, (int)H) : 0);
   L.a_sh = take(Is ? ((size_t)T + moe::kMxTileRows) * Is / 2 : 0);
   L.a_sh_sf = take(Is ? sf_bytes(tiles_t, (int)Is) : 0);
@@ -180,14 +186,12 @@ bool map_w2(CUtensorMap* m, const void* base, int K, int H, int N, int box_rows)
 moe_status gemms(const moe_config* c, int H, int I, int N, const uint8_t* x, const uint8_t* x_sf, uint64_t x_rows,
                  const uint8_t* w13, const uint8_t* w13_sf, const uint8_t* w2, const uint8_t* w2_sf, uint8_t* a,
                  uint8_t* a_sf, uint64_t a_rows, uint16_t* y, uint64_t y_rows, const GemmTile* tiles,
-                 const int32_t* num_tiles, int tile_rows, int identity_T, int64_t max_tiles, int* status,
-                 cudaStream_t s) {
-  const int sms = api::sm_count();
-  if (sms <= 0) return MOE_ERR_CUDA;
-  const bool pair = tile_rows != moe::kMxTileRows;
-  const int f13 = moe::mx_tile_features(tile_rows, 2 * I, max_tiles, sms);
-  const int f2 = moe::mx_tile_features(tile_rows, H, max_tiles, sms);
-  const uint64_t sf_tiles = (uint64_t)max_tiles * (tile_rows / moe::kMxTileRows);
+                 const int32_t* num_tiles, int tile_rows, int identity_T, int64_t max_tiles, int64_t tiles_expected,
+                 int sms, int* status, cudaStream_t s) {
+  const bool pair = tile_rows > moe::kMxTileRows;
+  const int f13 = moe::mx_tile_features(tile_rows, 2 * I, tiles_expected, sms);
+  const int f2 = moe::mx_tile_features(tile_rows, H, tiles_expected, sms);
+  const uint64_t sf_tiles = (uint64_t)max_tiles * scale_tiles(tile_rows);
   moe::MxMaps m13, m2;
   // a CTA of a pair loads half of the weight rows of an item
   if (!map_w13(&m13.w, w13, H, I, N, pair ? 32 : f13) || !map_rows(&m13.x, x, H, x_rows, 128) ||
@@ -250,31 +254,52 @@ moe_status ffn_impl(const moe_config* c, int32_t T, const uint8_t* codes, const 
   const Layout L = layout_of(c, T);
   const int H = c->hidden, I = c->intermediate, N = c->num_experts, slots = api::slots(c);
   const int64_t rows = api::max_rows(c, T);
-  const int tile_rows = moe::mx_tile_rows((int64_t)T * slots, N);
+  const int64_t routes = (int64_t)T * slots;
+  const int tile_rows = moe::mx_tile_rows(routes, N);
   const int64_t max_tiles = api::max_tiles(c, T, tile_rows);
-  int* status = at<int>(ws, L.status);
-  GemmTile* tiles = at<GemmTile>(ws, L.tiles);
-  int32_t* num_tiles = at<int32_t>(ws, L.num_tiles);
-  if (!moe::mx_gemm_smem_ok()) return MOE_ERR_CUDA;
-  const moe::TileListOut list{tiles, num_tiles, tile_rows, (int)max_tiles, nullptr};
-  moe::launch_tiles_and_rows(blocks, num_padded, sorted, slots, T, N, c->block_size, rows, &list, nullptr, status, 0,
-                             nullptr, nullptr, H, nullptr, s);
-  uint8_t* x_perm = at<uint8_t>(ws, L.x_perm);
-  uint8_t* x_sf = at<uint8_t>(ws, L.x_sf);
-  moe::launch_mx_gather(codes, scales, sorted, slots, T, H, tiles, num_tiles, tile_rows, 0, max_tiles, x_perm, x_sf,
-                        s);
+  const int sms = api::sm_count();
+  if (sms <= 0 || !moe::mx_gemm_smem_ok()) return MOE_ERR_CUDA;
+  moe::MxFrontArgs f{};
+  f.codes = codes;
+  f.scales = scales;
+  f.sorted = sorted;
+  f.block_expert = blocks;
+  f.num_padded = num_padded;
+  f.T = T;
+  f.slots = slots;
+  f.H = H;
+  f.N = N;
+  f.B = c->block_size;
+  f.tile_rows = tile_rows;
+  f.max_rows = rows;
+  f.max_tiles = max_tiles;
+  f.tiles = at<GemmTile>(ws, L.tiles);
+  f.num_tiles = at<int32_t>(ws, L.num_tiles);
+  f.x_perm = at<uint8_t>(ws, L.x_perm);
+  f.x_sf = at<uint8_t>(ws, L.x_sf);
+  f.status = at<int>(ws, L.status);
+  moe::launch_mx_front(f, sms, s);
   const uint64_t perm_rows = (uint64_t)rows + moe::kMxTileRows;
-  MOE_TRY(gemms(c, H, I, N, x_perm, x_sf, perm_rows, w.w13, w.w13_sf, w.w2, w.w2_sf, at<uint8_t>(ws, L.a),
-                at<uint8_t>(ws, L.a_sf), perm_rows, y_perm, (uint64_t)rows, tiles, num_tiles, tile_rows, 0, max_tiles,
-                status, s));
+  // tiles as they come: one for each expert that routes can touch, and the full ones
+  const int64_t expected = std::min<int64_t>(routes, N) + routes / tile_rows;
+  MOE_TRY(gemms(c, H, I, N, f.x_perm, f.x_sf, perm_rows, w.w13, w.w13_sf, w.w2, w.w2_sf, at<uint8_t>(ws, L.a),
+                at<uint8_t>(ws, L.a_sf), perm_rows, y_perm, (uint64_t)rows, f.tiles, f.num_tiles, tile_rows, 0, max_tiles,
+                expected, sms, f.status, s));
   if (c->shared_intermediate > 0) {
-    const int rows_t = moe::mx_tile_rows(T, 1);
-    const int64_t tiles_t = ((int64_t)T + rows_t - 1) / rows_t;
-    uint8_t* xs_sf = at<uint8_t>(ws, L.x_sh_sf);
-    moe::launch_mx_gather(codes, scales, nullptr, 1, T, H, nullptr, nullptr, rows_t, T, tiles_t, nullptr, xs_sf, s);
-    MOE_TRY(gemms(c, H, c->shared_intermediate, 1, codes, xs_sf, (uint64_t)T, w.w13s, w.w13s_sf, w.w2s, w.w2s_sf,
+    moe::MxFrontArgs g{};
+    g.codes = codes;
+    g.scales = scales;
+    g.T = T;
+    g.slots = 1;
+    g.H = H;
+    g.tile_rows = moe::mx_tile_rows(T, 1);
+    g.identity_T = T;
+    g.max_tiles = ((int64_t)T + g.tile_rows - 1) / g.tile_rows;
+    g.x_sf = at<uint8_t>(ws, L.x_sh_sf);
+    moe::launch_mx_front(g, sms, s);
+    MOE_TRY(gemms(c, H, c->shared_intermediate, 1, codes, g.x_sf, (uint64_t)T, w.w13s, w.w13s_sf, w.w2s, w.w2s_sf,
                   at<uint8_t>(ws, L.a_sh), at<uint8_t>(ws, L.a_sh_sf), (uint64_t)T + moe::kMxTileRows, y_shared, (uint64_t)T,
-                  nullptr, nullptr, rows_t, T, tiles_t, status, s));
+                  nullptr, nullptr, g.tile_rows, T, g.max_tiles, g.max_tiles, sms, f.status, s));
   }
   return api::last_error();
 }

@@ -43,25 +43,36 @@ constexpr int kThreads = (kRoleWarps + kEpiWarps) * 32;
 constexpr int kStageK = 256;                         // elements of K per stage: one 128-byte row
 constexpr int kSmallRows = 32;                       // token box of a tile with at most 32 routed rows
 constexpr uint32_t kSmemBudget = 226 * 1024;
+// Operands swapped where experts average at most so many rows.
+constexpr int kSwapMaxRows = 16;
+// Wide work items while they come to so many per SM.
+constexpr int kMinWaves = 4;
 constexpr uint32_t kSfUnits = kSfChunkBytes >> 4;    // a scale chunk in descriptor units
 
-template <int BN>
+// BN weight rows a work item.  kSwap (tiles of at most 32 token rows): the
+// weight rows are operand A and the tokens operand B (see below).
+template <int BN, bool kSwap>
 struct Cfg {
-  static constexpr int kSfbTiles = (BN + kSfRows - 1) / kSfRows;      // 128-row scale tiles of B
-  static constexpr uint32_t kABytes = kMxTileRows * 128;
+  static_assert(!kSwap || BN == 128, "swapped items have the 128 rows of an MMA");
+  static constexpr int kTokens = kSwap ? kSmallRows : kMxTileRows;    // token rows of a tile
+  static constexpr int kSfbTiles = (BN + kSfRows - 1) / kSfRows;      // 128-row scale tiles of the weights
+  static constexpr uint32_t kABytes = kTokens * 128;
   static constexpr uint32_t kBBytes = BN * 128;
   static constexpr uint32_t kSfaBytes = 2 * kSfChunkBytes;
   static constexpr uint32_t kSfbBytes = kSfbTiles * 2 * kSfChunkBytes;
   static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
+  static constexpr uint32_t kXchgBytes = kSwap ? 2 * 2 * 16 * 32 * 4 : 0;   // up values handed to the gate warps
   static constexpr uint32_t kBarBytes = 512;
-  static constexpr int kFit = (int)((kSmemBudget - kBarBytes - 1024) / kStageBytes);
-  static constexpr int kStages = kFit < 8 ? kFit : 8;
-  static constexpr int kNumAcc = BN <= 128 ? 2 : 1;
+  static constexpr int kFit = (int)((kSmemBudget - kBarBytes - kXchgBytes - 1024) / kStageBytes);
+  static constexpr int kMaxStages = kSwap ? 9 : 8;
+  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+  static constexpr int kCols = kSwap ? kTokens : BN;                   // columns of an accumulator
+  static constexpr int kNumAcc = kCols <= 128 ? 2 : 1;
   static constexpr uint32_t kSfCols = 8 + 8 * kSfbTiles;               // TMEM columns of a stage's scales
-  static constexpr uint32_t kSfCol0 = kNumAcc * BN;
+  static constexpr uint32_t kSfCol0 = kNumAcc * kCols;
   static constexpr uint32_t kColsUsed = kSfCol0 + kStages * kSfCols;
   static constexpr uint32_t kTmemCols = kColsUsed <= 256 ? 256 : 512;
-  static constexpr uint32_t kSmemBytes = kStages * kStageBytes + kBarBytes + 1024;
+  static constexpr uint32_t kSmemBytes = kStages * kStageBytes + kXchgBytes + kBarBytes + 1024;
   static_assert(kColsUsed <= 512, "accumulators and scales fit in TMEM");
   static_assert(kStageBytes % 1024 == 0, "stages stay aligned to the swizzle atom");
 };
@@ -211,11 +222,11 @@ __device__ __forceinline__ void store_bf16_block(const float (&v)[32], uint16_t*
   }
 }
 
-template <bool kW13, int BN>
+template <bool kW13, int BN, bool kSwap>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
                    const __grid_constant__ CUtensorMap x_map_small, const MxGemmArgs args) {
-  using C = Cfg<BN>;
+  using C = Cfg<BN, kSwap>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem_base;
   __shared__ volatile int s_abort;
@@ -223,7 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(16) RingSlot s_ring[kRing];
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t full0 = smem_u32(smem + C::kStages * C::kStageBytes);
+  float* xchg = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);
+  const uint32_t full0 = smem_u32(smem + C::kStages * C::kStageBytes + C::kXchgBytes);
   const uint32_t empty0 = full0 + 8 * C::kStages;
   const uint32_t tfull0 = empty0 + 8 * C::kStages;
   const uint32_t tempty0 = tfull0 + 16;
@@ -269,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();
   const int num_tiles =
-      uniform(args.identity_T ? (args.identity_T + kMxTileRows - 1) / kMxTileRows : *args.num_tiles);
+      uniform(args.identity_T ? (args.identity_T + C::kTokens - 1) / C::kTokens : *args.num_tiles);
   const int total = num_tiles * nf;
 
   if (warp == 0) {
@@ -283,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     Item w;
     for (int n = 0; ok && next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim); ++n) {
-      const bool small = w.valid <= kSmallRows;
+      const bool small = kSwap || w.valid <= kSmallRows;
       const uint32_t a_tx = (small ? kSmallRows : kMxTileRows) * 128u;
       // scale tiles of B that exist (the last item of an odd number of 128-row tiles has one)
       const int sft0 = w.f * BN / kSfRows;
@@ -350,7 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t adesc0 = sdesc_sw128(s0, 16, 1024), bdesc0 = sdesc_sw128(s0 + C::kABytes, 16, 1024);
     const uint64_t fadesc0 = sdesc_scales(s0 + C::kABytes + C::kBBytes);
     const uint64_t fbdesc0 = sdesc_scales(s0 + C::kABytes + C::kBBytes + C::kSfaBytes);
-    constexpr uint32_t kI0 = idesc_mxf4(kMxTileRows, BN, 0), kI1 = idesc_mxf4(kMxTileRows, BN, 1);
+    constexpr int kN = C::kCols;
+    constexpr uint32_t kI0 = idesc_mxf4(128, kN, 0), kI1 = idesc_mxf4(128, kN, 1);
     uint32_t soff = 0;
     bool ready = false;   // peeked a stage ahead
     Item w;
@@ -361,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = false;
         break;
       }
-      const uint32_t d0 = tmem + acc * BN;
+      const uint32_t d0 = tmem + acc * C::kCols;
       // one stage: chunks of 128 elements, for each the scales (A's in columns
       // ta + 4c, those of B's tile t in tb + (c kSfbTiles + t) 4), then two MMAs
       auto step = [&](auto two, bool first, bool last) -> bool {
@@ -389,9 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
-            const uint32_t sb = tb + 4 * c * C::kSfbTiles + sfb_skip;
-            mma_mxf4(d0, ad + 4 * c, bd + 4 * c, kI0, ta + 4 * c, sb, (c > 0 || !first) ? 1u : 0u);
-            mma_mxf4(d0, ad + 4 * c + 2, bd + 4 * c + 2, kI1, ta + 4 * c, sb, 1u);
+            const uint32_t sa = ta + 4 * c, sb = tb + 4 * c * C::kSfbTiles + sfb_skip;
+            const uint64_t m = (kSwap ? bd : ad) + 4 * c, k = (kSwap ? ad : bd) + 4 * c;
+            mma_mxf4(d0, m, k, kI0, kSwap ? sb : sa, kSwap ? sa : sb, (c > 0 || !first) ? 1u : 0u);
+            mma_mxf4(d0, m + 2, k + 2, kI1, kSwap ? sb : sa, kSwap ? sa : sb, 1u);
           }
           mma_commit(done);
           if (last) mma_commit(tfull0 + 8 * acc);
@@ -419,34 +433,71 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kRoleWarps) {
     // ------------------------------------------------------------ scheduler
     if (warp == 2 && lane == 0)
-      schedule<kMxTileRows>(args, s_ring, ifull0, iempty0, blockIdx.x, gridDim.x, total, num_tiles, nf, &s_abort, wlim);
+      schedule<C::kTokens>(args, s_ring, ifull0, iempty0, blockIdx.x, gridDim.x, total, num_tiles, nf, &s_abort, wlim);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;              // TMEM lanes this warp may access
     const int half = (warp - kRoleWarps) / 4;  // which blocks of columns
-    const int r = quarter * 32 + lane;         // token row of the tile
+    const int r = quarter * 32 + lane;         // token row of the tile (swapped: weight row of the item)
     constexpr int kBlockCols = kW13 ? 64 : 32; // columns of one block (W13: 32 gate, 32 up)
     constexpr int kBlocks = BN / kBlockCols;
     int acc = 0;
     uint32_t acc_phase = 0;
     Item w;
     bool ok = true;
-    for (int n = 0; next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim); ++n) {
-      int got = 1;
-      if (lane == 0) got = mbar_wait(tfull0 + 8 * acc, acc_phase, &s_abort, wlim) ? 1 : 0;
-      got = __shfl_sync(0xffffffffu, got, 0);
-      if (!got) {
-        if (lane == 0) {
-          s_abort = 1;
-          atomicOr(args.status, kDevErrTimeout);
-        }
-        break;
-      }
+    for (int n = 0;; ++n) {
+      bool got = next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim);
+      const bool more = got || !ok;
+      if (got) got = warp_wait(tfull0 + 8 * acc, acc_phase, &s_abort, wlim);
+      if (more && !got) ok = false;
+      // a gate warp and its up warp go on or stop together (they meet on a barrier for every item)
+      const int pair = 1 + half * 2 + quarter / 2;
+      if (kSwap && kW13) got = bar_and(pair, 64, got);
+      if (!got) break;
       tc_fence_after();
-      const uint32_t tbase = tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN;
-      const size_t row = (size_t)w.row0 + r;
-      if (quarter * 32 < w.valid) {
+      const uint32_t tbase = tmem + ((uint32_t)(quarter * 32) << 16) + acc * C::kCols;
+      if (kSwap) {
+        // lane: weight row; columns: tokens, 16 of them this warp's
+        float v[16];
+        const int t0 = half * 16;
+        if (t0 < w.valid) tmem_load16(tbase + t0, v);
+        if (kW13) {
+          // the item's rows are 32 gate, 32 up, 32 gate, 32 up features: quarters 1 and 3 hand
+          // theirs over; a block of 32 features lies across the lanes of a gate warp
+          float* buf = xchg + (half * 2 + quarter / 2) * (16 * 32) + lane;
+          if (quarter & 1) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) buf[j * 32] = v[j];
+          }
+          bar_sync(pair, 64);
+          if (!(quarter & 1)) {
+            const int feat = w.f * (BN / 2) + (quarter / 2) * 32;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              if (t0 + j >= w.valid) break;
+              const float a = __fdividef(v[j], 1.0f + __expf(-v[j])) * buf[j * 32];
+              const uint32_t byte = scale_byte(__float_as_uint(warp_amax(a)) & 0x7FFFFFFFu);
+              const float x = byte == 255u ? 0.0f : a * scale_inverse(byte);
+              const float y = __shfl_down_sync(0xffffffffu, x, 1);
+              const size_t row = (size_t)w.row0 + t0 + j;
+              if (!(lane & 1)) args.out_codes[(row * args.out_ld + feat + lane) / 2] = (uint8_t)pack2(x, y);
+              if (lane == 0)
+                args.out_sf[((size_t)w.tile * (args.out_ld / kSfChunkK) + feat / kSfChunkK) * kSfChunkBytes +
+                            sf_row_offset(t0 + j) + (feat % kSfChunkK) / kBlock] = (uint8_t)byte;
+            }
+          }
+          bar_sync(pair, 64);   // the buffer is free again
+        } else {
+          const int feat = w.f * BN + r;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (t0 + j < w.valid)
+              args.out[((size_t)w.row0 + t0 + j) * args.out_ld + feat] =
+                  __bfloat16_as_ushort(__float2bfloat16_rn(v[j]));
+        }
+      } else if (quarter * 32 < w.valid) {
+        const size_t row = (size_t)w.row0 + r;
         for (int b = half; b < kBlocks; b += 2) {
           if (kW13) {
             const int feat = w.f * (BN / 2) + b * 32;
@@ -896,10 +947,10 @@ void launch_pair_mx(const MxMaps& m, MxGemmArgs a, int64_t max_tiles, int sms, c
   launch_pdl(kernel, dim3(2 * pairs), dim3(kPairThreads), smem, s, m.w, m.x, m.sfa, m.sfb, m.y, a);
 }
 
-template <bool kW13, int BN>
+template <bool kW13, int BN, bool kSwap>
 void launch(const MxMaps& m, MxGemmArgs a, int64_t max_tiles, int sms, cudaStream_t s) {
-  auto kernel = mx_gemm_kernel<kW13, BN>;
-  constexpr int smem = (int)Cfg<BN>::kSmemBytes;
+  auto kernel = mx_gemm_kernel<kW13, BN, kSwap>;
+  constexpr int smem = (int)Cfg<BN, kSwap>::kSmemBytes;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -914,42 +965,192 @@ void launch(const MxMaps& m, MxGemmArgs a, int64_t max_tiles, int sms, cudaStrea
   launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, s, m.w, m.x, m.x_small, a);
 }
 
-// Routed rows in tile order: a warp a row (16 bytes of codes a lane, then one
-// 4-byte word of scales per 128 elements, placed by sf_row_offset).
-constexpr int kGatherWarps = 8;
-__global__ void __launch_bounds__(32 * kGatherWarps) mx_gather_kernel(
-    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, const int32_t* __restrict__ sorted, int slots,
-    int T, int H, const GemmTile* __restrict__ tiles, const int32_t* __restrict__ num_tiles, int tile_rows, int identity_T,
-    uint8_t* __restrict__ x_perm, uint8_t* __restrict__ x_sf) {
+// ------------------------------------------------------------------ front
+// One launch before the GEMMs: the tile list, and the activations in tile
+// order (codes of the routed rows, and scales in the chunks that the MMAs
+// take).  Every CTA derives the experts' segments from the block list on its
+// own (one pass over it), so that nothing waits for the list: CTA 0 writes
+// it, the others copy tiles.  With identity_T there is no list and the codes
+// stay where they are.  Bound by memory and latency: the codes go through
+// L2 once more, 33 MB in 8 us for 8192 tokens x 8 of 2048 elements.
+constexpr int kFrontThreads = 256;
+constexpr int kFrontChunks = 16;   // scale chunks staged at once
+
+__global__ void __launch_bounds__(kFrontThreads) mx_front_kernel(const MxFrontArgs a) {
+  __shared__ int s_first[256], s_last[256], s_off[257], s_scan[8];
+  __shared__ int s_bad;
+  __shared__ int s_token[kMxTileRows];
+  __shared__ __align__(16) uint32_t s_sf[kFrontChunks * (kSfChunkBytes / 4)];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = identity_T ? (identity_T + tile_rows - 1) / tile_rows : *num_tiles;
-  const int kchunks = H / kSfChunkK;
-  const long long R = (long long)T * slots;
-  const long long rows = (long long)n * tile_rows;
-  const long long step = (long long)gridDim.x * kGatherWarps;
-  for (long long i = (long long)blockIdx.x * kGatherWarps + warp; i < rows; i += step) {
-    const int tile = (int)(i / tile_rows), r = (int)(i % tile_rows);
-    long long token;
-    size_t row = (size_t)i;
-    if (identity_T) {
-      if (i >= identity_T) continue;
-      token = i;
-    } else {
-      if (r >= tiles[tile].valid) continue;
-      row = (size_t)tiles[tile].row0 + r;
-      const int id = sorted[row];
-      if (id < 0 || id >= R) continue;
-      token = id / slots;
-      const uint4* src = reinterpret_cast<const uint4*>(codes + token * (H / 2));
-      uint4* dst = reinterpret_cast<uint4*>(x_perm + row * (H / 2));
-      for (int c = lane; c < H / 32; c += 32) dst[c] = __ldg(src + c);
+  const int sub_rows = min(a.tile_rows, kMxTileRows);   // rows of a scale tile
+  const int subs = a.tile_rows / sub_rows;
+  const int kchunks = a.H / kSfChunkK;
+  const long long R = (long long)a.T * a.slots;
+  int total;   // tiles
+  if (a.identity_T) {
+    total = (a.identity_T + a.tile_rows - 1) / a.tile_rows;
+  } else {
+    const int P = *a.num_padded;
+    const bool bad_count = P < 0 || (long long)P > a.max_rows || P % a.B != 0;
+    const int nb = bad_count ? 0 : P / a.B;
+    s_first[tid] = 0;
+    s_last[tid] = 0;
+    if (tid == 0) s_bad = bad_count ? 1 : 0;
+    __syncthreads();
+    // where each expert's blocks begin and end; a list out of order or range is refused
+    constexpr int kUnroll = 4;
+    for (int b0 = tid; b0 < nb; b0 += kUnroll * kFrontThreads) {
+      int e[kUnroll], prev[kUnroll], next[kUnroll];
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        const int b = b0 + j * kFrontThreads;
+        e[j] = b < nb ? a.block_expert[b] : 0;
+        prev[j] = b < nb && b > 0 ? a.block_expert[b - 1] : -1;
+        next[j] = b + 1 < nb ? a.block_expert[b + 1] : a.N;
+      }
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        const int b = b0 + j * kFrontThreads;
+        if (b >= nb) continue;
+        if (e[j] < 0 || e[j] >= a.N || prev[j] > e[j]) {
+          s_bad = 1;
+          continue;
+        }
+        if (prev[j] != e[j]) s_first[e[j]] = b;
+        if (next[j] != e[j]) s_last[e[j]] = b + 1;
+      }
     }
-    const uint32_t* ssrc = reinterpret_cast<const uint32_t*>(scales + token * (H / kBlock));
-    for (int c = lane; c < kchunks; c += 32)
-      *reinterpret_cast<uint32_t*>(x_sf + ((size_t)(i / kSfRows) * kchunks + c) * kSfChunkBytes + sf_row_offset(r % kSfRows)) =
-          __ldg(ssrc + c);
+    __syncthreads();
+    if (s_bad) {
+      if (blockIdx.x == 0 && tid == 0) {
+        *a.num_tiles = 0;
+        atomicOr(a.status, kDevErrBadBlocks);
+      }
+      return;
+    }
+    // tiles of each expert, their exclusive sum
+    const int rows = (s_last[tid] - s_first[tid]) * a.B;
+    const int nt = segment_tiles(rows, a.tile_rows);
+    int incl = nt;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += v;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    int base = 0;
+    for (int i = 0; i < warp; ++i) base += s_scan[i];
+    s_off[tid] = base + incl - nt;
+    if (tid == kFrontThreads - 1) s_off[256] = base + incl;
+    __syncthreads();
+    total = s_off[256];
+    if (blockIdx.x == 0) {
+      // rows up to the segment's last route (the padding trails it), eight rows a round trip
+      const int row0 = s_first[tid] * a.B;
+      int used = rows;
+      while (used > 0) {
+        const int n = min(8, used);
+        int id[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) id[j] = j < n ? a.sorted[row0 + used - 1 - j] : -1;
+        int found = -1;
+#pragma unroll
+        for (int j = 7; j >= 0; --j)
+          if (j < n && id[j] >= 0 && id[j] < R) found = j;
+        if (found >= 0) {
+          used -= found;
+          break;
+        }
+        used -= n;
+      }
+      for (int j = 0; j < nt; ++j) {
+        const int i = s_off[tid] + j;
+        if (i < a.max_tiles) a.tiles[i] = segment_tile(tid, row0, rows, used, a.tile_rows, nt, j, s_off[tid]);
+      }
+      if (tid == 0) *a.num_tiles = min(total, (int)a.max_tiles);
+      return;
+    }
+  }
+  total = min(total, (int)a.max_tiles);
+  const int first = a.identity_T ? (int)blockIdx.x : (int)blockIdx.x - 1;
+  const int step = a.identity_T ? (int)gridDim.x : (int)gridDim.x - 1;
+  const int pieces = a.H / 32;   // 16 bytes of codes each
+  for (long long sub = first; sub < (long long)total * subs; sub += step) {
+    long long row0;
+    int rows;
+    if (a.identity_T) {
+      row0 = sub * sub_rows;
+      rows = (int)min((long long)sub_rows, a.identity_T - row0);
+    } else {
+      const int tile = (int)(sub / subs);
+      int lo = 0, hi = a.N - 1;   // the expert: the last whose tiles begin at or before this one
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_off[mid] <= tile) lo = mid;
+        else hi = mid - 1;
+      }
+      row0 = (long long)s_first[lo] * a.B + (long long)(tile - s_off[lo]) * a.tile_rows + (sub % subs) * sub_rows;
+      rows = (int)max(0ll, min((long long)sub_rows, (long long)s_last[lo] * a.B - row0));
+    }
+    __syncthreads();   // the last round's tokens and scales are read
+    if (tid < sub_rows) {
+      int token = -1;
+      if (tid < rows) {
+        if (a.identity_T) {
+          token = (int)(row0 + tid);
+        } else {
+          const int id = a.sorted[row0 + tid];
+          if (id >= 0 && id < R) token = id / a.slots;
+        }
+      }
+      s_token[tid] = token;
+    }
+    __syncthreads();
+    if (!a.identity_T) {
+      // a warp copies four rows at a time, two 16-byte pieces a lane of each
+      constexpr int kRowsAt = 4;
+      for (int r0 = warp; r0 < rows; r0 += kRowsAt * (kFrontThreads / 32)) {
+        for (int p0 = lane; p0 < pieces; p0 += 64) {
+          uint4 v[kRowsAt][2];
+#pragma unroll
+          for (int j = 0; j < kRowsAt; ++j) {
+            const int row = r0 + j * (kFrontThreads / 32);
+            const int token = row < rows ? s_token[row] : -1;
+            const uint4* src = reinterpret_cast<const uint4*>(a.codes + (size_t)max(token, 0) * (a.H / 2));
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              if (token >= 0 && p0 + 32 * u < pieces) v[j][u] = __ldg(src + p0 + 32 * u);
+          }
+#pragma unroll
+          for (int j = 0; j < kRowsAt; ++j) {
+            const int row = r0 + j * (kFrontThreads / 32);
+            const int token = row < rows ? s_token[row] : -1;
+            uint4* dst = reinterpret_cast<uint4*>(a.x_perm + (size_t)(row0 + row) * (a.H / 2));
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              if (token >= 0 && p0 + 32 * u < pieces) dst[p0 + 32 * u] = v[j][u];
+          }
+        }
+      }
+    }
+    uint4* out = reinterpret_cast<uint4*>(a.x_sf + (size_t)sub * kchunks * kSfChunkBytes);
+    for (int c0 = 0; c0 < kchunks; c0 += kFrontChunks) {
+      const int nc = min(kFrontChunks, kchunks - c0);
+      if (c0) __syncthreads();
+      for (int i = tid; i < sub_rows * kFrontChunks; i += kFrontThreads) {
+        const int row = i / kFrontChunks, c = i % kFrontChunks;
+        const int token = s_token[row];
+        if (c < nc)
+          s_sf[(c * kSfChunkBytes + sf_row_offset(row)) / 4] =
+              token >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(a.scales + (size_t)token * (a.H / kBlock)) + c0 + c) : 0u;
+      }
+      __syncthreads();
+      for (int i = tid; i < nc * (int)(kSfChunkBytes / 16); i += kFrontThreads)
+        out[(size_t)c0 * (kSfChunkBytes / 16) + i] = reinterpret_cast<const uint4*>(s_sf)[i];
+    }
   }
 }
 
@@ -959,46 +1160,42 @@ bool mx_gemm_smem_ok() {
   int dev = 0, optin = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-  return optin >= (int)Cfg<256>::kSmemBytes && optin >= (int)Cfg<64>::kSmemBytes &&
-         optin >= (int)PairCfgMx<true>::kSmemBytes && optin >= (int)PairCfgMx<false>::kSmemBytes;
+  return optin >= (int)kSmemBudget;
 }
+
+int64_t mx_swap_max_rows(int experts) { return (int64_t)kSwapMaxRows * experts; }
 
 int mx_tile_rows(int64_t rows, int experts) {
-  return rows >= (int64_t)kPairRowsMx * experts ? kPairRowsMx : kMxTileRows;
+  if (rows >= (int64_t)kPairRowsMx * experts) return kPairRowsMx;
+  return rows <= mx_swap_max_rows(experts) ? kSmallRows : kMxTileRows;
 }
 
-int mx_tile_features(int tile_rows, int features, int64_t max_tiles, int sms) {
+int mx_tile_features(int tile_rows, int features, int64_t tiles, int sms) {
   if (tile_rows == kPairRowsMx) return kPairN;
-  const int64_t wide = max_tiles * ((features + 255) / 256);
-  return wide >= 2 * sms ? 256 : 64;
+  if (tile_rows == kSmallRows) return 128;
+  for (int f = 256; f > 64; f /= 2)
+    if (tiles * ((features + f - 1) / f) >= kMinWaves * sms) return f;
+  return 64;
 }
 
 void launch_mx_gemm(bool w13, const MxMaps& m, const MxGemmArgs& a, int64_t max_tiles, int sms, cudaStream_t s) {
-  if (a.tile_rows == kPairRowsMx) {
-    if (w13)
-      launch_pair_mx<true>(m, a, max_tiles, sms, s);
-    else
-      launch_pair_mx<false>(m, a, max_tiles, sms, s);
-  } else if (a.tile_features == 256) {
-    if (w13)
-      launch<true, 256>(m, a, max_tiles, sms, s);
-    else
-      launch<false, 256>(m, a, max_tiles, sms, s);
-  } else {
-    if (w13)
-      launch<true, 64>(m, a, max_tiles, sms, s);
-    else
-      launch<false, 64>(m, a, max_tiles, sms, s);
-  }
+  auto go = [&](auto first, auto second) { (w13 ? first : second)(m, a, max_tiles, sms, s); };
+  if (a.tile_rows == kPairRowsMx)
+    go(launch_pair_mx<true>, launch_pair_mx<false>);
+  else if (a.tile_rows == kSmallRows)
+    go(launch<true, 128, true>, launch<false, 128, true>);
+  else if (a.tile_features == 256)
+    go(launch<true, 256, false>, launch<false, 256, false>);
+  else if (a.tile_features == 128)
+    go(launch<true, 128, false>, launch<false, 128, false>);
+  else
+    go(launch<true, 64, false>, launch<false, 64, false>);
 }
 
-void launch_mx_gather(const uint8_t* codes, const uint8_t* scales, const int32_t* sorted_route_ids, int slots,
-                      int T, int H, const GemmTile* tiles, const int32_t* num_tiles, int tile_rows, int identity_T,
-                      int64_t max_tiles, uint8_t* x_perm, uint8_t* x_sf, cudaStream_t s) {
-  const int64_t blocks = max_tiles * tile_rows / kGatherWarps;
-  const int grid = (int)(blocks < 152 * 8 ? blocks : 152 * 8);
-  launch_pdl(mx_gather_kernel, dim3(grid), dim3(32 * kGatherWarps), 0, s, codes, scales, sorted_route_ids, slots, T, H,
-             tiles, num_tiles, tile_rows, identity_T, x_perm, x_sf);
+void launch_mx_front(const MxFrontArgs& a, int sms, cudaStream_t s) {
+  const int64_t subs = a.max_tiles * (a.tile_rows > kMxTileRows ? a.tile_rows / kMxTileRows : 1);
+  const int64_t want = subs + (a.identity_T ? 0 : 1), cap = (int64_t)sms * 4;   // four CTAs an SM
+  launch_pdl(mx_front_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(kFrontThreads), 0, s, a);
 }
 
 }  // namespace moe

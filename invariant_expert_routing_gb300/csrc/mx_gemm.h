@@ -15,7 +15,7 @@ constexpr int kMxTileRows = 128;   // token rows of a CTA's tile; a pair's tile 
 struct MxGemmArgs {
   int K;                     // reduction length (H for W13, I for W2)
   int features;              // weight rows of one expert (2I or H)
-  int tile_rows;             // token rows of a tile of the list: kMxTileRows, or twice that (CTA pairs)
+  int tile_rows;             // token rows of a tile of the list: 256 (CTA pairs), 128, or 32 (operands swapped)
   int tile_features;         // weight rows of one work item
   const GemmTile* tiles;     // tile list on the device
   const int32_t* num_tiles;  // device count
@@ -41,16 +41,28 @@ struct MxMaps {
 };
 
 bool mx_gemm_smem_ok();
-// Token rows of a tile: 256 (CTA pairs) or 128.  max_rows: routed rows at most.
-int mx_tile_rows(int64_t max_rows, int experts);
-// Weight rows of a work item: a rule on the number of items (see the definition).
-int mx_tile_features(int tile_rows, int features, int64_t max_tiles, int sms);
+// Token rows of a tile: 256 (CTA pairs), 128, or 32 (operands swapped), by the
+// average number of rows an expert has.
+int mx_tile_rows(int64_t rows, int experts);
+int64_t mx_swap_max_rows(int experts);   // the most rows with 32-row tiles
+// Weight rows of a work item: a rule on the number of items (tiles: as expected).
+int mx_tile_features(int tile_rows, int features, int64_t tiles, int sms);
 void launch_mx_gemm(bool w13, const MxMaps& m, const MxGemmArgs& a, int64_t max_tiles, int sms, cudaStream_t s);
 
-// Routed rows of the activations in tile order: codes [rows, H/2] and scales
-// [128-row tile][H/128][512] (identity_T > 0: the scales alone, rows 0..T-1).
-void launch_mx_gather(const uint8_t* codes, const uint8_t* scales, const int32_t* sorted_route_ids, int slots,
-                      int T, int H, const GemmTile* tiles, const int32_t* num_tiles, int tile_rows, int identity_T,
-                      int64_t max_tiles, uint8_t* x_perm, uint8_t* x_sf, cudaStream_t s);
+// The launch before the GEMMs: the tile list (tile_rows rows), and the
+// activations in tile order: codes [rows, H/2] and scales [tile][H/128][512],
+// a tile of 256 rows as two of 128.  identity_T > 0: the scales of rows
+// 0..T-1 alone.
+struct MxFrontArgs {
+  const uint8_t *codes, *scales;   // [T, H/2], [T, H/32]
+  const int32_t *sorted, *block_expert, *num_padded;
+  int T, slots, H, N, B, tile_rows, identity_T;
+  int64_t max_rows, max_tiles;
+  GemmTile* tiles;
+  int32_t* num_tiles;
+  uint8_t *x_perm, *x_sf;
+  int* status;
+};
+void launch_mx_front(const MxFrontArgs& a, int sms, cudaStream_t s);
 
 }  // namespace moe

@@ -332,6 +332,8 @@ FFNS = [  # T, H, N, k, I, B, Is
     (1, 128, 1, 1, 128, 8, 0),
     (1, 256, 8, 2, 384, 64, 128),
     (5, 384, 4, 3, 256, 16, 256),
+    (33, 512, 16, 2, 384, 8, 128),       # tiles of 32 rows, several an expert
+    (100, 256, 4, 2, 128, 16, 0),
     (33, 640, 3, 1, 128, 128, 0),
     (130, 128, 8, 2, 256, 8, 128),
     (257, 256, 2, 2, 256, 32, 384),
@@ -382,10 +384,10 @@ def test_expert_ffn_nan_and_zero_rows(moe):
     assert (np.abs(got[[0, 2]] - ref) <= tol).all()
 
 
-@pytest.mark.parametrize("N", [32, 16])
+@pytest.mark.parametrize("N", [32, 16, 256])
 def test_expert_ffn_rows_do_not_depend_on_the_batch(moe, N):
-    """A token alone (narrow work items) and in a batch of many tiles (wide ones; with 16
-    experts CTA pairs): the same bits."""
+    """A token alone (operands swapped) and in a batch of many tiles (wide items; with 16
+    experts CTA pairs; with 256 tiles of 25 rows): the same bits."""
     torch = torch_()
     rng = np.random.default_rng(11)
     L = Layer(moe, 768, N, 4, 640, 16, Is=256, seed=6)
@@ -394,6 +396,12 @@ def test_expert_ffn_rows_do_not_depend_on_the_batch(moe, N):
     idx = torch.from_numpy(np.sort(np.argsort(rng.random((T, N)), axis=1)[:, :4], axis=1).astype(np.int32)).cuda()
     d = L.dispatch(idx)
     y, ysh = L.ffn(c, s, d)
+    few = slice(100, 170)   # 64-column items
+    df = L.dispatch(idx[few].contiguous())
+    yf, yshf = L.ffn(c[few].clone(), s[few].clone(), df)
+    for j in range(0, 280, 7):
+        assert torch.equal(y[d["pos"][400 + j]], yf[df["pos"][j]])
+    assert torch.equal(ysh[few], yshf)
     for t in (0, 3, 801, 1599):
         d1 = L.dispatch(idx[t:t + 1].contiguous())
         y1, ysh1 = L.ffn(c[t:t + 1].clone(), s[t:t + 1].clone(), d1)   # a copy: pointers are 16-byte aligned

@@ -106,8 +106,9 @@ def test_ffn_refusals(moe):
     cfg = moe.make_config(**CFG)
     n = moe.moe_workspace_bytes_mx(cfg, 8)
     assert n > 0 and moe.moe_workspace_bytes_mx(dict(CFG, hidden=100), 8) == 0
-    sizes = [moe.moe_workspace_bytes_mx(cfg, T) for T in (0, 1, 64, 1000)]
-    assert sizes == sorted(sizes)
+    for c in (CFG, dict(CFG, num_experts=128, top_k=8, block_size=16), dict(CFG, num_experts=1, top_k=1)):
+        sizes = [moe.moe_workspace_bytes_mx(c, T) for T in range(0, 1200)]   # across every tile height
+        assert sizes == sorted(sizes)
 
     def call(c=cfg, T=8, at=None, value=None, ws_bytes=n):
         ptrs = [OK16] * 6 + [None] * 4 + [OK16] * 4 + [None, OK16]
