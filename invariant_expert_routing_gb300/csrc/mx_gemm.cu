@@ -977,7 +977,7 @@ constexpr int kFrontThreads = 256;
 constexpr int kFrontChunks = 16;   // scale chunks staged at once
 
 __global__ void __launch_bounds__(kFrontThreads) mx_front_kernel(const MxFrontArgs a) {
-  __shared__ int s_first[256], s_last[256], s_off[257], s_scan[8];
+  __shared__ int s_first[256], s_last[256], s_used[256], s_off[257], s_scan[8];
   __shared__ int s_bad;
   __shared__ int s_token[kMxTileRows];
   __shared__ __align__(16) uint32_t s_sf[kFrontChunks * (kSfChunkBytes / 4)];
@@ -1030,9 +1030,41 @@ __global__ void __launch_bounds__(kFrontThreads) mx_front_kernel(const MxFrontAr
       }
       return;
     }
-    // tiles of each expert, their exclusive sum
+    // Rows up to each segment's last route (the padding trails it).  The list
+    // needs them, and where a tile is shorter than a block so does every CTA:
+    // a block's last tiles may then hold no route, and are left out.
     const int rows = (s_last[tid] - s_first[tid]) * a.B;
-    const int nt = segment_tiles(rows, a.tile_rows);
+    const bool short_tiles = a.tile_rows < a.B;
+    if (short_tiles || blockIdx.x == 0) {
+      s_used[tid] = 0;
+      __syncthreads();
+      constexpr int kLoads = 8;
+      for (int i0 = tid; i0 < a.N * a.B; i0 += kLoads * kFrontThreads) {   // the last blocks, flattened
+        int e[kLoads], row[kLoads], id[kLoads];
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+          const int i = i0 + j * kFrontThreads;
+          e[j] = min(i / a.B, a.N - 1);
+          row[j] = (s_last[e[j]] - 1) * a.B + i % a.B;
+          id[j] = i < a.N * a.B && s_last[e[j]] > 0 ? a.sorted[row[j]] : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+          if (id[j] >= 0 && id[j] < R) atomicMax(&s_used[e[j]], row[j] + 1 - s_first[e[j]] * a.B);
+      }
+      __syncthreads();
+      int used = s_used[tid];
+      if (used == 0 && rows > 0) {   // a caller's list may end in blocks without a route
+        for (used = rows - a.B; used > 0; --used) {
+          const int id = a.sorted[s_first[tid] * a.B + used - 1];
+          if (id >= 0 && id < R) break;
+        }
+        s_used[tid] = max(used, 0);
+      }
+      __syncthreads();
+    }
+    // tiles of each expert, their exclusive sum
+    const int nt = segment_tiles(short_tiles ? s_used[tid] : rows, a.tile_rows);
     int incl = nt;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -1048,24 +1080,7 @@ __global__ void __launch_bounds__(kFrontThreads) mx_front_kernel(const MxFrontAr
     __syncthreads();
     total = s_off[256];
     if (blockIdx.x == 0) {
-      // rows up to the segment's last route (the padding trails it), eight rows a round trip
-      const int row0 = s_first[tid] * a.B;
-      int used = rows;
-      while (used > 0) {
-        const int n = min(8, used);
-        int id[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) id[j] = j < n ? a.sorted[row0 + used - 1 - j] : -1;
-        int found = -1;
-#pragma unroll
-        for (int j = 7; j >= 0; --j)
-          if (j < n && id[j] >= 0 && id[j] < R) found = j;
-        if (found >= 0) {
-          used -= found;
-          break;
-        }
-        used -= n;
-      }
+      const int row0 = s_first[tid] * a.B, used = s_used[tid];
       for (int j = 0; j < nt; ++j) {
         const int i = s_off[tid] + j;
         if (i < a.max_tiles) a.tiles[i] = segment_tile(tid, row0, rows, used, a.tile_rows, nt, j, s_off[tid]);
