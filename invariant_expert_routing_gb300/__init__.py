@@ -155,13 +155,19 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_current_stream = None   # () -> handle of the current device's current stream; set at the first call
+
+
 def _stream(stream):
-    if stream is None:
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    global _current_stream
+    if _current_stream is None:
         import torch
         # the raw handle where torch offers it: building a Stream object costs about as much as a launch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
-    return stream if isinstance(stream, int) else stream.cuda_stream
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+        _current_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _current_stream()
 
 
 def _check(fn, st):
@@ -383,15 +389,25 @@ def _scoring(scoring) -> moe_scoring:
     return scoring if isinstance(scoring, moe_scoring) else make_scoring(**scoring)
 
 
+class _Dtypes(dict):
+    """torch dtypes by name, looked up once (torch is imported with the first tensor, not here)."""
+    def __missing__(self, name):
+        import torch
+        self[name] = getattr(torch, name)
+        return self[name]
+
+
+_dtypes = _Dtypes()
+
+
 def _want(name, t, dtype, shape, optional=False):
     """The address of a contiguous CUDA tensor of this type and shape (the C entry points see
     pointers only); None for an optional one that is absent."""
-    import torch
     if t is None:
         if optional:
             return None
         raise ValueError(f"{name}: a tensor is needed")
-    if t.dtype is not getattr(torch, dtype) or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype is not _dtypes[dtype] or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: a contiguous CUDA tensor of {dtype} {tuple(shape)} is needed, got "
                          f"{t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'} on {t.device}")
     return t.data_ptr()
@@ -399,8 +415,7 @@ def _want(name, t, dtype, shape, optional=False):
 
 def _want_at_least(name, t, dtype, n):
     """The address of a contiguous CUDA tensor of this type with at least n elements."""
-    import torch
-    if t is None or t.dtype is not getattr(torch, dtype) or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
+    if t is None or t.dtype is not _dtypes[dtype] or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: a contiguous CUDA tensor of at least {n} {dtype} is needed")
     return t.data_ptr()
 

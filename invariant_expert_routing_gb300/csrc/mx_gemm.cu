@@ -46,7 +46,7 @@ constexpr uint32_t kSmemBudget = 226 * 1024;
 // Operands swapped where experts average at most so many rows.
 constexpr int kSwapMaxRows = 16;
 // Wide work items while they come to so many per SM.
-constexpr int kMinWaves = 4;
+constexpr int kMinWaves = 8;
 constexpr uint32_t kSfUnits = kSfChunkBytes >> 4;    // a scale chunk in descriptor units
 
 // BN weight rows a work item.  kSwap (tiles of at most 32 token rows): the
