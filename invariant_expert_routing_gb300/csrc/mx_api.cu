@@ -192,11 +192,13 @@ moe_status gemms(const moe_config* c, int H, int I, int N, const uint8_t* x, con
   const int f13 = moe::mx_tile_features(tile_rows, 2 * I, tiles_expected, sms);
   const int f2 = moe::mx_tile_features(tile_rows, H, tiles_expected, sms);
   const uint64_t sf_tiles = (uint64_t)max_tiles * scale_tiles(tile_rows);
+  const bool swap = tile_rows < moe::kMxTileRows;
+  const uint32_t box = swap ? 32 : 128, box_small = swap ? 8 : 32;   // token rows
   moe::MxMaps m13, m2;
   // a CTA of a pair loads half of the weight rows of an item
-  if (!map_w13(&m13.w, w13, H, I, N, pair ? 32 : f13) || !map_rows(&m13.x, x, H, x_rows, 128) ||
-      !map_rows(&m13.x_small, x, H, x_rows, 32) || !map_w2(&m2.w, w2, I, H, N, pair ? f2 / 2 : f2) ||
-      !map_rows(&m2.x, a, I, a_rows, 128) || !map_rows(&m2.x_small, a, I, a_rows, 32))
+  if (!map_w13(&m13.w, w13, H, I, N, pair ? 32 : f13) || !map_rows(&m13.x, x, H, x_rows, box) ||
+      !map_rows(&m13.x_small, x, H, x_rows, box_small) || !map_w2(&m2.w, w2, I, H, N, pair ? f2 / 2 : f2) ||
+      !map_rows(&m2.x, a, I, a_rows, box) || !map_rows(&m2.x_small, a, I, a_rows, box_small))
     return MOE_ERR_CUDA;
   if (pair && (!map_scales(&m13.sfa, x_sf, sf_tiles * (H / 128)) || !map_scales(&m2.sfa, a_sf, sf_tiles * (I / 128)) ||
                !map_scales(&m13.sfb, w13_sf, (uint64_t)N * (2 * I / 128) * (H / 128)) ||

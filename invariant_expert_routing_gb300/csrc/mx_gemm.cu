@@ -43,9 +43,15 @@ constexpr int kThreads = (kRoleWarps + kEpiWarps) * 32;
 constexpr int kStageK = 256;                         // elements of K per stage: one 128-byte row
 constexpr int kSmallRows = 32;                       // token box of a tile with at most 32 routed rows
 constexpr uint32_t kSmemBudget = 226 * 1024;
-// Operands swapped where experts average at most so many rows.
+// Operands swapped where experts average at most so many rows (H 4096, I
+// 14336, 8 experts: 128 us against 136 with 16 rows, 149 against 137 with 25),
+// CTA pairs from so many on (H 2048, I 768, 128 experts: 94 us against 95 with
+// 96 rows, 79 against 88 with 64, 105 against 101 with 128).
 constexpr int kSwapMaxRows = 16;
-// Wide work items while they come to so many per SM.
+constexpr int kPairMinRows = 96;
+// Wide work items (256 weight rows, else 128, else 64) while they come to so
+// many per SM: 512 tokens x 8 of 128 experts, 5 waves of wide W13 items 73 us
+// a pass, 10 of 128 rows 70.5 us.
 constexpr int kMinWaves = 8;
 constexpr uint32_t kSfUnits = kSfChunkBytes >> 4;    // a scale chunk in descriptor units
 
@@ -295,8 +301,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     Item w;
     for (int n = 0; ok && next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim); ++n) {
-      const bool small = kSwap || w.valid <= kSmallRows;
-      const uint32_t a_tx = (small ? kSmallRows : kMxTileRows) * 128u;
+      // rows of the token box: swapped 8 or 32 (the copy engine takes about 2.5
+      // cycles a row), else 32 or 128
+      constexpr int kBoxMin = kSwap ? 8 : kSmallRows, kBoxMax = kSwap ? kSmallRows : kMxTileRows;
+      const bool small = w.valid <= kBoxMin;
+      const uint32_t a_tx = (small ? kBoxMin : kBoxMax) * 128u;
       // scale tiles of B that exist (the last item of an odd number of 128-row tiles has one)
       const int sft0 = w.f * BN / kSfRows;
       const int sft = min(C::kSfbTiles, args.features / kSfRows - sft0);
@@ -365,7 +374,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kN = C::kCols;
     constexpr uint32_t kI0 = idesc_mxf4(128, kN, 0), kI1 = idesc_mxf4(128, kN, 1);
     uint32_t soff = 0;
-    bool ready = false;   // peeked a stage ahead
     Item w;
     for (int n = 0; ok && next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim); ++n) {
       // an item narrower than a scale tile takes its columns of it
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // one stage: chunks of 128 elements, for each the scales (A's in columns
       // ta + 4c, those of B's tile t in tb + (c kSfbTiles + t) 4), then two MMAs
       auto step = [&](auto two, bool first, bool last) -> bool {
-        if (!__all_sync(0xffffffffu, ready) && !warp_wait(full0 + 8 * stage, phase, &s_abort, wlim)) return false;
+        if (!warp_wait(full0 + 8 * stage, phase, &s_abort, wlim)) return false;
         tc_fence_after();
         const uint32_t ta = tmem + C::kSfCol0 + stage * C::kSfCols, tb = ta + 8;
         const uint64_t ad = adesc0 + soff, bd = bdesc0 + soff, fa = fadesc0 + soff, fbd = fbdesc0 + soff;
@@ -390,7 +398,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           soff += C::kStageBytes >> 4;
         }
-        ready = mbar_test(full0 + 8 * stage, phase);
         if (elect_one()) {
           constexpr int kChunks = decltype(two)::value ? 2 : 1;
 #pragma unroll
@@ -1181,7 +1188,7 @@ bool mx_gemm_smem_ok() {
 int64_t mx_swap_max_rows(int experts) { return (int64_t)kSwapMaxRows * experts; }
 
 int mx_tile_rows(int64_t rows, int experts) {
-  if (rows >= (int64_t)kPairRowsMx * experts) return kPairRowsMx;
+  if (rows >= (int64_t)kPairMinRows * experts) return kPairRowsMx;
   return rows <= mx_swap_max_rows(experts) ? kSmallRows : kMxTileRows;
 }
 
