@@ -374,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kN = C::kCols;
     constexpr uint32_t kI0 = idesc_mxf4(128, kN, 0), kI1 = idesc_mxf4(128, kN, 1);
     uint32_t soff = 0;
+    const bool leader = elect_one();
     Item w;
     for (int n = 0; ok && next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim); ++n) {
       // an item narrower than a scale tile takes its columns of it
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // one stage: chunks of 128 elements, for each the scales (A's in columns
       // ta + 4c, those of B's tile t in tb + (c kSfbTiles + t) 4), then two MMAs
       auto step = [&](auto two, bool first, bool last) -> bool {
-        if (!warp_wait(full0 + 8 * stage, phase, &s_abort, wlim)) return false;
+        if (!mbar_wait(full0 + 8 * stage, phase, &s_abort, wlim)) return false;
         tc_fence_after();
         const uint32_t ta = tmem + C::kSfCol0 + stage * C::kSfCols, tb = ta + 8;
         const uint64_t ad = adesc0 + soff, bd = bdesc0 + soff, fa = fadesc0 + soff, fbd = fbdesc0 + soff;
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           soff += C::kStageBytes >> 4;
         }
-        if (elect_one()) {
+        if (leader) {
           constexpr int kChunks = decltype(two)::value ? 2 : 1;
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
@@ -417,11 +418,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(done);
           if (last) mma_commit(tfull0 + 8 * acc);
         }
-        __syncwarp();
         return true;
       };
       for (int ks = 0; ok && ks < kchunks / 2; ++ks) ok = step(std::true_type{}, ks == 0, 2 * ks + 2 == kchunks);
       if (ok && (kchunks & 1)) ok = step(std::false_type{}, kchunks == 1, true);
+      ok = __all_sync(0xffffffffu, ok);
       if (++acc == C::kNumAcc) {
         acc = 0;
         acc_phase ^= 1u;
@@ -747,13 +748,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const uint64_t fbdesc0 = sdesc_scales(s0 + C::kABytes + C::kBBytes + C::kSfaBytes);
       constexpr uint32_t kI0 = idesc_mxf4(kPairRowsMx, kPairN, 0), kI1 = idesc_mxf4(kPairRowsMx, kPairN, 1);
       uint32_t soff = 0;
+      const bool leader = elect_one();
       bool ok = true;
       Item w;
-      // The next stage's barrier, and that of the step whose MMAs read the
-      // scale slot it will rewrite, are looked at while this stage's
-      // instructions are issued: the issue of a stage then stays below its 384
-      // cycles of MMAs (a wait in place costs about 80).
-      bool ready = false, slot_free = true;
       for (int n = 0; ok && next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim); ++n) {
         const int acc = n & 1;
         const uint32_t sfb_skip = (uint32_t)(w.f * kPairN % kSfRows) / 32u;
@@ -763,10 +760,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         const uint32_t d0 = tmem + acc * kPairN;
         auto step = [&](auto two, bool first, bool last) -> bool {
-          if (!__all_sync(0xffffffffu, ready && slot_free)) {
-            if (!warp_wait_cluster(full0 + 8 * stage, phase, &s_abort, wlim)) return false;
-            if (C::kStages > kSfSlots && steps >= kSfSlots && !warp_wait_cluster(empty0 + 8 * old, old_phase, &s_abort, wlim)) return false;
-          }
+          if (!mbar_wait_cluster(full0 + 8 * stage, phase, &s_abort, wlim)) return false;
+          // the scale slot is free once the step kSfSlots before this one has been committed
+          if (C::kStages > kSfSlots && steps >= kSfSlots &&
+              !mbar_wait_cluster(empty0 + 8 * old, old_phase, &s_abort, wlim))
+            return false;
           tc_fence_after();
           const uint32_t ta = tmem + C::kSfCol0 + slot * C::kSfCols, tb = ta + 8;
           const uint64_t ad = adesc0 + soff, bd = bdesc0 + soff, fa = fadesc0 + soff, fbd = fbdesc0 + soff;
@@ -783,9 +781,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             old = 0;
             old_phase ^= 1u;
           }
-          ready = mbar_test(full0 + 8 * stage, phase);
-          if (C::kStages > kSfSlots && steps >= kSfSlots) slot_free = mbar_test(empty0 + 8 * old, old_phase);
-          if (elect_one()) {
+          if (leader) {
             constexpr int kChunks = decltype(two)::value ? 2 : 1;
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
@@ -802,11 +798,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             mma_commit_pair(done, 0x3);
             if (last) mma_commit_pair(tfull0 + 8 * acc, 0x3);
           }
-          __syncwarp();
           return true;
         };
         for (int ks = 0; ok && ks < kchunks / 2; ++ks) ok = step(std::true_type{}, ks == 0, 2 * ks + 2 == kchunks);
         if (ok && (kchunks & 1)) ok = step(std::false_type{}, kchunks == 1, true);
+        ok = __all_sync(0xffffffffu, ok);
       }
       if (!ok) {
         s_abort = 1;
