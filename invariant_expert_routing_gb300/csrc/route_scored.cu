@@ -10,12 +10,14 @@
 //   gate_j = scale * score_j [/ (sum of the selected scores + 1e-20)]
 // Ties go to the lower index, NaN ranks last.
 //
-// Two kernels, by N and the groups alone.  Where a lane can hold 4 or 8
-// consecutive experts of one group, each lane sorts its four best values (16
-// compare-exchanges, no indices); group scores are a merge of the lanes' first
-// two, and a round of the top-k is a redux, a ballot and a shift of the
-// winner's list, without a scan of the lane's experts.  Any other shape, and
-// a row with an infinite or NaN value, takes experts lane + 32 s and scans,
+// Two kernels, by N and the groups alone.  Where a lane can hold 4, 8 or 16
+// consecutive experts of one group, half a warp takes a token: each lane sorts
+// its four best values (no indices), group scores are a merge of the lanes'
+// first two, and a round of the top-k is a maximum over the lanes, a ballot and
+// a shift of the winner's list, without a scan of the lane's experts; two tokens
+// share every instruction (a whole warp per token: 89 us where this takes 69,
+// 131072 tokens, 256 experts).  Any other shape, and
+// a token with an infinite or NaN value, takes experts lane + 32 s and scans,
 // ranking through order-preserving integer keys.  Bound by instruction issue;
 // the scores alone (an exponential and a reciprocal per expert) are a fifth.
 #include <cmath>
@@ -50,8 +52,8 @@ __device__ __forceinline__ float sigmoid(float l) {
   return r;
 }
 
-// Scores of a lane's E experts from its logits (absent experts: -inf).
-template <int E>
+// Scores of a lane's E experts from its logits (absent experts: -inf), W lanes a token.
+template <int W, int E>
 __device__ __forceinline__ void scores_of(float (&sc)[E], int sigmoids) {
   constexpr uint32_t kAll = 0xffffffffu;
   if (sigmoids) {
@@ -63,7 +65,7 @@ __device__ __forceinline__ void scores_of(float (&sc)[E], int sigmoids) {
 #pragma unroll
   for (int s = 1; s < E; ++s) m = fmaxf(m, sc[s]);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
+  for (int off = W / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
   if (m == -INFINITY) m = 0.0f;   // every logit is -inf (or NaN): scores 0 (NaN)
   float sum = 0.0f;
 #pragma unroll
@@ -72,7 +74,7 @@ __device__ __forceinline__ void scores_of(float (&sc)[E], int sigmoids) {
     sum += sc[s];
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
+  for (int off = W / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
   const float inv = sum == 0.0f ? 1.0f : 1.0f / sum;
 #pragma unroll
   for (int s = 0; s < E; ++s) sc[s] *= inv;
@@ -90,7 +92,7 @@ __device__ __noinline__ void route_row(const float* __restrict__ row, const floa
   uint32_t key[kSlots];
 #pragma unroll
   for (int s = 0; s < kSlots; ++s) sc[s] = lane + 32 * s < N ? __ldg(row + lane + 32 * s) : -INFINITY;
-  scores_of<kSlots>(sc, sigmoids);
+  scores_of<32, kSlots>(sc, sigmoids);
 #pragma unroll
   for (int s = 0; s < kSlots; ++s) {
     const int e = lane + 32 * s;
@@ -185,21 +187,21 @@ __device__ __forceinline__ void sort4(float& a, float& b, float& c, float& d) {
 // The four largest of a lane's E values, descending.
 template <int E>
 __device__ __forceinline__ void best_four(const float (&v)[E], float (&top)[4]) {
-  float lo[4] = {v[0], v[1], v[2], v[3]};
-  sort4(lo[0], lo[1], lo[2], lo[3]);
-  if (E == 8) {
-    float hi[4] = {v[E - 4], v[E - 3], v[E - 2], v[E - 1]};
-    sort4(hi[0], hi[1], hi[2], hi[3]);
-    // the larger of lo[i] and hi[3 - i] are the four largest, a bitonic sequence
 #pragma unroll
-    for (int i = 0; i < 4; ++i) lo[i] = fmaxf(lo[i], hi[3 - i]);
-    order(lo[0], lo[2]);
-    order(lo[1], lo[3]);
-    order(lo[0], lo[1]);
-    order(lo[2], lo[3]);
+  for (int i = 0; i < 4; ++i) top[i] = v[i];
+  sort4(top[0], top[1], top[2], top[3]);
+#pragma unroll
+  for (int g = 1; g < E / 4; ++g) {
+    float o[4] = {v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+    sort4(o[0], o[1], o[2], o[3]);
+    // the larger of top[i] and o[3 - i] are the four largest, a bitonic sequence
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], o[3 - i]);
+    order(top[0], top[2]);
+    order(top[1], top[3]);
+    order(top[0], top[1]);
+    order(top[2], top[3]);
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) top[i] = lo[i];
 }
 
 // Bits of a lane's `count` largest values, the last of them `last` (equal
@@ -221,62 +223,67 @@ __device__ __forceinline__ uint32_t taken(const float (&v)[E], int count, float 
   return bits;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-  float r;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
-}
-
-// E consecutive experts a lane; groups of whole lanes, a power of two of them.
-// Finite values alone: a row with an infinite or NaN value is left to
+// E consecutive experts a lane, W lanes a token; groups of 2^lanes_log2 lanes.
+// Finite values alone: a token with an infinite or NaN value is left to
 // route_row, which ranks every float.
-template <int E>
+template <int W, int E>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
     const float* __restrict__ logits, const float* __restrict__ bias, int T, int N, int k, int sigmoids, int groups,
-    int top_groups, int top2, int renormalize, float scale, int32_t* __restrict__ idx_out,
+    int lanes_log2, int top_groups, int top2, int renormalize, float scale, int32_t* __restrict__ idx_out,
     float* __restrict__ gate_out) {
   __shared__ uint32_t s_key[kRouteWarps][32 * kSlots];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long t = (long long)blockIdx.x * kRouteWarps + warp;
+  constexpr int kTokens = 32 / W;   // of a warp
   constexpr uint32_t kAll = 0xffffffffu;
-  const bool in = lane * E < N;   // N % E == 0: a lane's experts exist or do not together
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % W, me = lane / W;
+  const uint32_t mine = W == 32 ? kAll : ((1u << (W % 32)) - 1u) << (me * W);   // the token's lanes
+  const uint32_t before = mine & ((1u << lane) - 1u);                            // those before this one
+  const long long t0 = ((long long)blockIdx.x * kRouteWarps + warp) * kTokens;
+  const long long t = t0 + me;
   pdl_wait();
   pdl_trigger();
-  if (t >= T) return;
+  if (t0 >= T) return;
+  const bool in = l * E < N && t < T;   // N % E == 0: a lane's experts exist or do not together
   float sc[E], b[E];
 #pragma unroll
   for (int q = 0; q < E / 4; ++q) {
-    const float4 v = in ? __ldcs(reinterpret_cast<const float4*>(logits + t * N + lane * E) + q)
+    const float4 v = in ? __ldcs(reinterpret_cast<const float4*>(logits + t * N + l * E) + q)
                         : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     sc[4 * q] = v.x;
     sc[4 * q + 1] = v.y;
     sc[4 * q + 2] = v.z;
     sc[4 * q + 3] = v.w;
   }
-  scores_of<E>(sc, sigmoids);
+  scores_of<W, E>(sc, sigmoids);
+  float check = 0.0f;
 #pragma unroll
   for (int q = 0; q < E / 4; ++q) {
-    const float4 v = bias && in ? __ldg(reinterpret_cast<const float4*>(bias + lane * E) + q)
+    const float4 v = bias && in ? __ldg(reinterpret_cast<const float4*>(bias + l * E) + q)
                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     b[4 * q] = sc[4 * q] + v.x;
     b[4 * q + 1] = sc[4 * q + 1] + v.y;
     b[4 * q + 2] = sc[4 * q + 2] + v.z;
     b[4 * q + 3] = sc[4 * q + 3] + v.w;
+    check += fabsf(b[4 * q]) + fabsf(b[4 * q + 1]) + fabsf(b[4 * q + 2]) + fabsf(b[4 * q + 3]);
   }
-  float check = 0.0f;
+  const unsigned odd = __ballot_sync(kAll, !(check < INFINITY));
+  const bool left = (odd & mine) != 0u;   // this token is left to route_row
+  if (odd != 0u) {
+    for (int i = 0; i < kTokens; ++i) {
+      if (!(odd >> (i * W) & (kAll >> (32 - W)))) continue;
+      route_row(logits + (t0 + i) * N, bias, N, k, sigmoids, groups, top_groups, top2, renormalize, scale,
+                s_key[warp], idx_out + (t0 + i) * k, gate_out + (t0 + i) * k);
+      __syncwarp();
+    }
+    if (__all_sync(kAll, left)) return;
 #pragma unroll
-  for (int s = 0; s < E; ++s) check += fabsf(b[s]);
-  if (__any_sync(kAll, !(check < INFINITY))) {
-    route_row(logits + t * N, bias, N, k, sigmoids, groups, top_groups, top2, renormalize, scale, s_key[warp],
-              idx_out + t * k, gate_out + t * k);
-    return;
+    for (int s = 0; s < E; ++s) b[s] = left ? 0.0f : b[s];
   }
   float top[4];
   best_four<E>(b, top);
   if (!in) top[0] = top[1] = top[2] = top[3] = -INFINITY;
 
   if (groups > 1) {
-    const int lanes = N / groups / E;   // of one group
+    const int lanes = 1 << lanes_log2;   // of one group
     float x = top[0], y = top[1];
     for (int off = 1; off < lanes; off <<= 1) {
       const float ox = __shfl_xor_sync(kAll, x, off), oy = __shfl_xor_sync(kAll, y, off);
@@ -284,27 +291,28 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
       x = fmaxf(x, ox);
     }
     // the group's rank: its lanes share the comparisons with the other groups
-    const float mine = top2 ? x + y : x;
-    const int group = lane / lanes;
+    const float score = top2 ? x + y : x;
+    const int group = l >> lanes_log2;
     int better = 0;
     for (int g0 = 0; g0 < groups; g0 += lanes) {
-      const int g = g0 + lane % lanes;
-      const float o = __shfl_sync(kAll, mine, g * lanes & 31);
-      better += g < groups && (o > mine || (o == mine && g < group)) ? 1 : 0;
+      const int g = g0 + (l & (lanes - 1));
+      const float o = __shfl_sync(kAll, score, me * W + ((g << lanes_log2) & (W - 1)));
+      better += g < groups && (o > score || (o == score && g < group)) ? 1 : 0;
     }
     for (int off = 1; off < lanes; off <<= 1) better += __shfl_xor_sync(kAll, better, off);
     if (better >= top_groups) top[0] = top[1] = top[2] = top[3] = -INFINITY;
   }
 
-  uint32_t chosen = 0;          // bit s: expert lane * E + s is selected
+  uint32_t chosen = 0;          // bit s: expert l * E + s is selected
   float last = INFINITY;        // the last value this lane gave up
   int count = 0;
-  const uint32_t below = (1u << lane) - 1u;
   for (int j = 0; j < k; ++j) {
-    const float best = warp_max(top[0]);
+    float best = top[0];
+#pragma unroll
+    for (int off = W / 2; off > 0; off >>= 1) best = fmaxf(best, __shfl_xor_sync(kAll, best, off));
     const bool eq = top[0] == best;
     const unsigned who = __ballot_sync(kAll, eq);
-    if (eq && (who & below) == 0u) {   // the lowest lane: the lowest expert of equal values
+    if (eq && (who & before) == 0u) {   // the lowest lane: the lowest expert of equal values
       ++count;
       last = best;
       top[0] = top[1];
@@ -314,12 +322,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
     }
     if (E > 4 && j >= 3 && __any_sync(kAll, count == 4)) {
       // a lane's list has run out: what it gave leaves its values, and the next four come
-      const bool mine = count == 4;
-      const uint32_t bits = taken<E>(b, mine ? 4 : 0, mine ? last : INFINITY);
+      const bool out = count == 4;
+      const uint32_t bits = taken<E>(b, out ? 4 : 0, out ? last : INFINITY);
       chosen |= bits;
 #pragma unroll
       for (int s = 0; s < E; ++s) b[s] = (bits >> s) & 1u ? -INFINITY : b[s];
-      if (mine) {
+      if (out) {
         best_four<E>(b, top);
         count = 0;
         last = INFINITY;
@@ -328,24 +336,25 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
   }
   chosen |= taken<E>(b, count, last);
 
-  // slots: the selected experts of lower lanes come first
+  // slots: the selected experts of the lanes before come first
   const int n = __popc(chosen);
   int slot = 0;
 #pragma unroll
-  for (int bit = 0; bit < 4; ++bit) slot += __popc(__ballot_sync(kAll, (n >> bit) & 1) & below) << bit;
-  uint2* out = reinterpret_cast<uint2*>(s_key[warp]) + slot;   // k <= 16 slots
+  for (int bit = 0; bit < 5; ++bit) slot += __popc(__ballot_sync(kAll, (n >> bit) & 1) & before) << bit;
+  uint2* s_out = reinterpret_cast<uint2*>(s_key[warp]) + me * 16;   // k <= 16 slots a token
+  uint2* out = s_out + slot;
 #pragma unroll
   for (int s = 0; s < E; ++s)
-    if ((chosen >> s) & 1u) *out++ = make_uint2(lane * E + s, __float_as_uint(sc[s]));
+    if ((chosen >> s) & 1u) *out++ = make_uint2(l * E + s, __float_as_uint(sc[s]));
   __syncwarp();
-  const uint2 mine = lane < k ? reinterpret_cast<const uint2*>(s_key[warp])[lane] : make_uint2(0, 0);
-  float gate = __uint_as_float(mine.y), sum = gate;
+  const uint2 got = l < k ? s_out[l] : make_uint2(0, 0);
+  float gate = __uint_as_float(got.y), sum = gate;
 #pragma unroll
   for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);   // the 16 slots
   gate = scale * (renormalize ? gate / (sum + 1e-20f) : gate);
-  if (lane < k) {
-    idx_out[t * k + lane] = (int32_t)mine.x;
-    gate_out[t * k + lane] = gate;
+  if (l < k && t < T && !left) {
+    idx_out[t * k + l] = (int32_t)got.x;
+    gate_out[t * k + l] = gate;
   }
 }
 
@@ -371,18 +380,26 @@ void launch_route_scored(const float* logits, const float* bias, int T, int N, i
                          int top_groups, bool top2, bool renormalize, float scale, int32_t* topk_idx,
                          float* topk_gate, cudaStream_t s) {
   // a lane's experts lie in one group, and a group is a power of two of lanes
-  auto lanes_ok = [&](int e) {
-    if (N % e || N > 32 * e) return false;
+  auto lanes_ok = [&](int w, int e) {
+    if (N % e || N > w * e) return false;
     if (groups == 1) return true;
     const int size = N / groups;
     return size % e == 0 && (size / e & (size / e - 1)) == 0;
   };
+  auto go = [&](auto kernel, int w, int e) {
+    const int tokens = kRouteWarps * (32 / w);
+    int log2 = 0;
+    while (groups > 1 && e << log2 < N / groups) ++log2;
+    launch_pdl(kernel, dim3((T + tokens - 1) / tokens), dim3(32 * kRouteWarps), 0, s, logits, bias, T, N, k,
+               sigmoid ? 1 : 0, groups, log2, top_groups, top2 ? 1 : 0, renormalize ? 1 : 0, scale, topk_idx,
+               topk_gate);
+  };
+  if (lanes_ok(16, 4)) return go(route_lanes_kernel<16, 4>, 16, 4);
+  if (lanes_ok(16, 8)) return go(route_lanes_kernel<16, 8>, 16, 8);
+  if (lanes_ok(16, 16)) return go(route_lanes_kernel<16, 16>, 16, 16);
+  if (lanes_ok(32, 4)) return go(route_lanes_kernel<32, 4>, 32, 4);
+  if (lanes_ok(32, 8)) return go(route_lanes_kernel<32, 8>, 32, 8);
   const dim3 grid((T + kRouteWarps - 1) / kRouteWarps), block(32 * kRouteWarps);
-  if (lanes_ok(4) || lanes_ok(8)) {
-    launch_pdl(lanes_ok(4) ? route_lanes_kernel<4> : route_lanes_kernel<8>, grid, block, 0, s, logits, bias, T, N, k,
-               sigmoid ? 1 : 0, groups, top_groups, top2 ? 1 : 0, renormalize ? 1 : 0, scale, topk_idx, topk_gate);
-    return;
-  }
   launch_pdl(route_scored_kernel, grid, block, 0, s, logits, bias, T, N, k, sigmoid ? 1 : 0,
              groups, top_groups, top2 ? 1 : 0, renormalize ? 1 : 0, scale, topk_idx, topk_gate);
 }

@@ -165,6 +165,8 @@ ROUTES = [  # T, N, k, sigmoid, bias, groups, top_groups, top2, renorm
     (17, 250, 3, True, True, 25, 2, False, True),
     (9, 64, 4, False, False, 32, 7, True, True),
     (300, 96, 7, True, True, 3, 1, True, True),
+    (301, 64, 5, False, True, 4, 2, True, True),
+    (33, 256, 16, True, True, 2, 1, True, False),
     (70, 256, 16, False, True, 1, 1, False, True),
     (70, 128, 6, True, True, 32, 9, True, True),
     (70, 224, 12, True, False, 7, 2, False, False),     # a lane's list runs out (16 lanes, 12 slots)
@@ -255,6 +257,26 @@ def test_route_rows_do_not_depend_on_the_batch(moe):
     for t in (0, 400, 776):
         i1, g1 = _route(moe, l[t:t + 1], None, 6, False, 5, 2, True, True)
         assert (i1 == idx[t]).all() and (g1 == gate[t]).all()
+
+
+@pytest.mark.parametrize("N,groups", [(256, 8), (128, 4), (96, 3)])
+def test_route_odd_rows_do_not_touch_their_neighbours(moe, N, groups):
+    rng = np.random.default_rng(N)
+    l = rng.standard_normal((41, N)).astype(np.float32)
+    idx, gate = _route(moe, l, None, 5, True, groups, 2, True, True)
+    odd = l.copy()
+    odd[::3, 7] = np.nan
+    odd[1::6, 9] = -np.inf
+    bias = np.zeros(N)
+    bias[3] = -np.inf            # an expert closed for every token
+    i2, g2 = _route(moe, odd, None, 5, True, groups, 2, True, True)
+    keep = np.isfinite(odd).all(1)
+    assert (i2[keep] == idx[keep]).all() and (g2[keep] == gate[keep]).all()
+    want, wg, _ = mx_ref.route(odd, None, 5, True, groups, 2, True, True)
+    np.testing.assert_array_equal(i2, want)
+    np.testing.assert_allclose(g2, wg, rtol=2e-6)
+    i3, _ = _route(moe, l, bias, 5, True, groups, 2, True, True)
+    np.testing.assert_array_equal(i3, mx_ref.route(l, bias, 5, True, groups, 2, True, True)[0])
 
 
 # ------------------------------------------------------------------ expert FFN
