@@ -265,19 +265,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
     b[4 * q + 3] = sc[4 * q + 3] + v.w;
     check += fabsf(b[4 * q]) + fabsf(b[4 * q + 1]) + fabsf(b[4 * q + 2]) + fabsf(b[4 * q + 3]);
   }
+  // a token with such a value goes through the motions, and is routed at the end
   const unsigned odd = __ballot_sync(kAll, !(check < INFINITY));
-  const bool left = (odd & mine) != 0u;   // this token is left to route_row
-  if (odd != 0u) {
-    for (int i = 0; i < kTokens; ++i) {
-      if (!(odd >> (i * W) & (kAll >> (32 - W)))) continue;
-      route_row(logits + (t0 + i) * N, bias, N, k, sigmoids, groups, top_groups, top2, renormalize, scale,
-                s_key[warp], idx_out + (t0 + i) * k, gate_out + (t0 + i) * k);
-      __syncwarp();
-    }
-    if (__all_sync(kAll, left)) return;
-#pragma unroll
-    for (int s = 0; s < E; ++s) b[s] = left ? 0.0f : b[s];
-  }
   float top[4];
   best_four<E>(b, top);
   if (!in) top[0] = top[1] = top[2] = top[3] = -INFINITY;
@@ -335,6 +324,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
     }
   }
   chosen |= taken<E>(b, count, last);
+  const bool left = (odd & mine) != 0u;
+  if (left) chosen = 0u;
 
   // slots: the selected experts of the lanes before come first
   const int n = __popc(chosen);
@@ -355,6 +346,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
   if (l < k && t < T && !left) {
     idx_out[t * k + l] = (int32_t)got.x;
     gate_out[t * k + l] = gate;
+  }
+  if (odd != 0u) {
+    for (int i = 0; i < kTokens; ++i) {
+      if (!(odd >> (i * W) & (kAll >> (32 - W)))) continue;
+      __syncwarp();
+      route_row(logits + (t0 + i) * N, bias, N, k, sigmoids, groups, top_groups, top2, renormalize, scale,
+                s_key[warp], idx_out + (t0 + i) * k, gate_out + (t0 + i) * k);
+    }
   }
 }
 
