@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) atomicOr(args.status, kDevErrTimeout);
     }
     // all issued MMAs must be complete before TMEM is released
-    if (elect_one()) mma_commit(drain);
+    if (leader) mma_commit(drain);
     __syncwarp();
     volatile int no_abort = 0;
     mbar_wait(drain, 0, &no_abort);
@@ -808,7 +808,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         s_abort = 1;
         if (lane == 0) atomicOr(args.status, kDevErrTimeout);
       }
-      if (elect_one()) mma_commit_pair(drain, 0x1);
+      if (leader) mma_commit_pair(drain, 0x1);
       __syncwarp();
       volatile int no_abort = 0;
       mbar_wait(drain, 0, &no_abort);
@@ -1140,16 +1140,15 @@ __global__ void __launch_bounds__(kFrontThreads) mx_front_kernel(const MxFrontAr
             const uint4* src = reinterpret_cast<const uint4*>(a.codes + (size_t)max(token, 0) * (a.H / 2));
 #pragma unroll
             for (int u = 0; u < 2; ++u)
-              if (token >= 0 && p0 + 32 * u < pieces) v[j][u] = __ldg(src + p0 + 32 * u);
+              v[j][u] = token >= 0 && p0 + 32 * u < pieces ? __ldg(src + p0 + 32 * u) : make_uint4(0, 0, 0, 0);
           }
 #pragma unroll
           for (int j = 0; j < kRowsAt; ++j) {
             const int row = r0 + j * (kFrontThreads / 32);
-            const int token = row < rows ? s_token[row] : -1;
             uint4* dst = reinterpret_cast<uint4*>(a.x_perm + (size_t)(row0 + row) * (a.H / 2));
 #pragma unroll
             for (int u = 0; u < 2; ++u)
-              if (token >= 0 && p0 + 32 * u < pieces) dst[p0 + 32 * u] = v[j][u];
+              if (row < rows && p0 + 32 * u < pieces) dst[p0 + 32 * u] = v[j][u];   // no route: zeros
           }
         }
       }

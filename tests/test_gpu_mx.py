@@ -434,6 +434,27 @@ def test_expert_ffn_rows_do_not_depend_on_the_batch(moe, N):
     assert torch.equal(again, y)
 
 
+def test_expert_ffn_list_with_holes(moe):
+    """A caller's list may hold ids out of range between routes and end in blocks without a
+    route: the routed rows are what they are without them."""
+    torch = torch_()
+    L = Layer(moe, 256, 4, 2, 128, 64, seed=13)
+    T = 60
+    rng = np.random.default_rng(13)
+    c, s = (torch.from_numpy(v).cuda() for v in _tokens(rng, T, 256))
+    idx = torch.from_numpy(np.sort(np.argsort(rng.random((T, 4)), axis=1)[:, :2], axis=1).astype(np.int32)).cuda()
+    d = L.dispatch(idx)
+    y, _ = L.ffn(c, s, d)
+    ids, P = d["ids"].clone(), int(d["npad"][0])
+    keep = (ids >= 0) & (ids < 2 * T)
+    ids[1:P:9] = 2 * T                    # holes
+    ids[3:P:11] = -5
+    d2 = dict(d, ids=ids)
+    y2, _ = L.ffn(c, s, d2)
+    same = keep & (ids == d["ids"]) & (torch.arange(len(ids), device="cuda") < P)
+    assert torch.equal(y2[same], y[same])
+
+
 def test_expert_ffn_bad_block_list_does_no_work(moe):
     torch = torch_()
     L = Layer(moe, 128, 4, 1, 128, 8, seed=9)
@@ -447,6 +468,47 @@ def test_expert_ffn_bad_block_list_does_no_work(moe):
     torch.cuda.synchronize()
     assert moe.moe_get_device_status(ws) & moe.MOE_DEV_ERR_BAD_BLOCKS
     assert (y == 7.0).all()
+
+
+@pytest.mark.parametrize("T,N,k,Is", [
+    (9, 8, 2, 1024),      # swapped operands, also the shared expert
+    (70, 2, 1, 0),        # 64-column items
+    (300, 8, 2, 0),       # wider ones
+    (600, 8, 2, 14336)])  # CTA pairs
+def test_expert_ffn_waits_run_out_and_report(moe, T, N, k, Is):
+    """With a 1 ns limit a wait that one suspension does not see through gives up (the longest
+    are those for a tile of a 14336-deep reduction): the status says so, nothing hangs, and the
+    next call with the default limits gives the usual bits."""
+    torch = torch_()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    H, I, B = 4096, 14336, 16
+
+    def rand(*shape, low=0, high=256):
+        return torch.randint(low, high, shape, generator=g, device="cuda", dtype=torch.uint8)
+    L = Layer.__new__(Layer)
+    L.cfg, L.moe = moe.make_config(H, N, k, I, B, shared_intermediate=Is), moe
+    L.H, L.N, L.k, L.I, L.B, L.Is = H, N, k, I, B, Is
+    L.dev = [rand(N, 2 * I, H // 2), rand(N, 2 * I, H // 32, low=118, high=122),
+             rand(N, H, I // 2), rand(N, H, I // 32, low=118, high=122)]
+    L.dev += [rand(1, 2 * Is, H // 2), rand(1, 2 * Is, H // 32, low=118, high=122),
+              rand(1, H, Is // 2), rand(1, H, Is // 32, low=118, high=122)] if Is else [None] * 4
+    c, s = rand(T, H // 2), rand(T, H // 32, low=124, high=128)
+    idx = torch.rand(T, N, generator=g, device="cuda").topk(k, 1).indices.sort(1).values.int()
+    d = L.dispatch(idx)
+    y, ysh = L.ffn(c, s, d)
+    ws, y2 = moe.workspace_mx(L.cfg, T), torch.empty_like(y)
+    L.cfg.debug_wait_ns = 1
+    for _ in range(2):
+        moe.moe_clear_device_status(ws)
+        moe.moe_expert_ffn_mx(L.cfg, c, s, *L.dev, d["ids"], d["blocks"], d["npad"], y2,
+                              None if ysh is None else torch.empty_like(ysh), ws)
+        torch.cuda.synchronize()
+        assert moe.moe_get_device_status(ws) & moe.MOE_DEV_ERR_TIMEOUT
+    L.cfg.debug_wait_ns = 0
+    y3, ysh3 = L.ffn(c, s, d, ws)
+    assert torch.equal(y3.view(torch.int16), y.view(torch.int16))
+    assert ysh is None or torch.equal(ysh3.view(torch.int16), ysh.view(torch.int16))
 
 
 def test_expert_ffn_on_another_stream(moe):
