@@ -23,6 +23,7 @@
 // Each stage has TMEM columns of its own for its scales: they are rewritten
 // only after the commit of the MMAs that read them released the stage.
 #include <cuda_bf16.h>
+#include <algorithm>
 #include <cstdint>
 #include <type_traits>
 
@@ -971,28 +972,76 @@ void launch(const MxMaps& m, MxGemmArgs a, int64_t max_tiles, int sms, cudaStrea
 // ------------------------------------------------------------------ front
 // One launch before the GEMMs: the tile list, and the activations in tile
 // order (codes of the routed rows, and scales in the chunks that the MMAs
-// take).  Every CTA derives the experts' segments from the block list on its
-// own (one pass over it), so that nothing waits for the list: CTA 0 writes
-// it, the others copy tiles.  With identity_T there is no list and the codes
-// stay where they are.  Bound by memory and latency: the codes go through
-// L2 once more, 33 MB in 8 us for 8192 tokens x 8 of 2048 elements.
+// take).  Bound by memory (the codes once more in L2) and by chains of
+// dependent loads, so CTAs work side by side on parts that need little of each
+// other: CTA 0 writes the list; the next ones place scales, each deriving the
+// experts' segments from the block list on its own; the others copy codes,
+// which lie in the order of the routes and need no list.  With identity_T
+// there is no list and the codes stay where they are.
 constexpr int kFrontThreads = 256;
-constexpr int kFrontChunks = 16;   // scale chunks staged at once
+constexpr int kFrontWarps = kFrontThreads / 32;
+constexpr int kFrontChunks = 16;   // scale chunks of a tile placed at once
+constexpr int kFrontRows = 4;      // code rows a warp copies at once
+
+// Codes of padded rows [0, P) (zeros in a row without a route), kFrontRows rows
+// a warp, two 16-byte pieces a lane of each; the next rows' routes are under
+// way meanwhile.
+__device__ __forceinline__ void front_codes(const MxFrontArgs& a, int first, int step, int lane) {
+  const int R = (int)min((long long)a.T * a.slots, 0x7FFFFFFFll), pieces = a.H / 32;
+  auto route_at = [&](long long row) { return lane < kFrontRows && row + lane < a.max_rows ? a.sorted[row + lane] : -1; };
+  long long row0 = (long long)first * kFrontRows;
+  int id = route_at(row0);
+  const int P = *a.num_padded;
+  if (P < 0 || P > a.max_rows) return;
+  while (row0 < P) {
+    const long long next = row0 + (long long)step * kFrontRows;
+    const int id_next = route_at(next);
+    const int token = id >= 0 && id < R ? id / a.slots : -1;
+    int tok[kFrontRows];
+#pragma unroll
+    for (int j = 0; j < kFrontRows; ++j) tok[j] = __shfl_sync(0xffffffffu, token, j);
+    for (int p0 = lane; p0 < pieces; p0 += 64) {
+      uint4 v[kFrontRows][2];
+#pragma unroll
+      for (int j = 0; j < kFrontRows; ++j) {
+        const uint4* src = reinterpret_cast<const uint4*>(a.codes + (size_t)max(tok[j], 0) * (a.H / 2));
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          v[j][u] = tok[j] >= 0 && p0 + 32 * u < pieces ? __ldg(src + p0 + 32 * u) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < kFrontRows; ++j) {
+        uint4* dst = reinterpret_cast<uint4*>(a.x_perm + (size_t)(row0 + j) * (a.H / 2));
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (row0 + j < P && p0 + 32 * u < pieces) dst[p0 + 32 * u] = v[j][u];
+      }
+    }
+    row0 = next;
+    id = id_next;
+  }
+}
 
 __global__ void __launch_bounds__(kFrontThreads) mx_front_kernel(const MxFrontArgs a) {
-  __shared__ int s_first[256], s_last[256], s_used[256], s_off[257], s_scan[8];
+  __shared__ int s_first[256], s_last[256], s_used[256], s_off[257], s_scan[kFrontWarps];
   __shared__ int s_bad;
   __shared__ int s_token[kMxTileRows];
   __shared__ __align__(16) uint32_t s_sf[kFrontChunks * (kSfChunkBytes / 4)];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
+  if ((int)blockIdx.x > a.scale_ctas) {
+    const int ctas = (int)gridDim.x - 1 - a.scale_ctas;
+    front_codes(a, ((int)blockIdx.x - 1 - a.scale_ctas) * kFrontWarps + warp, ctas * kFrontWarps, lane);
+    return;
+  }
   const int sub_rows = min(a.tile_rows, kMxTileRows);   // rows of a scale tile
   const int subs = a.tile_rows / sub_rows;
   const int kchunks = a.H / kSfChunkK;
   const long long R = (long long)a.T * a.slots;
   int total;   // tiles
   if (a.identity_T) {
+    if (blockIdx.x == 0) return;
     total = (a.identity_T + a.tile_rows - 1) / a.tile_rows;
   } else {
     const int P = *a.num_padded;
@@ -1003,27 +1052,40 @@ __global__ void __launch_bounds__(kFrontThreads) mx_front_kernel(const MxFrontAr
     if (tid == 0) s_bad = bad_count ? 1 : 0;
     __syncthreads();
     // where each expert's blocks begin and end; a list out of order or range is refused
+    auto visit = [&](int b, int prev, int e) {
+      if (e < 0 || e >= a.N || prev > e) {
+        s_bad = 1;
+        return;
+      }
+      if (prev != e) {
+        s_first[e] = b;
+        if (prev >= 0) s_last[prev] = b;   // at b = 0: -1
+      }
+      if (b == nb - 1) s_last[e] = nb;
+    };
     constexpr int kUnroll = 4;
-    for (int b0 = tid; b0 < nb; b0 += kUnroll * kFrontThreads) {
-      int e[kUnroll], prev[kUnroll], next[kUnroll];
+    for (int g0 = tid; g0 < nb / 4; g0 += kUnroll * kFrontThreads) {   // four blocks a load
+      int4 e[kUnroll];
+      int prev[kUnroll];
 #pragma unroll
       for (int j = 0; j < kUnroll; ++j) {
-        const int b = b0 + j * kFrontThreads;
-        e[j] = b < nb ? a.block_expert[b] : 0;
-        prev[j] = b < nb && b > 0 ? a.block_expert[b - 1] : -1;
-        next[j] = b + 1 < nb ? a.block_expert[b + 1] : a.N;
+        const int g = min(g0 + j * kFrontThreads, nb / 4 - 1);
+        e[j] = reinterpret_cast<const int4*>(a.block_expert)[g];
+        prev[j] = g ? a.block_expert[4 * g - 1] : -1;
       }
 #pragma unroll
       for (int j = 0; j < kUnroll; ++j) {
-        const int b = b0 + j * kFrontThreads;
-        if (b >= nb) continue;
-        if (e[j] < 0 || e[j] >= a.N || prev[j] > e[j]) {
-          s_bad = 1;
-          continue;
-        }
-        if (prev[j] != e[j]) s_first[e[j]] = b;
-        if (next[j] != e[j]) s_last[e[j]] = b + 1;
+        const int b = 4 * (g0 + j * kFrontThreads);
+        if (b >= nb / 4 * 4) continue;
+        visit(b, prev[j], e[j].x);
+        visit(b + 1, e[j].x, e[j].y);
+        visit(b + 2, e[j].y, e[j].z);
+        visit(b + 3, e[j].z, e[j].w);
       }
+    }
+    if (tid < nb % 4) {
+      const int b = nb / 4 * 4 + tid;
+      visit(b, b ? a.block_expert[b - 1] : -1, a.block_expert[b]);
     }
     __syncthreads();
     if (s_bad) {
@@ -1092,11 +1154,12 @@ __global__ void __launch_bounds__(kFrontThreads) mx_front_kernel(const MxFrontAr
       return;
     }
   }
+  // scales: kFrontChunks chunks of a 128-row tile at a time, through shared memory
   total = min(total, (int)a.max_tiles);
-  const int first = a.identity_T ? (int)blockIdx.x : (int)blockIdx.x - 1;
-  const int step = a.identity_T ? (int)gridDim.x : (int)gridDim.x - 1;
-  const int pieces = a.H / 32;   // 16 bytes of codes each
-  for (long long sub = first; sub < (long long)total * subs; sub += step) {
+  const int parts = (kchunks + kFrontChunks - 1) / kFrontChunks;
+  for (long long unit = (int)blockIdx.x - 1; unit < (long long)total * subs * parts; unit += a.scale_ctas) {
+    const long long sub = unit / parts;
+    const int c0 = (int)(unit % parts) * kFrontChunks, nc = min(kFrontChunks, kchunks - c0);
     long long row0;
     int rows;
     if (a.identity_T) {
@@ -1113,7 +1176,6 @@ __global__ void __launch_bounds__(kFrontThreads) mx_front_kernel(const MxFrontAr
       row0 = (long long)s_first[lo] * a.B + (long long)(tile - s_off[lo]) * a.tile_rows + (sub % subs) * sub_rows;
       rows = (int)max(0ll, min((long long)sub_rows, (long long)s_last[lo] * a.B - row0));
     }
-    __syncthreads();   // the last round's tokens and scales are read
     if (tid < sub_rows) {
       int token = -1;
       if (tid < rows) {
@@ -1126,48 +1188,26 @@ __global__ void __launch_bounds__(kFrontThreads) mx_front_kernel(const MxFrontAr
       }
       s_token[tid] = token;
     }
+    __syncthreads();   // also: the last unit's scales are read
+    constexpr int kWords = kMxTileRows * kFrontChunks / kFrontThreads;   // words a thread, one chunk of a row each
+    uint32_t v[kWords];
+    const int c = tid % kFrontChunks;
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+      const int row = tid / kFrontChunks + j * (kFrontThreads / kFrontChunks);
+      const int token = row < sub_rows ? s_token[row] : -1;
+      v[j] = token >= 0 && c < nc
+                 ? __ldg(reinterpret_cast<const uint32_t*>(a.scales + (size_t)token * (a.H / kBlock)) + c0 + c) : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+      const int row = tid / kFrontChunks + j * (kFrontThreads / kFrontChunks);
+      s_sf[(c * kSfChunkBytes + sf_row_offset(row)) / 4] = v[j];
+    }
     __syncthreads();
-    if (!a.identity_T) {
-      // a warp copies four rows at a time, two 16-byte pieces a lane of each
-      constexpr int kRowsAt = 4;
-      for (int r0 = warp; r0 < rows; r0 += kRowsAt * (kFrontThreads / 32)) {
-        for (int p0 = lane; p0 < pieces; p0 += 64) {
-          uint4 v[kRowsAt][2];
-#pragma unroll
-          for (int j = 0; j < kRowsAt; ++j) {
-            const int row = r0 + j * (kFrontThreads / 32);
-            const int token = row < rows ? s_token[row] : -1;
-            const uint4* src = reinterpret_cast<const uint4*>(a.codes + (size_t)max(token, 0) * (a.H / 2));
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              v[j][u] = token >= 0 && p0 + 32 * u < pieces ? __ldg(src + p0 + 32 * u) : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int j = 0; j < kRowsAt; ++j) {
-            const int row = r0 + j * (kFrontThreads / 32);
-            uint4* dst = reinterpret_cast<uint4*>(a.x_perm + (size_t)(row0 + row) * (a.H / 2));
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              if (row < rows && p0 + 32 * u < pieces) dst[p0 + 32 * u] = v[j][u];   // no route: zeros
-          }
-        }
-      }
-    }
-    uint4* out = reinterpret_cast<uint4*>(a.x_sf + (size_t)sub * kchunks * kSfChunkBytes);
-    for (int c0 = 0; c0 < kchunks; c0 += kFrontChunks) {
-      const int nc = min(kFrontChunks, kchunks - c0);
-      if (c0) __syncthreads();
-      for (int i = tid; i < sub_rows * kFrontChunks; i += kFrontThreads) {
-        const int row = i / kFrontChunks, c = i % kFrontChunks;
-        const int token = s_token[row];
-        if (c < nc)
-          s_sf[(c * kSfChunkBytes + sf_row_offset(row)) / 4] =
-              token >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(a.scales + (size_t)token * (a.H / kBlock)) + c0 + c) : 0u;
-      }
-      __syncthreads();
-      for (int i = tid; i < nc * (int)(kSfChunkBytes / 16); i += kFrontThreads)
-        out[(size_t)c0 * (kSfChunkBytes / 16) + i] = reinterpret_cast<const uint4*>(s_sf)[i];
-    }
+    uint4* out = reinterpret_cast<uint4*>(a.x_sf + ((size_t)sub * kchunks + c0) * kSfChunkBytes);
+    for (int i = tid; i < nc * (int)(kSfChunkBytes / 16); i += kFrontThreads)
+      out[i] = reinterpret_cast<const uint4*>(s_sf)[i];
   }
 }
 
@@ -1209,10 +1249,15 @@ void launch_mx_gemm(bool w13, const MxMaps& m, const MxGemmArgs& a, int64_t max_
     go(launch<true, 64, false>, launch<false, 64, false>);
 }
 
-void launch_mx_front(const MxFrontArgs& a, int sms, cudaStream_t s) {
+void launch_mx_front(const MxFrontArgs& args, int sms, cudaStream_t s) {
+  // at most two CTAs an SM for the scales and three for the codes: all resident at once
+  MxFrontArgs a = args;
   const int64_t subs = a.max_tiles * (a.tile_rows > kMxTileRows ? a.tile_rows / kMxTileRows : 1);
-  const int64_t want = subs + (a.identity_T ? 0 : 1), cap = (int64_t)sms * 4;   // four CTAs an SM
-  launch_pdl(mx_front_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(kFrontThreads), 0, s, a);
+  const int64_t units = subs * ((a.H / kSfChunkK + kFrontChunks - 1) / kFrontChunks);
+  const int64_t copies = a.identity_T ? 0 : (a.max_rows + kFrontWarps * kFrontRows - 1) / (kFrontWarps * kFrontRows);
+  a.scale_ctas = (int)std::min<int64_t>(units, 2 * sms);
+  const int code_ctas = (int)std::min<int64_t>(copies, 3 * sms - 1);
+  launch_pdl(mx_front_kernel, dim3((unsigned)(1 + a.scale_ctas + code_ctas)), dim3(kFrontThreads), 0, s, a);
 }
 
 }  // namespace moe

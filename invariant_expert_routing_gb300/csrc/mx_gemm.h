@@ -63,6 +63,7 @@ struct MxFrontArgs {
   int32_t* num_tiles;
   uint8_t *x_perm, *x_sf;
   int* status;
+  int scale_ctas;                  // CTAs that place scales (set by the launcher)
 };
 void launch_mx_front(const MxFrontArgs& a, int sms, cudaStream_t s);
 
