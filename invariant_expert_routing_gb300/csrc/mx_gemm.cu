@@ -188,17 +188,39 @@ __device__ __forceinline__ bool next_item(const RingSlot* ring, uint32_t ifull0,
   return uniform(v.more) != 0;
 }
 
+// silu(g) * u.  exp and the reciprocal without the steps that keep subnormal
+// results: 1 + exp is 1 where exp(-g) is one, and a reciprocal that is one
+// counts as 0 (g below -87).
+__device__ __forceinline__ float swiglu(float g, float u) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504088896f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return g * r * u;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // a = silu(g) * u of 32 neighbouring features of one token, quantised:
 // 16 bytes of codes, one scale byte.
 __device__ __forceinline__ void store_swiglu_block(const float (&g)[32], float (&u)[32], uint8_t* codes,
                                                    uint8_t* scale) {
-  uint32_t m = 0;
+  float hi = 0.0f, lo = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    u[i] = __fdividef(g[i], 1.0f + __expf(-g[i])) * u[i];
-    m = max(m, __float_as_uint(u[i]) & 0x7FFFFFFFu);   // orders infinities and NaN above the finite values
+  for (int i = 0; i < 32; i += 2) {
+    u[i] = swiglu(g[i], u[i]);
+    u[i + 1] = swiglu(g[i + 1], u[i + 1]);
+    hi = max3(hi, u[i], u[i + 1]);   // NaN if one is
+    lo = min3(lo, u[i], u[i + 1]);
   }
-  const uint32_t byte = scale_byte(m);
+  const uint32_t byte = scale_byte(max(__float_as_uint(hi) & 0x7FFFFFFFu, __float_as_uint(lo) & 0x7FFFFFFFu));
   uint4 c = make_uint4(0, 0, 0, 0);
   if (byte != 255u) {
     const float inv = scale_inverse(byte);
@@ -485,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               if (t0 + j >= w.valid) break;
-              const float a = __fdividef(v[j], 1.0f + __expf(-v[j])) * buf[j * 32];
+              const float a = swiglu(v[j], buf[j * 32]);
               const uint32_t byte = scale_byte(__float_as_uint(warp_amax(a)) & 0x7FFFFFFFu);
               const float x = byte == 255u ? 0.0f : a * scale_inverse(byte);
               const float y = __shfl_down_sync(0xffffffffu, x, 1);
