@@ -14,14 +14,29 @@
 // and columns of an MMA are independent sums, so a token's row does not
 // depend on the batch or on the column width of the work item.
 //
-// Persistent kernel, one CTA per SM:
+// Persistent kernels, one CTA per SM:
 //   warp 0      TMA producer: codes (tensor maps) and scales (512-byte chunks)
 //   warp 1      TMEM allocation; copies the stage's scales into TMEM
 //               (tcgen05.cp) and issues the MMAs
 //   warp 2      scheduler: looks the work items up ahead of the others
-//   warps 4..11 epilogue (two warps per TMEM lane quarter)
-// Each stage has TMEM columns of its own for its scales: they are rewritten
-// only after the commit of the MMAs that read them released the stage.
+//   warps 4..   epilogue: eight warps, two per TMEM lane quarter (twelve in CTA
+//               pairs, three per quarter)
+// Each stage has TMEM columns of its own for its scales (CTA pairs: see
+// there): they are rewritten only after the commit of the MMAs that read them
+// released the stage.
+//
+// Three forms, by the average number of rows an expert has (the thresholds
+// stand at kSwapMaxRows and kPairMinRows), since what bounds them differs:
+//   few rows    operands swapped, 32-row tiles: bound by the weights' bytes.
+//               One token on 2 of 8 experts, H 4096, I 14336: W13 21 us (125 MB
+//               of codes, 6.3 TB/s with the scales), W2 15 us (4.4 TB/s: 64
+//               items; items of 64 rows on 128 SMs were 2 us slower).
+//   some rows   128-row tiles on single CTAs: weights' bytes again.  512
+//               tokens x 8 of 128 experts, H 2048, I 768: a pass 68 us, 337 MB.
+//   many rows   CTA pairs, 256-row tiles.  4096 tokens x 2 of 8 experts, H 4096,
+//               I 14336: W13 300 us (6.4 PFLOP/s), W2 170 us (5.7); 8192 x 8 of
+//               128, H 2048, I 768: W13 84 us, W2 72 us, the latter bound by its
+//               400 MB (5.5 TB/s).
 #include <cuda_bf16.h>
 #include <algorithm>
 #include <cstdint>
@@ -324,8 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     Item w;
     for (int n = 0; ok && next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim); ++n) {
-      // rows of the token box: swapped 8 or 32 (the copy engine takes about 2.5
-      // cycles a row), else 32 or 128
+      // rows of the token box: swapped 8 or 32 (with 32 for every tile a pass of one
+      // token takes 1 us more), else 32 or 128
       constexpr int kBoxMin = kSwap ? 8 : kSmallRows, kBoxMax = kSwap ? kSmallRows : kMxTileRows;
       const bool small = w.valid <= kBoxMin;
       const uint32_t a_tx = (small ? kBoxMin : kBoxMax) * 128u;
@@ -574,7 +589,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // 128 rows.  192 columns, because two accumulators and the scale columns then
 // fit into TMEM: with 256 the accumulators have to share columns, and each
 // tile's first MMA waits for the last one's epilogue to begin (about 1800
-// cycles, where a tile of K = 768 has 1700 cycles of MMAs).
+// cycles, where a tile of K = 768 has 1700 cycles of MMAs).  What holds a tile
+// back, from copies of the kernel timed without a part (8192 tokens x 8 of 128
+// experts | 4096 x 2 of 8, a whole pass of 190 | 490 us): operand loads cut to
+// 8 rows 171 | 415, without the scale copies 5 | 19 less, W13's epilogue 5 less,
+// W2's output not written 33 | 14 less; and an expert's last tile is half empty
+// on average (320 tiles where 256 would be full | 36 where 32).
 //
 // TMEM (512 columns): accumulators at 0 and 192, five slots of scale columns
 // behind them.  W13's shared memory holds two stages more than there are slots:
@@ -999,7 +1019,9 @@ void launch(const MxMaps& m, MxGemmArgs a, int64_t max_tiles, int sms, cudaStrea
 // other: CTA 0 writes the list; the next ones place scales, each deriving the
 // experts' segments from the block list on its own; the others copy codes,
 // which lie in the order of the routes and need no list.  With identity_T
-// there is no list and the codes stay where they are.
+// there is no list and the codes stay where they are.  8192 tokens x 8 of 128
+// experts, H 2048: 20 us for 137 MB through L2 (37 with a CTA to each tile for
+// codes and scales); 4096 x 2 of 8, H 4096: 8 us (40); one token: 4 us (7).
 constexpr int kFrontThreads = 256;
 constexpr int kFrontWarps = kFrontThreads / 32;
 constexpr int kFrontChunks = 16;   // scale chunks of a tile placed at once
