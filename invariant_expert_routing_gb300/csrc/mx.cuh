@@ -97,6 +97,10 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+// Bytes into L2, no answer (16-byte aligned, size % 16 == 0).
+__device__ __forceinline__ void bulk_prefetch(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 // Shared-memory descriptor of a 32 x 16-byte matrix stored without swizzle:
 // 8-row groups 128 bytes apart.
 __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {

@@ -279,6 +279,8 @@ moe_status ffn_impl(const moe_config* c, int32_t T, const uint8_t* codes, const 
   f.num_tiles = at<int32_t>(ws, L.num_tiles);
   f.x_perm = at<uint8_t>(ws, L.x_perm);
   f.x_sf = at<uint8_t>(ws, L.x_sf);
+  f.w13 = w.w13;
+  f.I = I;
   f.status = at<int>(ws, L.status);
   moe::launch_mx_front(f, sms, s);
   const uint64_t perm_rows = (uint64_t)rows + moe::kMxTileRows;

@@ -1017,8 +1017,9 @@ void launch(const MxMaps& m, MxGemmArgs a, int64_t max_tiles, int sms, cudaStrea
 // take).  Bound by memory (the codes once more in L2) and by chains of
 // dependent loads, so CTAs work side by side on parts that need little of each
 // other: CTA 0 writes the list; the next ones place scales, each deriving the
-// experts' segments from the block list on its own; the others copy codes,
-// which lie in the order of the routes and need no list.  With identity_T
+// experts' segments from the block list on its own; the next copy codes,
+// which lie in the order of the routes and need no list; and where the GEMMs
+// are bound by the weights' bytes, the last ones ask for W13's first.  With identity_T
 // there is no list and the codes stay where they are.  8192 tokens x 8 of 128
 // experts, H 2048: 20 us for 137 MB through L2 (37 with a CTA to each tile for
 // codes and scales); 4096 x 2 of 8, H 4096: 8 us (40); one token: 4 us (7).
@@ -1026,6 +1027,12 @@ constexpr int kFrontThreads = 256;
 constexpr int kFrontWarps = kFrontThreads / 32;
 constexpr int kFrontChunks = 16;   // scale chunks of a tile placed at once
 constexpr int kFrontRows = 4;      // code rows a warp copies at once
+// About what HBM delivers while the front runs (more delays W13's own loads).
+// One token on 2 of 8 experts, H 4096, I 14336 | 512 tokens x 8 of 128, H 2048,
+// I 768: none 44.0 | 68.4 us a pass; 16 MB 41.9 | 67.4, 24 MB 41.8 | 66.8, 32 MB
+// 42.6 | 67.1, 48 MB 44.0 | 66.7.  Spread over every SM: requests queue in the
+// copy engine that W13's loads pass through (H 7168, 48 MB from 28 SMs: 44 -> 58).
+constexpr int kPrefetchBytes = 24 << 20, kPrefetchPiece = 4096, kPrefetchParts = 4;
 
 // Codes of padded rows [0, P) (zeros in a row without a route), kFrontRows rows
 // a warp, two 16-byte pieces a lane of each; the next rows' routes are under
@@ -1066,6 +1073,40 @@ __device__ __forceinline__ void front_codes(const MxFrontArgs& a, int first, int
   }
 }
 
+// The codes that W13's first items read, into L2: units of 32 gate and the same
+// 32 up features, of the experts in the order of the list.
+__device__ __forceinline__ void front_prefetch(const MxFrontArgs& a, int first, int step, int lane) {
+  const int P = *a.num_padded;
+  if (P < 0 || P > a.max_rows) return;
+  const int nb = P / a.B, per = a.I / 32;
+  const size_t row = a.H / 2;
+  for (int i = first; i < a.prefetch_units * kPrefetchParts; i += step) {
+    const int unit = i / kPrefetchParts, part = i % kPrefetchParts;
+    int skip = unit / per, expert = -1;   // the expert: that many before it in the list
+    for (int b0 = 0; b0 < nb && expert < 0; b0 += 32) {
+      const int b = b0 + lane;
+      const int e = b < nb ? a.block_expert[b] : -1, prev = b < nb && b ? a.block_expert[b - 1] : -1;
+      uint32_t heads = __ballot_sync(0xffffffffu, b < nb && e != prev);
+      const int n = __popc(heads);
+      if (skip < n) {
+        for (int j = 0; j < skip; ++j) heads &= heads - 1;
+        expert = __shfl_sync(0xffffffffu, e, __ffs(heads) - 1);
+        break;
+      }
+      skip -= n;
+    }
+    if (expert < 0 || expert >= a.N) return;
+    // 32 rows are contiguous
+    const int bytes = 32 / kPrefetchParts * (int)row;
+    const uint8_t* gate = a.w13 + ((size_t)expert * 2 * a.I + (unit % per) * 32) * row + part * bytes;
+    for (int p = lane * kPrefetchPiece; p < bytes; p += 32 * kPrefetchPiece) {
+      const uint32_t n = (uint32_t)min(kPrefetchPiece, bytes - p);
+      bulk_prefetch(gate + p, n);
+      bulk_prefetch(gate + (size_t)a.I * row + p, n);
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kFrontThreads) mx_front_kernel(const MxFrontArgs a) {
   __shared__ int s_first[256], s_last[256], s_used[256], s_off[257], s_scan[kFrontWarps];
   __shared__ int s_bad;
@@ -1075,8 +1116,13 @@ __global__ void __launch_bounds__(kFrontThreads) mx_front_kernel(const MxFrontAr
   pdl_wait();
   pdl_trigger();
   if ((int)blockIdx.x > a.scale_ctas) {
-    const int ctas = (int)gridDim.x - 1 - a.scale_ctas;
-    front_codes(a, ((int)blockIdx.x - 1 - a.scale_ctas) * kFrontWarps + warp, ctas * kFrontWarps, lane);
+    const int cta = (int)blockIdx.x - 1 - a.scale_ctas;
+    const int prefetch_ctas = (int)gridDim.x - 1 - a.scale_ctas - a.code_ctas;
+    if (cta < a.code_ctas)
+      front_codes(a, cta * kFrontWarps + warp, a.code_ctas * kFrontWarps, lane);
+    else
+      front_prefetch(a, cta - a.code_ctas + warp * prefetch_ctas,
+                     prefetch_ctas * kFrontWarps, lane);
     return;
   }
   const int sub_rows = min(a.tile_rows, kMxTileRows);   // rows of a scale tile
@@ -1300,8 +1346,11 @@ void launch_mx_front(const MxFrontArgs& args, int sms, cudaStream_t s) {
   const int64_t units = subs * ((a.H / kSfChunkK + kFrontChunks - 1) / kFrontChunks);
   const int64_t copies = a.identity_T ? 0 : (a.max_rows + kFrontWarps * kFrontRows - 1) / (kFrontWarps * kFrontRows);
   a.scale_ctas = (int)std::min<int64_t>(units, 2 * sms);
-  const int code_ctas = (int)std::min<int64_t>(copies, 3 * sms - 1);
-  launch_pdl(mx_front_kernel, dim3((unsigned)(1 + a.scale_ctas + code_ctas)), dim3(kFrontThreads), 0, s, a);
+  a.code_ctas = (int)std::min<int64_t>(copies, 3 * sms - 1);
+  // where the GEMMs are bound by the weights' bytes
+  a.prefetch_units = a.identity_T || a.tile_rows > kMxTileRows ? 0 : kPrefetchBytes / (32 * a.H);
+  const int prefetch_ctas = std::min(a.prefetch_units * kPrefetchParts, sms);
+  launch_pdl(mx_front_kernel, dim3((unsigned)(1 + a.scale_ctas + a.code_ctas + prefetch_ctas)), dim3(kFrontThreads), 0, s, a);
 }
 
 }  // namespace moe

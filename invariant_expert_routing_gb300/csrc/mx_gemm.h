@@ -63,7 +63,10 @@ struct MxFrontArgs {
   int32_t* num_tiles;
   uint8_t *x_perm, *x_sf;
   int* status;
-  int scale_ctas;                  // CTAs that place scales (set by the launcher)
+  const uint8_t* w13;              // W13 codes [N, 2I, H/2]: the first of them are prefetched
+  int I;
+  int scale_ctas, code_ctas;       // CTAs that place scales and copy codes (set by the launcher)
+  int prefetch_units;              // 32 features of W13 each (set by the launcher)
 };
 void launch_mx_front(const MxFrontArgs& a, int sms, cudaStream_t s);
 
