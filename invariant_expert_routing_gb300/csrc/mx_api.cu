@@ -192,8 +192,7 @@ moe_status gemms(const moe_config* c, int H, int I, int N, const uint8_t* x, con
   const int f13 = moe::mx_tile_features(tile_rows, 2 * I, tiles_expected, sms);
   const int f2 = moe::mx_tile_features(tile_rows, H, tiles_expected, sms);
   const uint64_t sf_tiles = (uint64_t)max_tiles * scale_tiles(tile_rows);
-  const bool swap = tile_rows < moe::kMxTileRows;
-  const uint32_t box = swap ? 32 : 128, box_small = swap ? 8 : 32;   // token rows
+  const uint32_t box = 128, box_small = 32;   // token rows
   moe::MxMaps m13, m2;
   // a CTA of a pair loads half of the weight rows of an item
   if (!map_w13(&m13.w, w13, H, I, N, pair ? 32 : f13) || !map_rows(&m13.x, x, H, x_rows, box) ||

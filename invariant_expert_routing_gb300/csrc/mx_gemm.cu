@@ -28,11 +28,12 @@
 // Three forms, by the average number of rows an expert has (the thresholds
 // stand at kSwapMaxRows and kPairMinRows), since what bounds them differs:
 //   few rows    operands swapped, 32-row tiles: bound by the weights' bytes.
-//               One token on 2 of 8 experts, H 4096, I 14336: W13 21 us (125 MB
-//               of codes, 6.3 TB/s with the scales), W2 15 us (4.4 TB/s: 64
-//               items; items of 64 rows on 128 SMs were 2 us slower).
+//               One token on 2 of 8 experts, H 4096, I 14336: a pass 42 us, 187
+//               MB; of it W13 19 us (21, 6.3 TB/s, without the front's
+//               prefetch), W2 15 us (4.4 TB/s: 64 items; items of 64 rows on
+//               128 SMs were 2 us slower).
 //   some rows   128-row tiles on single CTAs: weights' bytes again.  512
-//               tokens x 8 of 128 experts, H 2048, I 768: a pass 68 us, 337 MB.
+//               tokens x 8 of 128 experts, H 2048, I 768: a pass 67 us, 337 MB.
 //   many rows   CTA pairs, 256-row tiles.  4096 tokens x 2 of 8 experts, H 4096,
 //               I 14336: W13 300 us (6.4 PFLOP/s), W2 170 us (5.7); 8192 x 8 of
 //               128, H 2048, I 768: W13 84 us, W2 72 us, the latter bound by its
@@ -57,7 +58,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kRoleWarps = 4;                        // producer, MMA issuer, scheduler, none: the epilogue starts at a lane quarter of 0
 constexpr int kThreads = (kRoleWarps + kEpiWarps) * 32;
 constexpr int kStageK = 256;                         // elements of K per stage: one 128-byte row
-constexpr int kSmallRows = 32;                       // token box of a tile with at most 32 routed rows
+constexpr int kSmallRows = 32;                       // token box of a tile with at most 32 routed rows, rows of a swapped tile
 constexpr uint32_t kSmemBudget = 226 * 1024;
 // Operands swapped where experts average at most so many rows (H 4096, I
 // 14336, 8 experts: 128 us against 136 with 16 rows, 149 against 137 with 25),
@@ -339,11 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     Item w;
     for (int n = 0; ok && next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim); ++n) {
-      // rows of the token box: swapped 8 or 32 (with 32 for every tile a pass of one
-      // token takes 1 us more), else 32 or 128
-      constexpr int kBoxMin = kSwap ? 8 : kSmallRows, kBoxMax = kSwap ? kSmallRows : kMxTileRows;
-      const bool small = w.valid <= kBoxMin;
-      const uint32_t a_tx = (small ? kBoxMin : kBoxMax) * 128u;
+      const bool small = kSwap || w.valid <= kSmallRows;   // the token box
+      const uint32_t a_tx = (small ? kSmallRows : kMxTileRows) * 128u;
       // scale tiles of B that exist (the last item of an odd number of 128-row tiles has one)
       const int sft0 = w.f * BN / kSfRows;
       const int sft = min(C::kSfbTiles, args.features / kSfRows - sft0);

@@ -32,8 +32,7 @@ struct MxGemmArgs {
 };
 
 // w: W13 5-D (K bytes, 32 rows, gate/up, 32-feature block, expert), W2 3-D (K
-// bytes, row, expert); x / x_small: activation codes, boxes of 128 and 32 rows
-// (32-row tiles: 32 and 8).
+// bytes, row, expert); x / x_small: activation codes, boxes of 128 and 32 rows.
 // CTA pairs also take the scales, as rows of one 512-byte chunk, boxes of two
 // (sfa, sfb), and the W2 output, boxes of 32 rows x 64 columns (y); their W13 box
 // is one run of 32 rows.
