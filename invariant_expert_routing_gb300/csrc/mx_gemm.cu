@@ -59,7 +59,7 @@ constexpr int kRoleWarps = 4;                        // producer, MMA issuer, sc
 constexpr int kThreads = (kRoleWarps + kEpiWarps) * 32;
 constexpr int kStageK = 256;                         // elements of K per stage: one 128-byte row
 constexpr int kSmallRows = 32;                       // token box of a tile with at most 32 routed rows, rows of a swapped tile
-constexpr uint32_t kSmemBudget = 226 * 1024;
+constexpr uint32_t kSmemLimit = 226 * 1024;
 // Operands swapped where experts average at most so many rows (H 4096, I
 // 14336, 8 experts: 128 us against 136 with 16 rows, 149 against 137 with 25),
 // CTA pairs from so many on (H 2048, I 768, 128 experts: 94 us against 95 with
@@ -86,7 +86,7 @@ struct Cfg {
   static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
   static constexpr uint32_t kXchgBytes = kSwap ? 2 * 2 * 16 * 32 * 4 : 0;   // up values handed to the gate warps
   static constexpr uint32_t kBarBytes = 512;
-  static constexpr int kFit = (int)((kSmemBudget - kBarBytes - kXchgBytes - 1024) / kStageBytes);
+  static constexpr int kFit = (int)((kSmemLimit - kBarBytes - kXchgBytes - 1024) / kStageBytes);
   static constexpr int kMaxStages = kSwap ? 9 : 8;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kCols = kSwap ? kTokens : BN;                   // columns of an accumulator
@@ -621,7 +621,7 @@ struct PairCfgMx {
   static constexpr uint32_t kSmemBytes = kStages * kStageBytes + kOutBytes + kBarBytes + 1024;
   static constexpr uint32_t kSfCols = 24;
   static constexpr uint32_t kSfCol0 = 2 * kPairN;
-  static_assert(kSmemBytes <= kSmemBudget, "stages fit");
+  static_assert(kSmemBytes <= kSmemLimit, "stages fit");
   static_assert(kSfCol0 + kSfSlots * kSfCols <= 512, "accumulators and scales fit in TMEM");
   static_assert(kStageBytes % 1024 == 0, "stages stay aligned to the swizzle atom");
 };
@@ -1305,7 +1305,7 @@ bool mx_gemm_smem_ok() {
   int dev = 0, optin = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-  return optin >= (int)kSmemBudget;
+  return optin >= (int)kSmemLimit;
 }
 
 int64_t mx_swap_max_rows(int experts) { return (int64_t)kSwapMaxRows * experts; }

@@ -434,6 +434,20 @@ def test_expert_ffn_rows_do_not_depend_on_the_batch(moe, N):
     assert torch.equal(again, y)
 
 
+@pytest.mark.parametrize("T", [8300, 8301])
+def test_expert_ffn_long_block_list(moe, T):
+    """More blocks than one round of the front's loads takes; counts that four does not divide."""
+    torch = torch_()
+    rng = np.random.default_rng(T)
+    L = Layer(moe, 128, 16, 4, 128, 8, seed=15)
+    c, s = _tokens(rng, T, 128)
+    idx = np.sort(np.argsort(rng.random((T, 16)), axis=1)[:, :4], axis=1).astype(np.int32)
+    d = L.dispatch(torch.from_numpy(idx).cuda())
+    y, _ = L.ffn(torch.from_numpy(c).cuda(), torch.from_numpy(s).cuda(), d)
+    assert int(d["npad"][0]) > 4096 * L.B
+    _check_rows(L, y, mx_ref.dequantize(c, s), d)
+
+
 def test_expert_ffn_list_with_holes(moe):
     """A caller's list may hold ids out of range between routes and end in blocks without a
     route: the routed rows are what they are without them."""
