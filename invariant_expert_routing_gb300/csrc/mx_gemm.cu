@@ -61,14 +61,14 @@ constexpr int kStageK = 256;                         // elements of K per stage:
 constexpr int kSmallRows = 32;                       // token box of a tile with at most 32 routed rows, rows of a swapped tile
 constexpr uint32_t kSmemLimit = 226 * 1024;
 // Operands swapped where experts average at most so many rows (H 4096, I
-// 14336, 8 experts: 128 us against 136 with 16 rows, 149 against 137 with 25),
-// CTA pairs from so many on (H 2048, I 768, 128 experts: 94 us against 95 with
-// 96 rows, 79 against 88 with 64, 105 against 101 with 128).
+// 14336, 8 experts: swapped 126 us against 132 with 16 rows, 142 against 132
+// with 25), CTA pairs from so many on (H 2048, I 768, 128 experts: single CTAs
+// 75 us against 83 with 64 rows, 88 against 88 with 96, 97 against 93 with 128).
 constexpr int kSwapMaxRows = 16;
 constexpr int kPairMinRows = 96;
 // Wide work items (256 weight rows, else 128, else 64) while they come to so
-// many per SM: 512 tokens x 8 of 128 experts, 5 waves of wide W13 items 73 us
-// a pass, 10 of 128 rows 70.5 us.
+// many per SM: 512 tokens x 8 of 128 experts, 5 waves of wide W13 items 69.3 us
+// a pass, 10 of 128 rows 67.4 us.
 constexpr int kMinWaves = 8;
 constexpr uint32_t kSfUnits = kSfChunkBytes >> 4;    // a scale chunk in descriptor units
 
