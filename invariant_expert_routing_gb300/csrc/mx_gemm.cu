@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem_base;
   __shared__ volatile int s_abort;
+  __shared__ int s_issued;   // operand loads the producer asked for
   __shared__ __align__(8) uint64_t s_ibar[2 * kRing];   // the ring's full, then empty barriers
   __shared__ __align__(16) RingSlot s_ring[kRing];
 
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s0 = smem_u32(smem);
     int stage = 0;
     uint32_t phase = 0;
-    int armed = 0;
+    int issued = 0;   // loads
     bool ok = true;
     Item w;
     for (int n = 0; ok && next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim); ++n) {
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bulk_load(sFb + 2 * kSfChunkBytes, sfb + ((size_t)kchunks + 2 * ks) * kSfChunkBytes, sf_bytes, fb);
         }
         __syncwarp();
-        armed = min(armed + 1, C::kStages);
+        ++issued;
         if (++stage == C::kStages) {
           stage = 0;
           phase ^= 1u;
@@ -381,19 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       s_abort = 1;
       if (lane == 0) atomicOr(args.status, kDevErrTimeout);
     }
-    if (s_abort && lane == 0) {
-      // let the copies already issued land before exit
-      volatile int no_abort = 0;
-      int s = stage;
-      uint32_t ph = phase;
-      for (int i = 0; i < armed; ++i) {
-        if (--s < 0) {
-          s = C::kStages - 1;
-          ph ^= 1u;
-        }
-        mbar_wait(full0 + 8 * s, ph, &no_abort);
-      }
-    }
+    if (lane == 0) s_issued = issued;
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -578,6 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+  if (threadIdx.x == 0 && s_abort) land_loads(full0, C::kStages, s_issued);
 }
 
 // ------------------------------------------------------------------ CTA pairs
@@ -635,6 +625,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem_base;
   __shared__ volatile int s_abort;
+  __shared__ int s_issued;   // operand loads the producer asked for
+  __shared__ volatile PairEnd s_peer;
   __shared__ __align__(8) uint64_t s_ibar[2 * kRing];   // the ring's full, then empty barriers
   __shared__ __align__(16) RingSlot s_ring[kRing];
 
@@ -704,7 +696,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t full_lead = mapa_shared(full0, 0);   // the even CTA's full barriers
     int stage = 0;
     uint32_t phase = 0;
-    int armed = 0;
+    int issued = 0;   // loads
     bool ok = true;
     Item w;
     for (int n = 0; ok && next_item(s_ring, ifull0, iempty0, n, w, ok, &s_abort, wlim); ++n) {
@@ -742,7 +734,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           tma_load_2d_pair(sFb + 2 * kSfChunkBytes, &sfb_map, 0, sfb_row + kchunks + 2 * ks, fb, pol_w);
         }
         __syncwarp();
-        armed = min(armed + 1, C::kStages);
+        ++issued;
         if (++stage == C::kStages) {
           stage = 0;
           phase ^= 1u;
@@ -753,27 +745,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       s_abort = 1;
       if (lane == 0) atomicOr(args.status, kDevErrTimeout);
     }
-    if (s_abort && lane == 0) {
-      if (lead) {
-        // copies already issued (ours and the odd CTA's) complete on our full barriers
-        volatile int no_abort = 0;
-        int s = stage;
-        uint32_t ph = phase;
-        for (int i = 0; i < armed; ++i) {
-          if (--s < 0) {
-            s = C::kStages - 1;
-            ph ^= 1u;
-          }
-          mbar_wait_cluster(full0 + 8 * s, ph, &no_abort);
-        }
-      } else {
-        // the odd CTA's copies complete on the even CTA's barriers: give any
-        // still in flight time to land in our shared memory
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 200000ull) {
-        }
-      }
-    }
+    if (lane == 0) s_issued = issued;
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
@@ -849,7 +821,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         s_abort = 1;
         if (lane == 0) atomicOr(args.status, kDevErrTimeout);
       }
-      if (leader) mma_commit_pair(drain, 0x1);
+      if (leader) mma_commit_pair(drain, 0x3);
       __syncwarp();
       volatile int no_abort = 0;
       mbar_wait(drain, 0, &no_abort);
@@ -939,7 +911,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync();   // nothing of either CTA still targets the other's shared memory
+  end_pair(lead, full0, drain, C::kStages, s_issued, s_abort, &s_peer, [](int) { return C::kStageBytes; });
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }

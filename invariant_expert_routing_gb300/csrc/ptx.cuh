@@ -4,6 +4,8 @@
 #include <cuda.h>
 #include <cstdint>
 
+#include "pipeline_end.h"
+
 namespace moe {
 
 // A bounded wait gives up after this long (ns of %globaltimer) and reports
@@ -231,6 +233,21 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
   }
 }
 
+// The same arrival with bytes to expect, on another CTA's mbarrier, and a word
+// into another CTA's shared memory.
+__device__ __forceinline__ void mbar_arrive_expect_tx_remote(uint32_t cluster_addr, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void store_cluster(uint32_t cluster_addr, int v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+// Counts bytes as arrived that no copy will bring.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 // TMA load into this CTA's shared memory that completes on an mbarrier of
 // either CTA of the pair (bar: shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* m, int32_t c0, int32_t c1,
@@ -277,6 +294,54 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t cta_mask)
           bar),
       "h"(cta_mask)
       : "memory");
+}
+
+// ---------------------------------------------------------------- the end of a GEMM's CTA
+// Thread 0 of a CTA whose roles are all done, when one of them gave up: the
+// loads already issued have landed on return (a bounded wait).
+__device__ __forceinline__ void land_loads(uint32_t full0, int stages, int issued) {
+  volatile int no_abort = 0;
+  wait_last_loads(issued, stages, [&](int stage, uint32_t parity) { mbar_wait(full0 + 8 * stage, parity, &no_abort); });
+}
+
+// What one CTA of a pair tells the other at the end.
+struct PairEnd {
+  int issued, gave_up;
+};
+
+// Every thread of both CTAs of a pair, once its roles are done (after a
+// __syncthreads): nothing still targets either CTA's shared memory on return.
+// issued: loads this CTA asked for; stage_tx(s): bytes of its last load into
+// stage s; peer_end: written by the other CTA.  full0: the full barriers, at the
+// same offset in both CTAs; drain: a barrier of each CTA that the issuing
+// thread's last commit arrives on, behind its other arrivals.
+template <class StageTx>
+__device__ __forceinline__ void end_pair(bool even, uint32_t full0, uint32_t drain, int stages, int issued, int gave_up,
+                                         volatile PairEnd* peer_end, StageTx stage_tx) {
+  volatile int no_abort = 0;
+  if (threadIdx.x == 0) {
+    const uint32_t there = mapa_shared(smem_u32(const_cast<PairEnd*>(peer_end)), even ? 1 : 0);
+    store_cluster(there, issued);
+    store_cluster(there + 4, gave_up);
+  }
+  __syncwarp();
+  cluster_sync();   // also: neither CTA issues anything from here on
+  if (gave_up || peer_end->gave_up) {   // the same in every thread of both CTAs
+    if (threadIdx.x == 0) {
+      const int peer = peer_end->issued;
+      settle_pair_loads(
+          even, issued, peer, stages, [&](int s) { mbar_complete_tx(full0 + 8 * s, stage_tx(s)); },
+          [&](int s) { mbar_arrive_expect_tx_remote(mapa_shared(full0 + 8 * s, 0), stage_tx(s)); });
+      if (even)
+        wait_last_loads(issued > peer ? issued : peer, stages, [&](int s, uint32_t parity) {
+          mbar_wait_cluster(full0 + 8 * s, parity, &no_abort);
+        });
+    }
+    __syncwarp();
+    cluster_sync();
+  }
+  if (threadIdx.x == 0) mbar_wait_cluster(drain, 0, &no_abort);
+  __syncwarp();
 }
 
 }  // namespace moe
