@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem_base;
   __shared__ volatile int s_abort;
+  __shared__ int s_issued;   // operand loads the producer asked for
   __shared__ __align__(8) uint64_t s_ibar[2 * kItemRing];   // item ring: full, then empty barriers
   __shared__ ItemSlot s_ring[kItemRing];
 
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t pol_x = policy_evict_last();
     int stage = 0;
     uint32_t phase = 0;
-    int armed = 0;  // stages armed and not yet known consumed (for the abort path)
+    int issued = 0;   // loads
     bool ok = true;
     // Items: the CTA's own index first, then from the tile counter
     // (whichever CTA is free takes the next tile) or, without one, every
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d(smem_u32(sB), small ? &x_map_small : &x_map, k0, cur.row0, fb, pol_x);
         }
         __syncwarp();
-        armed = min(armed + 1, C::kStages);
+        ++issued;
         if (++stage == C::kStages) {
           stage = 0;
           phase ^= 1u;
@@ -312,20 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       s_abort = 1;
       if (lane == 0) atomicOr(args.status, kDevErrTimeout);
     }
-    if (s_abort && lane == 0) {
-      // Let the copies already issued into shared memory land before exit:
-      // wait (bounded) for the last `armed` stages' full barriers.
-      volatile int no_abort = 0;
-      int s = stage;
-      uint32_t ph = phase;
-      for (int i = 0; i < armed; ++i) {
-        if (--s < 0) {
-          s = C::kStages - 1;
-          ph ^= 1u;
-        }
-        mbar_wait(full0 + 8 * s, ph, &no_abort);
-      }
-    }
+    if (lane == 0) s_issued = issued;
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
@@ -486,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+  if (threadIdx.x == 0 && s_abort) land_loads(full0, C::kStages, s_issued);
 }
 
 // ------------------------------------------------------------------ CTA pairs
@@ -589,6 +578,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem_base;
   __shared__ volatile int s_abort;
+  __shared__ int s_issued;   // operand loads the producer asked for
+  __shared__ uint32_t s_tx[C::kStages];   // bytes of the last load into each stage
+  __shared__ volatile PairEnd s_peer;
 
   const uint32_t rank = cluster_ctarank();            // 0: issues the MMAs
   const bool lead = rank == 0;
@@ -650,7 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint64_t pol_x = policy_evict_last();
     int stage = 0;
     uint32_t phase = 0;
-    int armed = 0;
+    int issued = 0;   // loads
     bool ok = true;
     for (int item = pair0; item < total && ok; item += pairs) {
       const Work wk = work_of<kPairRows>(args, item, num_tiles, nfe);
@@ -680,6 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t fb = mapa_shared(full0 + 8 * stage, 0);   // the even CTA's full barrier
         const int k0 = ks * kBK;
         if (lane == 0) {
+          s_tx[stage] = cta_tx;
           if (lead) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * cta_tx);
           // rows 0..63 and 64..127 of this CTA's weight tile: two 64-wide boxes
           const int c_hi = kW13 ? args.up_col + fcol : fcol + 64;
@@ -692,7 +685,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tma_load_2d_pair(smem_u32(sB), small ? &x_map_small : &x_map, k0, brow0, fb, pol_x);
         }
         __syncwarp();
-        armed = min(armed + 1, C::kStages);
+        ++issued;
         if (++stage == C::kStages) {
           stage = 0;
           phase ^= 1u;
@@ -703,28 +696,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       s_abort = 1;
       if (lane == 0) atomicOr(args.status, kDevErrTimeout);
     }
-    if (s_abort && lane == 0) {
-      if (lead) {
-        // copies already issued (ours and the odd CTA's) complete on our full
-        // barriers: let them land before exit
-        volatile int no_abort = 0;
-        int st = stage;
-        uint32_t ph = phase;
-        for (int i = 0; i < armed; ++i) {
-          if (--st < 0) {
-            st = C::kStages - 1;
-            ph ^= 1u;
-          }
-          mbar_wait_cluster(full0 + 8 * st, ph, &no_abort);
-        }
-      } else {
-        // the odd CTA's copies complete on the even CTA's barriers: give any
-        // still in flight time to land in our shared memory
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 200000ull) {
-        }
-      }
-    }
+    if (lane == 0) s_issued = issued;
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
     if (lead && lane == 0) {
@@ -785,7 +757,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         s_abort = 1;
         atomicOr(args.status, kDevErrTimeout);
       }
-      mma_commit_pair(drain, 0x1);
+      mma_commit_pair(drain, 0x3);
       volatile int no_abort = 0;
       mbar_wait(drain, 0, &no_abort);
     }
@@ -878,7 +850,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync();   // nothing of either CTA still targets the other's shared memory
+  end_pair(lead, full0, drain, C::kStages, s_issued, s_abort, &s_peer, [&](int stage) { return s_tx[stage]; });
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, C::kTmemCols);
 }

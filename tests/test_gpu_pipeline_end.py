@@ -75,3 +75,28 @@ def test_mx_ffn(T, N, k, Is):
         moe.moe_expert_ffn_mx(c, codes, scales, *w, ids, blocks, npad, y, ysh, ws)
         return [y] if ysh is None else [y, ysh]
     _check(moe, cfg, call, ws)
+
+
+@pytest.mark.parametrize("H,I,T,N,k,flags", [
+    (4096, 14336, 20, 4, 2, 0),        # CTA pairs, decode instances
+    (14336, 4096, 600, 4, 2, 0),       # CTA pairs
+    (4096, 14336, 600, 4, 2, 0),       # wide W2 items
+    (14336, 4096, 600, 4, 2, 0x2000),  # W13 on single CTAs
+    (640, 14336, 600, 4, 2, 0)])       # W2 on single CTAs
+def test_bf16_ffn(H, I, T, N, k, flags):
+    import torch
+    import invariant_expert_routing_gb300 as moe
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + I)
+    cfg = moe.make_config(H, N, k, I, 16, debug_flags=flags)
+    rand = lambda *s: 0.05 * torch.randn(*s, generator=g, device="cuda")
+    h, w13, w2 = rand(T, H).bfloat16(), rand(N, H, 2 * I).bfloat16(), rand(N, I, H).bfloat16()
+    idx = torch.rand(T, N, generator=g, device="cuda").topk(k, 1).indices.sort(1).values.int()
+    ids, blocks, npad = _dispatch(moe, cfg, idx, T, k, N)
+    ws = moe.workspace(cfg, T)
+
+    def call(c):
+        y = torch.zeros(ids.numel(), H, dtype=torch.bfloat16, device="cuda")
+        moe.moe_expert_ffn(c, h, w13, w2, None, None, ids, blocks, npad, y, None, ws)
+        return [y]
+    _check(moe, cfg, call, ws)
