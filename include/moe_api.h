@@ -547,6 +547,12 @@ moe_status moe_expert_ffn_mx(const moe_config* cfg, int32_t T, const uint8_t* x_
                              const int32_t* sorted_route_ids, const int32_t* block_expert, const int32_t* num_padded,
                              uint16_t* y_perm, uint16_t* y_shared, void* ws, size_t ws_bytes, void* stream);
 
+/* Diagnostic: token rows of a tile of moe_expert_ffn_mx's routed experts, 32, 128
+ * or 256, which follow the rows that an expert averages (T*k / N; with expert
+ * choice moe_capacity): no result bit depends on it.  0 if the configuration is
+ * invalid. */
+int32_t moe_expert_ffn_mx_tile_rows(const moe_config* cfg, int32_t T);
+
 /* A pre-norm MoE layer on 4-bit experts:
  *   v, n, MX(n) = moe_add_norm(x, residual);  logits = moe_router_logits(n)
  *   moe_route_scored -> moe_dispatch_align -> moe_expert_ffn_mx(MX(n))

@@ -122,6 +122,7 @@ _SIGS = {
     "moe_quantize_weights_mx": ([_i32, _i32, _i32] + [_vp] * 4, ctypes.c_int),
     "moe_pack_scales_mx": ([_i32, _i32, _i32, _i32] + [_vp] * 3, ctypes.c_int),
     "moe_workspace_bytes_mx": ([_cfgp, _i32], _sz),
+    "moe_expert_ffn_mx_tile_rows": ([_cfgp, _i32], _i32),
     "moe_expert_ffn_mx": ([_cfgp, _i32] + [_vp] * 16 + [_sz, _vp], ctypes.c_int),
     "moe_forward_mx": ([_cfgp, _scp, _i32] + [_vp] * 3 + [ctypes.c_float] + [_vp] * 13 + [_sz, _vp],
                        ctypes.c_int),
@@ -529,6 +530,10 @@ def moe_expert_ffn_mx(cfg, x_codes, x_scales, w13, w13_scales, w2, w2_scales, w1
         _ptr(w2_scales), _ptr(w13_shared), _ptr(w13_shared_scales), _ptr(w2_shared),
         _ptr(w2_shared_scales), _ptr(sorted_route_ids), _ptr(block_expert), _ptr(num_padded), _ptr(y_perm),
         _ptr(y_shared), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_expert_ffn_mx_tile_rows(cfg, T: int) -> int:
+    return int(_lib.moe_expert_ffn_mx_tile_rows(ctypes.byref(_cfg(cfg)), T))
 
 
 def moe_forward_mx(cfg, scoring, x, residual, norm_weight, eps, w_gate, router_bias, score_bias, w13,

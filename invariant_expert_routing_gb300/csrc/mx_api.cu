@@ -28,6 +28,29 @@ size_t sf_bytes(int64_t tiles, int K) { return (size_t)tiles * moe::kMxTileRows 
 // 128-row scale tiles under a tile of the list.
 int64_t scale_tiles(int tile_rows) { return tile_rows > moe::kMxTileRows ? tile_rows / moe::kMxTileRows : 1; }
 
+// Rows that hold a route (at most, with a capacity): what the experts average.
+// With expert choice a token has a slot for every expert but the experts take
+// `capacity` tokens each.
+int64_t routed_rows(const moe_config* c, int32_t T) {
+  if (c->routing == MOE_ROUTING_EXPERT_CHOICE) return (int64_t)c->num_experts * api::capacity(c, T);
+  return (int64_t)T * c->top_k;
+}
+
+int tile_rows_of(const moe_config* c, int32_t T) { return moe::mx_tile_rows(routed_rows(c, T), c->num_experts); }
+
+// The most tokens up to T that run with 32-row tiles.
+int32_t swap_tokens(const moe_config* c, int32_t T) {
+  int32_t lo = 0, hi = T;
+  while (lo < hi) {
+    const int32_t mid = lo + (hi - lo + 1) / 2;
+    if (routed_rows(c, mid) <= moe::mx_swap_max_rows(c->num_experts))
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
 // Workspace regions, each 256-byte aligned; the status word is at offset 0.
 struct Layout {
   size_t status, tiles, num_tiles, x_perm, x_sf, a, a_sf, x_sh_sf, a_sh, a_sh_sf,
@@ -39,11 +62,10 @@ struct Layout {
 Layout layout_of(const moe_config* c, int32_t T) {
   const size_t N = c->num_experts, H = c->hidden, I = c->intermediate, Is = c->shared_intermediate;
   const size_t R = (size_t)T * api::slots(c), rows = (size_t)api::max_rows(c, T);
-  // The tile height follows the number of routes; the regions hold the list
+  // The tile height follows the number of routed rows; the regions hold the list
   // and the scale tiles of any height that up to T tokens may take, so that a
   // workspace for T serves every smaller call.
-  const int32_t t_swap = (int32_t)std::min<int64_t>(T, moe::mx_swap_max_rows((int)N) / api::slots(c));
-  const int64_t tiles = std::max(api::max_tiles(c, t_swap, 32), api::max_tiles(c, T, moe::kMxTileRows));
+  const int64_t tiles = std::max(api::max_tiles(c, swap_tokens(c, T), 32), api::max_tiles(c, T, moe::kMxTileRows));
   const int64_t sf_tiles = std::max(tiles, 2 * api::max_tiles(c, T, 2 * moe::kMxTileRows));
   const int64_t tiles_t = 2 * (((int64_t)T + 2 * moe::kMxTileRows - 1) / (2 * moe::kMxTileRows));
   Layout L{};
@@ -255,8 +277,8 @@ moe_status ffn_impl(const moe_config* c, int32_t T, const uint8_t* codes, const 
   const Layout L = layout_of(c, T);
   const int H = c->hidden, I = c->intermediate, N = c->num_experts, slots = api::slots(c);
   const int64_t rows = api::max_rows(c, T);
-  const int64_t routes = (int64_t)T * slots;
-  const int tile_rows = moe::mx_tile_rows(routes, N);
+  const int64_t routed = routed_rows(c, T);
+  const int tile_rows = tile_rows_of(c, T);
   const int64_t max_tiles = api::max_tiles(c, T, tile_rows);
   const int sms = api::sm_count();
   if (sms <= 0 || !moe::mx_gemm_smem_ok()) return MOE_ERR_CUDA;
@@ -284,7 +306,7 @@ moe_status ffn_impl(const moe_config* c, int32_t T, const uint8_t* codes, const 
   moe::launch_mx_front(f, sms, s);
   const uint64_t perm_rows = (uint64_t)rows + moe::kMxTileRows;
   // tiles as they come: one for each expert that routes can touch, and the full ones
-  const int64_t expected = std::min<int64_t>(routes, N) + routes / tile_rows;
+  const int64_t expected = std::min<int64_t>(routed, N) + routed / tile_rows;
   MOE_TRY(gemms(c, H, I, N, f.x_perm, f.x_sf, perm_rows, w.w13, w.w13_sf, w.w2, w.w2_sf, at<uint8_t>(ws, L.a),
                 at<uint8_t>(ws, L.a_sf), perm_rows, y_perm, (uint64_t)rows, f.tiles, f.num_tiles, tile_rows, 0, max_tiles,
                 expected, sms, f.status, s));
@@ -411,6 +433,11 @@ moe_status moe_pack_scales_mx(int32_t experts, int32_t rows, int32_t K, int32_t 
 size_t moe_workspace_bytes_mx(const moe_config* cfg, int32_t max_tokens) {
   if (api::check_config(cfg) != MOE_OK || api::check_tokens(cfg, max_tokens) != MOE_OK) return 0;
   return layout_of(cfg, max_tokens).total;
+}
+
+int32_t moe_expert_ffn_mx_tile_rows(const moe_config* cfg, int32_t T) {
+  if (api::check_config(cfg) != MOE_OK || api::check_tokens(cfg, T) != MOE_OK) return 0;
+  return tile_rows_of(cfg, T);
 }
 
 moe_status moe_expert_ffn_mx(const moe_config* cfg, int32_t T, const uint8_t* x_codes, const uint8_t* x_scales,
