@@ -42,14 +42,14 @@ __device__ __forceinline__ uint4 pack_bf16(const float (&v)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// NV: 256-element chunks a warp holds.
+// NV: 256-element chunks a warp holds.  residual_out and out may be x or
+// residual (no __restrict__ on the four): a row is read before the barrier and
+// written after it.
 template <int NV>
-__global__ void __launch_bounds__(1024) add_norm_kernel(const uint16_t* __restrict__ x,
-                                                        const uint16_t* __restrict__ residual,
+__global__ void __launch_bounds__(1024) add_norm_kernel(const uint16_t* x, const uint16_t* residual,
                                                         const uint16_t* __restrict__ weight, float eps, int H,
-                                                        uint16_t* __restrict__ residual_out,
-                                                        uint16_t* __restrict__ out, uint8_t* __restrict__ codes,
-                                                        uint8_t* __restrict__ scales) {
+                                                        uint16_t* residual_out, uint16_t* out,
+                                                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   __shared__ float s_sum[kNormMaxChunks];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int chunks = (H + kNormChunk - 1) / kNormChunk;
