@@ -467,7 +467,9 @@ moe_status moe_dispatch_align_noalloc(const moe_config* cfg, int32_t T, const in
  *   codes [T, H/2] and scales [T, H/32], both or neither; out or codes given.
  * residual_out may be x or residual itself (each row is read before it is
  * written), and so may out; no other overlap.  H % 32 == 0, H <= 32768.  The sum of squares
- * has one order for every T. */
+ * has one order for every T.  It is fp32: with values past 1.8e19 it is infinite
+ * (out is 0), and with eps = 0 it may vanish (values below about 1e-23: out is
+ * infinite, and NaN where v is 0). */
 moe_status moe_add_norm(int32_t T, int32_t H, const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
                         float eps, uint16_t* residual_out, uint16_t* out, uint8_t* codes, uint8_t* scales,
                         void* stream);

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const uint16_t* x, const
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
   const float root = sqrtf(total / (float)H + eps), inv = 1.0f / root;
-  const bool finite = root <= 3.402823466e38f;   // no correction of a quotient by infinity
+  const bool normal = root > 0.0f && root <= 3.402823466e38f;   // no correction of a quotient by zero or infinity
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (warp + i * warps) * kNormChunk + lane * 8;
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const uint16_t* x, const
       // v / root with one correction: the product alone rounds twice, which
       // turns a bf16 rounding (and a 4-bit one behind it) twice as often
       const float q = v[i][j] * inv;
-      n[j] = (finite ? fmaf(fmaf(-q, root, v[i][j]), inv, q) : q) * w[j];
+      n[j] = (normal ? fmaf(fmaf(-q, root, v[i][j]), inv, q) : q) * w[j];
     }
     const uint4 nb = pack_bf16(n);
     if (in && out) *reinterpret_cast<uint4*>(out + row + c) = nb;
