@@ -503,7 +503,10 @@ moe_status moe_check_scoring(const moe_config* cfg, const moe_scoring* scoring);
  *   logits [T, N] fp32, score_bias [N] fp32 or NULL
  *   topk_idx [T, k] int32 out, experts in ascending index; topk_gate [T, k] fp32 out
  * Ties go to the lower index (of expert and of group); NaN ranks last.  A row
- * of -inf logits has softmax scores of zero. */
+ * of -inf logits has softmax scores of zero.  Scores are fp32: sigmoid is 0 below
+ * l = -88.7, softmax 0 some 104 below the largest logit, and what ranks is b, not
+ * l.  moe_route ranks by the logits, so the two may choose differently where
+ * unequal logits have equal scores. */
 moe_status moe_route_scored(const moe_config* cfg, const moe_scoring* scoring, int32_t T, const float* logits,
                             const float* score_bias, int32_t* topk_idx, float* topk_gate, void* stream);
 

@@ -45,20 +45,27 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
 }
 
-__device__ __forceinline__ float sigmoid(float l) {
-  // accurate exponential; the reciprocal is off by one unit at most, 0 for an infinite argument
+// Four times the sigmoid: the reciprocal is taken of a quarter of 1 + exp(-l), so that it is a
+// normal number wherever the exponential is finite, and the factor of a quarter, applied where
+// scores are used, brings the subnormal scores between l = -88.7 and -87.3, which still rank.
+// (131072 tokens x 256 experts: 69.9 us, 69.0 without, 70.8 with the factor here, 73.6 with a reciprocal that
+// handles subnormals itself.)  The exponential is accurate, the reciprocal off by one unit at
+// most, 0 for an infinite argument (l below -88.7).
+__device__ __forceinline__ float sigmoid4(float l) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-l)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(0.25f, expf(-l), 0.25f)));
   return r;
 }
+__device__ __forceinline__ float score_unit(int sigmoids) { return sigmoids ? 0.25f : 1.0f; }
 
-// Scores of a lane's E experts from its logits (absent experts: -inf), W lanes a token.
+// Scores of a lane's E experts from its logits (absent experts: -inf), W lanes a token, in units
+// of score_unit.
 template <int W, int E>
 __device__ __forceinline__ void scores_of(float (&sc)[E], int sigmoids) {
   constexpr uint32_t kAll = 0xffffffffu;
   if (sigmoids) {
 #pragma unroll
-    for (int s = 0; s < E; ++s) sc[s] = sigmoid(sc[s]);
+    for (int s = 0; s < E; ++s) sc[s] = sigmoid4(sc[s]);
     return;
   }
   float m = sc[0];
@@ -93,10 +100,11 @@ __device__ __noinline__ void route_row(const float* __restrict__ row, const floa
 #pragma unroll
   for (int s = 0; s < kSlots; ++s) sc[s] = lane + 32 * s < N ? __ldg(row + lane + 32 * s) : -INFINITY;
   scores_of<32, kSlots>(sc, sigmoids);
+  const float unit = score_unit(sigmoids);
 #pragma unroll
   for (int s = 0; s < kSlots; ++s) {
     const int e = lane + 32 * s;
-    key[s] = e < N ? key_of(bias ? sc[s] + __ldg(bias + e) : sc[s]) : 0u;
+    key[s] = e < N ? key_of(fmaf(unit, sc[s], bias ? __ldg(bias + e) : 0.0f)) : 0u;
   }
 
   if (groups > 1) {
@@ -156,7 +164,7 @@ __device__ __noinline__ void route_row(const float* __restrict__ row, const floa
   for (int s = 0; s < kSlots; ++s) {
     mask[s] = __ballot_sync(kAll, (chosen >> s) & 1u);
     if (renormalize)
-      for (unsigned m = mask[s]; m != 0u; m &= m - 1u) sum += __shfl_sync(kAll, sc[s], __ffs(m) - 1);
+      for (unsigned m = mask[s]; m != 0u; m &= m - 1u) sum += unit * __shfl_sync(kAll, sc[s], __ffs(m) - 1);
   }
   const float div = renormalize ? sum + 1e-20f : 1.0f;
   int base = 0;
@@ -165,7 +173,7 @@ __device__ __noinline__ void route_row(const float* __restrict__ row, const floa
     if ((chosen >> s) & 1u) {
       const int slot = base + __popc(mask[s] & ((1u << lane) - 1u));
       idx_out[slot] = lane + 32 * s;
-      gate_out[slot] = scale * (sc[s] / div);
+      gate_out[slot] = scale * (unit * sc[s] / div);
     }
     base += __popc(mask[s]);
   }
@@ -254,15 +262,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
     sc[4 * q + 3] = v.w;
   }
   scores_of<W, E>(sc, sigmoids);
+  const float unit = score_unit(sigmoids);
   float check = 0.0f;
 #pragma unroll
   for (int q = 0; q < E / 4; ++q) {
     const float4 v = bias && in ? __ldg(reinterpret_cast<const float4*>(bias + l * E) + q)
                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    b[4 * q] = sc[4 * q] + v.x;
-    b[4 * q + 1] = sc[4 * q + 1] + v.y;
-    b[4 * q + 2] = sc[4 * q + 2] + v.z;
-    b[4 * q + 3] = sc[4 * q + 3] + v.w;
+    b[4 * q] = fmaf(unit, sc[4 * q], v.x);
+    b[4 * q + 1] = fmaf(unit, sc[4 * q + 1], v.y);
+    b[4 * q + 2] = fmaf(unit, sc[4 * q + 2], v.z);
+    b[4 * q + 3] = fmaf(unit, sc[4 * q + 3], v.w);
     check += fabsf(b[4 * q]) + fabsf(b[4 * q + 1]) + fabsf(b[4 * q + 2]) + fabsf(b[4 * q + 3]);
   }
   // a token with such a value goes through the motions, and is routed at the end
@@ -339,7 +348,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
     if ((chosen >> s) & 1u) *out++ = make_uint2(l * E + s, __float_as_uint(sc[s]));
   __syncwarp();
   const uint2 got = l < k ? s_out[l] : make_uint2(0, 0);
-  float gate = __uint_as_float(got.y), sum = gate;
+  float gate = unit * __uint_as_float(got.y), sum = gate;
 #pragma unroll
   for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);   // the 16 slots
   gate = scale * (renormalize ? gate / (sum + 1e-20f) : gate);
