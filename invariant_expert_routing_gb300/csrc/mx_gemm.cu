@@ -206,7 +206,10 @@ __device__ __forceinline__ bool next_item(const RingSlot* ring, uint32_t ifull0,
 
 // silu(g) * u.  exp and the reciprocal without the steps that keep subnormal
 // results: 1 + exp is 1 where exp(-g) is one, and a reciprocal that is one
-// counts as 0 (g below -87).
+// counts as 0 (g below -87).  The exponent is one rounded product, so silu is
+// off by 2^-21 + max(-g, 0) 2^-23 of itself at most: past 2^-20 only below g =
+// -4, where silu is under a 50th of |g| and a 4-bit value keeps two bits of it.
+// The accurate exponential took 2 to 3 % of a prompt's pass.
 __device__ __forceinline__ float swiglu(float g, float u) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504088896f));
