@@ -350,8 +350,10 @@ moe_status moe_router_margin(const moe_config* cfg, int32_t T, const float* logi
  *   Is == 0); y_perm [moe_max_padded_rows, H] bf16 out; y_shared [T, H] bf16
  *   out or NULL when Is == 0 (the expert outputs are stored in bf16: half the
  *   bytes of the W2 store and of the combine's reads; every sum stays fp32).
- *   Rows of y_perm that hold the sentinel, and rows past *num_padded, are
- *   not written.
+ *   Rows of y_perm past the last route of an expert's segment (its padding),
+ *   and past *num_padded, are not written.  A list of the caller's own may
+ *   hold the sentinel or another id outside [0, T*S) before that route: such
+ *   a row is computed from a row of zeros and written (zero for finite weights).
  * One tile shape and one K order for every T, no split-K: each y row
  * depends only on its own x row and the expert's weights. */
 moe_status moe_expert_ffn(const moe_config* cfg, int32_t T, const uint16_t* h, const uint16_t* w13,
@@ -544,6 +546,7 @@ size_t moe_workspace_bytes_mx(const moe_config* cfg, int32_t max_tokens);
  *   w13_shared [2Is, H/2], w2_shared [H, Is/2] (or NULL): codes; their scales
  *   as moe_pack_scales_mx writes them
  *   sorted_route_ids, block_expert, num_padded, y_perm, y_shared: as in moe_expert_ffn
+ *   (also which rows of y_perm are written)
  * One K order and no split-K: a row does not depend on the batch. */
 moe_status moe_expert_ffn_mx(const moe_config* cfg, int32_t T, const uint8_t* x_codes, const uint8_t* x_scales,
                              const uint8_t* w13, const uint8_t* w13_scales, const uint8_t* w2,
