@@ -1,7 +1,7 @@
 // Routing by scores (sigmoid or softmax) with a selection bias, expert groups
 // and renormalised, scaled gates.
 //
-// Per token, one warp:
+// Per token:
 //   score_e = 1 / (1 + exp(-l_e))  or  exp(l_e - m) / sum_i exp(l_i - m)
 //   b_e = score_e + bias_e                       (selection only)
 //   groups of N / G consecutive experts rank by the largest b or by the sum
@@ -15,11 +15,12 @@
 // its four best values (no indices), group scores are a merge of the lanes'
 // first two, and a round of the top-k is a maximum over the lanes, a ballot and
 // a shift of the winner's list, without a scan of the lane's experts; two tokens
-// share every instruction (a whole warp per token: 89 us where this takes 69,
-// 131072 tokens, 256 experts).  Any other shape, and
-// a token with an infinite or NaN value, takes experts lane + 32 s and scans,
-// ranking through order-preserving integer keys.  Bound by instruction issue;
-// the scores alone (an exponential and a reciprocal per expert) are a fifth.
+// share every instruction (131072 tokens, 256 experts, 8 groups: 70.4 us; a
+// whole warp per token took 20 more).  Any other shape, and a token with a NaN
+// or +inf value or fewer than k values above -inf, takes experts lane + 32 s
+// and scans, ranking through order-preserving integer keys (every token so, after
+// the lanes gave it up: 304 us).  Bound by instruction issue; the scores alone
+// (an exponential and a reciprocal per expert) are a fifth.
 #include <cmath>
 #include <cstdint>
 
@@ -232,8 +233,8 @@ __device__ __forceinline__ uint32_t taken(const float (&v)[E], int count, float 
 }
 
 // E consecutive experts a lane, W lanes a token; groups of 2^lanes_log2 lanes.
-// Finite values alone: a token with an infinite or NaN value is left to
-// route_row, which ranks every float.
+// -inf is "not available": a token with a NaN or +inf value, or with -inf among
+// its k best, is left to route_row, which ranks every float.
 template <int W, int E>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
     const float* __restrict__ logits, const float* __restrict__ bias, int T, int N, int k, int sigmoids, int groups,
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
   }
   scores_of<W, E>(sc, sigmoids);
   const float unit = score_unit(sigmoids);
-  float check = 0.0f;
+  float check = 0.0f;   // NaN or +inf if a value is; -inf values alone leave it -inf
 #pragma unroll
   for (int q = 0; q < E / 4; ++q) {
     const float4 v = bias && in ? __ldg(reinterpret_cast<const float4*>(bias + l * E) + q)
@@ -272,10 +273,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
     b[4 * q + 1] = fmaf(unit, sc[4 * q + 1], v.y);
     b[4 * q + 2] = fmaf(unit, sc[4 * q + 2], v.z);
     b[4 * q + 3] = fmaf(unit, sc[4 * q + 3], v.w);
-    check += fabsf(b[4 * q]) + fabsf(b[4 * q + 1]) + fabsf(b[4 * q + 2]) + fabsf(b[4 * q + 3]);
+    check += b[4 * q] + b[4 * q + 1] + b[4 * q + 2] + b[4 * q + 3];
   }
-  // a token with such a value goes through the motions, and is routed at the end
-  const unsigned odd = __ballot_sync(kAll, !(check < INFINITY));
+  unsigned odd = __ballot_sync(kAll, !(check < INFINITY));
   float top[4];
   best_four<E>(b, top);
   if (!in) top[0] = top[1] = top[2] = top[3] = -INFINITY;
@@ -304,8 +304,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
   uint32_t chosen = 0;          // bit s: expert l * E + s is selected
   float last = INFINITY;        // the last value this lane gave up
   int count = 0;
+  float best = 0.0f;
   for (int j = 0; j < k; ++j) {
-    float best = top[0];
+    best = top[0];
 #pragma unroll
     for (int off = W / 2; off > 0; off >>= 1) best = fmaxf(best, __shfl_xor_sync(kAll, best, off));
     const bool eq = top[0] == best;
@@ -333,6 +334,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(
     }
   }
   chosen |= taken<E>(b, count, last);
+  // a token with such a value, or with fewer than k values above -inf (the last round found none),
+  // has gone through the motions and is routed below
+  odd |= __ballot_sync(kAll, best == -INFINITY && t < T);
   const bool left = (odd & mine) != 0u;
   if (left) chosen = 0u;
 
