@@ -526,7 +526,7 @@ moe_status moe_quantize_weights_mx(int32_t experts, int32_t K, int32_t F, const 
 /* Scales of an MX weight tensor [experts, rows, K/32] in the order the GEMMs
  * read them (same number of bytes; done once, when the weights are loaded).
  * gate_up = 1 for w13 and w13_shared, 0 for w2 and w2_shared.  rows % 128 ==
- * 0, K % 128 == 0. */
+ * 0, K % 128 == 0; scales and packed may not overlap (MOE_ERR_INVALID_ARG). */
 moe_status moe_pack_scales_mx(int32_t experts, int32_t rows, int32_t K, int32_t gate_up, const uint8_t* scales,
                               uint8_t* packed, void* stream);
 

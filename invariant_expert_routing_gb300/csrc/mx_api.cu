@@ -426,6 +426,9 @@ moe_status moe_pack_scales_mx(int32_t experts, int32_t rows, int32_t K, int32_t 
   if (experts == 0) return MOE_OK;
   MOE_TRY(api::need(scales));
   MOE_TRY(api::need(packed));
+  // every word moves: there is no order in which this could be done in place
+  const uint8_t* end = scales + (size_t)experts * rows * (K / kSfBlock);
+  if (packed < end && scales < packed + (end - scales)) return MOE_ERR_INVALID_ARG;
   moe::launch_pack_scales_mx(scales, experts, rows, K, gate_up != 0, packed, static_cast<cudaStream_t>(stream));
   return api::last_error();
 }
