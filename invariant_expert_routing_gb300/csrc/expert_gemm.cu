@@ -23,7 +23,8 @@
 //               warps per TMEM lane quarter, one half of the columns each)
 // Smem stages are guarded by full/empty mbarriers, the TMEM accumulators by
 // tmem_full/tmem_empty; where two buffers fit in the 512 TMEM columns (W2)
-// the epilogue of one tile overlaps the MMAs of the next.  Every wait is bounded (see mbar_wait).
+// the epilogue of one tile overlaps the MMAs of the next.  Every wait is bounded (see mbar_wait);
+// a CTA in which one ran out ends as pipeline_end.h says.
 #include <cuda_bf16.h>
 #include <cstdint>
 

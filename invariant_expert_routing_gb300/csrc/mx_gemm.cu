@@ -21,6 +21,7 @@
 //   warp 2      scheduler: looks the work items up ahead of the others
 //   warps 4..   epilogue: eight warps, two per TMEM lane quarter (twelve in CTA
 //               pairs, three per quarter)
+// Every wait is bounded; a CTA in which one ran out ends as pipeline_end.h says.
 // Each stage has TMEM columns of its own for its scales (CTA pairs: see
 // there): they are rewritten only after the commit of the MMAs that read them
 // released the stage.

@@ -7,10 +7,10 @@
 // programmatic dependency it returns at once), and pdl_trigger() to let the
 // kernel after it be scheduled early.  Every kernel launched this way calls
 // pdl_wait() before its first read of device data, so each kernel still
-// starts its work after all earlier kernels have finished.  Only kernels
-// followed by small kernels trigger early: a persistent GEMM scheduled early
-// would hold its SMs idle (and keep the shared expert's GEMMs on the second
-// stream off them) until its predecessor ends.
+// starts its work after all earlier kernels have finished.  The kernels that
+// trigger, persistent GEMMs among them, do so right after pdl_wait(): a trigger
+// takes effect once every CTA of the grid has called it or ended, so the next
+// grid's CTAs only take room that this grid has no CTA left for.
 #pragma once
 #include <cuda_runtime.h>
 
