@@ -580,7 +580,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __shared__ uint32_t s_tmem_base;
   __shared__ volatile int s_abort;
   __shared__ int s_issued;   // operand loads the producer asked for
-  __shared__ uint32_t s_tx[C::kStages];   // bytes of the last load into each stage
+  __shared__ uint32_t s_small;   // bit i: the load i before the last had the small token box
   __shared__ volatile PairEnd s_peer;
 
   const uint32_t rank = cluster_ctarank();            // 0: issues the MMAs
@@ -613,6 +613,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(drain, 1);
     s_abort = 0;
+    s_peer.gave_up = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -644,6 +645,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     int issued = 0;   // loads
+    uint32_t smalls = 0;
     bool ok = true;
     for (int item = pair0; item < total && ok; item += pairs) {
       const Work wk = work_of<kPairRows>(args, item, num_tiles, nfe);
@@ -673,7 +675,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t fb = mapa_shared(full0 + 8 * stage, 0);   // the even CTA's full barrier
         const int k0 = ks * kBK;
         if (lane == 0) {
-          s_tx[stage] = cta_tx;
           if (lead) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * cta_tx);
           // rows 0..63 and 64..127 of this CTA's weight tile: two 64-wide boxes
           const int c_hi = kW13 ? args.up_col + fcol : fcol + 64;
@@ -687,6 +688,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ++issued;
+        smalls = smalls << 1 | (small ? 1u : 0u);
         if (++stage == C::kStages) {
           stage = 0;
           phase ^= 1u;
@@ -697,7 +699,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       s_abort = 1;
       if (lane == 0) atomicOr(args.status, kDevErrTimeout);
     }
-    if (lane == 0) s_issued = issued;
+    if (lane == 0) {
+      s_issued = issued;
+      s_small = smalls;
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
     if (lead && lane == 0) {
@@ -851,7 +856,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  end_pair(lead, full0, drain, C::kStages, s_issued, s_abort, &s_peer, [&](int stage) { return s_tx[stage]; });
+  end_pair(lead, full0, drain, C::kStages, s_issued, s_abort, &s_peer, [&](int i) {
+    return C::kABytes + (kDecode || (s_small >> (s_issued - 1 - i)) & 1u ? kSmallRows : C::kRowsCta) * kBK * 2u;
+  });
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, C::kTmemCols);
 }

@@ -667,6 +667,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       mbar_init(iempty0 + 8 * i, (lead ? 2 : 1) + kPairEpiWarps);
     }
     s_abort = 0;
+    s_peer.gave_up = 0;
     fence_mbar_init();
   }
   if (warp == 1) {

@@ -31,14 +31,14 @@ MOE_HD void wait_last_loads(int issued, int stages, Wait wait) {
 }
 
 // A CTA of a pair, `mine` and `peer` the loads that it and the other issued:
-// complete(stage) on the even CTA, arm(stage) on the odd one.
+// complete(load) on the even CTA, arm(load) on the odd one.
 template <class Complete, class Arm>
-MOE_HD void settle_pair_loads(bool even, int mine, int peer, int stages, Complete complete, Arm arm) {
+MOE_HD void settle_pair_loads(bool even, int mine, int peer, Complete complete, Arm arm) {
   for (int i = peer; i < mine; ++i) {
     if (even)
-      complete(i % stages);
+      complete(i);
     else
-      arm(i % stages);
+      arm(i);
   }
 }
 

@@ -304,34 +304,36 @@ __device__ __forceinline__ void land_loads(uint32_t full0, int stages, int issue
   wait_last_loads(issued, stages, [&](int stage, uint32_t parity) { mbar_wait(full0 + 8 * stage, parity, &no_abort); });
 }
 
-// What one CTA of a pair tells the other at the end.
+// What one CTA of a pair tells the other at the end (gave_up: 0 from before the
+// pair's first cluster barrier).
 struct PairEnd {
   int issued, gave_up;
 };
 
 // Every thread of both CTAs of a pair, once its roles are done (after a
 // __syncthreads): nothing still targets either CTA's shared memory on return.
-// issued: loads this CTA asked for; stage_tx(s): bytes of its last load into
-// stage s; peer_end: written by the other CTA.  full0: the full barriers, at the
+// issued: loads this CTA asked for; load_tx(i): bytes of the i-th, one of the last
+// `stages`; peer_end: written by the other CTA.  full0: the full barriers, at the
 // same offset in both CTAs; drain: a barrier of each CTA that the issuing
-// thread's last commit arrives on, behind its other arrivals.
-template <class StageTx>
+// thread's last commit arrives on, behind its other arrivals.  A pair in which
+// nothing gave up stores nothing remotely: the cluster barrier would wait for it.
+template <class LoadTx>
 __device__ __forceinline__ void end_pair(bool even, uint32_t full0, uint32_t drain, int stages, int issued, int gave_up,
-                                         volatile PairEnd* peer_end, StageTx stage_tx) {
+                                         volatile PairEnd* peer_end, LoadTx load_tx) {
   volatile int no_abort = 0;
-  if (threadIdx.x == 0) {
-    const uint32_t there = mapa_shared(smem_u32(const_cast<PairEnd*>(peer_end)), even ? 1 : 0);
-    store_cluster(there, issued);
-    store_cluster(there + 4, gave_up);
-  }
+  const uint32_t there = mapa_shared(smem_u32(const_cast<PairEnd*>(peer_end)), even ? 1 : 0);
+  if (threadIdx.x == 0 && gave_up) store_cluster(there + 4, 1);
   __syncwarp();
   cluster_sync();   // also: neither CTA issues anything from here on
   if (gave_up || peer_end->gave_up) {   // the same in every thread of both CTAs
+    if (threadIdx.x == 0) store_cluster(there, issued);
+    __syncwarp();
+    cluster_sync();
     if (threadIdx.x == 0) {
       const int peer = peer_end->issued;
       settle_pair_loads(
-          even, issued, peer, stages, [&](int s) { mbar_complete_tx(full0 + 8 * s, stage_tx(s)); },
-          [&](int s) { mbar_arrive_expect_tx_remote(mapa_shared(full0 + 8 * s, 0), stage_tx(s)); });
+          even, issued, peer, [&](int i) { mbar_complete_tx(full0 + 8 * (i % stages), load_tx(i)); },
+          [&](int i) { mbar_arrive_expect_tx_remote(mapa_shared(full0 + 8 * (i % stages), 0), load_tx(i)); });
       if (even)
         wait_last_loads(issued > peer ? issued : peer, stages, [&](int s, uint32_t parity) {
           mbar_wait_cluster(full0 + 8 * s, parity, &no_abort);

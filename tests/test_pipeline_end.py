@@ -55,13 +55,10 @@ int run(std::mt19937& g, bool pair) {
         if (used < even && (!pair || used < odd) && bars[used % S].done((unsigned)(used / S) & 1u)) ++used;
     }
   }
-  std::vector<long> last_even(S), last_odd(S);
-  for (int i = 0; i < even; ++i) last_even[i % S] = tx[i];
-  for (int i = 0; i < odd; ++i) last_odd[i % S] = tx[i];
   if (pair) {
     auto never = [](int) { std::puts("the wrong side"); std::exit(1); };
-    moe::settle_pair_loads(true, even, odd, S, [&](int s) { bars[s].complete(last_even[s]); }, never);
-    moe::settle_pair_loads(false, odd, even, S, never, [&](int s) { bars[s].arm(last_odd[s]); });
+    moe::settle_pair_loads(true, even, odd, [&](int i) { bars[i % S].complete(tx[i]); }, never);
+    moe::settle_pair_loads(false, odd, even, never, [&](int i) { bars[i % S].arm(tx[i]); });
   }
   std::vector<std::pair<int, unsigned>> waits;
   moe::wait_last_loads(even > odd ? even : odd, S, [&](int s, unsigned parity) { waits.push_back({s, parity}); });
