@@ -575,6 +575,125 @@ moe_status moe_forward_mx(const moe_config* cfg, const moe_scoring* scoring, int
                           const uint8_t* w13_shared, const uint8_t* w13_shared_scales, const uint8_t* w2_shared,
                           const uint8_t* w2_shared_scales, uint16_t* out, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The layer's training step on bf16 experts: the products grouped by expert
+ * with the gradients of their inputs and weights, SwiGLU with the gates and
+ * its gradient, layer norm, and the gradients of both norms.
+ *
+ * A forward that keeps what the gradient needs, and its gradient (S = slots
+ * per token, H -> 2I -> H; ids and counts from moe_dispatch_align or
+ * moe_route_expert_choice):
+ *   gu    = moe_grouped_gemm(h, w13, GATHER)              [rows, 2I]
+ *   a     = moe_swiglu(gu, gates)                         [rows, I]
+ *   y     = moe_grouped_gemm(a, w2)                       [rows, H]
+ *   out   = moe_combine(h, gates of 1, y)
+ *   dw2   = moe_grouped_wgrad(a, dout, GATHER_DY)
+ *   da    = moe_grouped_gemm(dout, w2, GATHER | TRANSPOSED)
+ *   dgu, dgate = moe_swiglu_backward(gu, gates, da)
+ *   dw13  = moe_grouped_wgrad(h, dgu, GATHER_X)
+ *   dx    = moe_grouped_gemm(dgu, w13, TRANSPOSED)        [rows, H]
+ *   dh    = moe_combine(dout, gates of 1, dx)
+ *
+ * Rows are grouped as the dispatch lays them out: expert e's segment starts
+ * at the sum of the earlier experts' expert_counts, each rounded up to a
+ * multiple of B, and holds expert_counts[e] rows.  A gathered operand is
+ * [T, columns]: row p of the segment reads its row sorted_route_ids[p] / S (an
+ * id outside [0, T*S) reads zeros).  An operand in place is [rows, columns],
+ * rows = moe_max_padded_rows(cfg, T).  Rows of the padding are neither read
+ * nor written, whatever they hold.  Counts that are negative or need more than
+ * rows rows set MOE_DEV_ERR_BAD_BLOCKS and nothing is computed.
+ * cfg gives N, B, the slots and the bound on the rows; K and F are multiples
+ * of 8 up to 65536, free of cfg's hidden and intermediate.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of workspace of moe_grouped_gemm and moe_grouped_wgrad for up to
+ * max_tokens tokens (0 if the configuration is invalid): the device status
+ * word at its start, nothing kept from call to call. */
+size_t moe_workspace_bytes_grouped(const moe_config* cfg, int32_t max_tokens);
+
+/* y_perm[p] = bf16(x[row(p)] . W_e), fp32 accumulation, for every row p of
+ * every expert e's segment.
+ *   x [T, K] (GATHER) or [rows, K] bf16;  y_perm [rows, F] bf16 out
+ *   w [N, K, F] bf16, with TRANSPOSED [N, F, K] (the product with W_e^T: the
+ *   gradient of the input of a product with w [N, F, K])
+ * sorted_route_ids may be NULL without GATHER.  y_perm may not overlap x or w.
+ * One K order for every T, no split-K: a row does not depend on the batch. */
+#define MOE_GROUPED_GATHER 0x1u
+#define MOE_GROUPED_TRANSPOSED 0x2u
+moe_status moe_grouped_gemm(const moe_config* cfg, int32_t T, int32_t K, int32_t F, uint32_t flags, const uint16_t* x,
+                            const uint16_t* w, const int32_t* sorted_route_ids, const int32_t* expert_counts,
+                            uint16_t* y_perm, void* ws, size_t ws_bytes, void* stream);
+
+/* dw[e] = dw_add[e] + sum over the rows p of expert e's segment of
+ * x[row(p)]^T dy[row(p)], in ascending p (fp32 accumulation, no atomics: the
+ * same bits on every run).  An expert without rows gets dw_add or zeros.
+ *   x  [T, K] (GATHER_X) or [rows, K] bf16, dy [T, F] (GATHER_DY) or [rows, F]
+ *   dw [N, K, F] fp32 out, with BF16 bf16 (rounded once)
+ *   dw_add [N, K, F] fp32 or NULL, may be dw itself (no other overlap); not
+ *   with BF16
+ * T = 0 writes dw too: dw_add or zeros. */
+#define MOE_WGRAD_GATHER_X 0x1u
+#define MOE_WGRAD_GATHER_DY 0x2u
+#define MOE_WGRAD_BF16 0x4u
+moe_status moe_grouped_wgrad(const moe_config* cfg, int32_t T, int32_t K, int32_t F, uint32_t flags, const uint16_t* x,
+                             const uint16_t* dy, const int32_t* sorted_route_ids, const int32_t* expert_counts,
+                             const float* dw_add, void* dw, void* ws, size_t ws_bytes, void* stream);
+
+/* a[p] = bf16(w silu(g) u) for every row p < *num_padded whose route
+ * r = sorted_route_ids[p] is in [0, T*S): g, u the halves of gu[p], silu(g) =
+ * g / (1 + e^-g), w = topk_gate[r] (1 if topk_gate is NULL).  Other rows of a
+ * are not written.
+ *   gu [rows, 2I] bf16 (I = cfg->intermediate; the output of moe_grouped_gemm
+ *   with w13), topk_gate [T, S] fp32 or NULL, a [rows, I] bf16 out, no overlap.
+ * With the gate here the second product needs none: moe_combine then runs
+ * with gates of 1. */
+moe_status moe_swiglu(const moe_config* cfg, int32_t T, const uint16_t* gu, const float* topk_gate,
+                      const int32_t* sorted_route_ids, const int32_t* num_padded, uint16_t* a, void* stream);
+
+/* The gradient of moe_swiglu: with s = 1 / (1 + e^-g), per row
+ *   dgu = bf16[ w da u s (1 + g (1 - s)) | w da silu(g) ]
+ *   dgate[r] = sum over I of da silu(g) u   (fp32, one order for every T)
+ *   a as in moe_swiglu (the activation need not be kept for the weight gradient)
+ *   da [rows, I] bf16, dgu [rows, 2I] bf16 out, dgate [T, S] fp32 out or NULL
+ *   (entries of routes that are in no row are not written), a [rows, I] bf16
+ *   out or NULL.
+ * dgu may be gu and a may be da; no other overlap. */
+moe_status moe_swiglu_backward(const moe_config* cfg, int32_t T, const uint16_t* gu, const float* topk_gate,
+                               const uint16_t* da, const int32_t* sorted_route_ids, const int32_t* num_padded,
+                               uint16_t* dgu, float* dgate, uint16_t* a, void* stream);
+
+/* Residual addition and layer norm:
+ *   v = x + residual (fp32);  residual_out = bf16(v)
+ *   out = bf16((v - mean(v)) / sqrt(var(v) + eps) * weight + bias)
+ *   x, residual [T, H] bf16 (residual NULL: v = x), weight [H] bf16, bias [H]
+ *   bf16 or NULL, residual_out [T, H] bf16 or NULL, out [T, H] bf16.
+ * var is the mean square of the deviations from the mean, computed from them.
+ * residual_out may be x or residual itself, and so may out; no other overlap.
+ * H % 8 == 0, H <= 32768.  Sums are fp32 in one order for every T; with eps = 0
+ * a row of equal values gives NaN. */
+moe_status moe_add_layer_norm(int32_t T, int32_t H, const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
+                              const uint16_t* bias, float eps, uint16_t* residual_out, uint16_t* out, void* stream);
+
+/* Bytes of workspace of moe_norm_backward (0 if T or H is invalid). */
+size_t moe_workspace_bytes_norm_backward(int32_t max_tokens, int32_t H);
+
+/* The gradient of moe_add_layer_norm (centre = 1) or moe_add_norm (centre =
+ * 0) with respect to v and the parameters:
+ *   n = (v - mean) / root, root = sqrt(var + eps) (RMS norm: mean = 0, var =
+ *   mean(v^2)); g = dout * weight
+ *   dx = bf16(dresidual + (g - mean(g) - n mean(g n)) / root)  (RMS norm
+ *   without mean(g)): the gradient of x and of residual
+ *   dweight = sum over t of dout n;  dbias = sum over t of dout
+ *   v [T, H] bf16 (the forward's residual_out, or x without a residual), dout
+ *   [T, H] bf16, dresidual [T, H] bf16 or NULL (the gradient of residual_out),
+ *   weight [H] bf16, dx [T, H] bf16 out, dweight, dbias [H] fp32 out or NULL.
+ * The statistics are computed again from v.  dx may be dresidual; no other
+ * overlap.  The sums over rows have one order for a given T, H and number of
+ * SMs, without atomics.  T = 0 sets dweight and dbias to zero.  H as above. */
+moe_status moe_norm_backward(int32_t T, int32_t H, int32_t centre, const uint16_t* v, const uint16_t* dout,
+                             const uint16_t* dresidual, const uint16_t* weight, float eps, uint16_t* dx, float* dweight,
+                             float* dbias, void* ws, size_t ws_bytes, void* stream);
+
 /* Reads the device status word of `ws` (synchronises `stream`): the whole word
  * in *status_out; MOE_ERR_DEVICE if any bit of MOE_DEV_ERR_MASK is set. */
 moe_status moe_get_device_status(const void* ws, int32_t* status_out, void* stream);

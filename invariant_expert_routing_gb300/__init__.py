@@ -55,6 +55,11 @@ MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
 MOE_GROUP_MAX = 0
 MOE_GROUP_TOP2_SUM = 1
+MOE_GROUPED_GATHER = 0x1
+MOE_GROUPED_TRANSPOSED = 0x2
+MOE_WGRAD_GATHER_X = 0x1
+MOE_WGRAD_GATHER_DY = 0x2
+MOE_WGRAD_BF16 = 0x4
 
 
 class moe_config(ctypes.Structure):
@@ -126,6 +131,14 @@ _SIGS = {
     "moe_expert_ffn_mx": ([_cfgp, _i32] + [_vp] * 16 + [_sz, _vp], ctypes.c_int),
     "moe_forward_mx": ([_cfgp, _scp, _i32] + [_vp] * 3 + [ctypes.c_float] + [_vp] * 13 + [_sz, _vp],
                        ctypes.c_int),
+    "moe_workspace_bytes_grouped": ([_cfgp, _i32], _sz),
+    "moe_grouped_gemm": ([_cfgp, _i32, _i32, _i32, ctypes.c_uint32] + [_vp] * 6 + [_sz, _vp], ctypes.c_int),
+    "moe_grouped_wgrad": ([_cfgp, _i32, _i32, _i32, ctypes.c_uint32] + [_vp] * 7 + [_sz, _vp], ctypes.c_int),
+    "moe_swiglu": ([_cfgp, _i32] + [_vp] * 6, ctypes.c_int),
+    "moe_swiglu_backward": ([_cfgp, _i32] + [_vp] * 9, ctypes.c_int),
+    "moe_add_layer_norm": ([_i32, _i32] + [_vp] * 4 + [ctypes.c_float] + [_vp] * 3, ctypes.c_int),
+    "moe_workspace_bytes_norm_backward": ([_i32, _i32], _sz),
+    "moe_norm_backward": ([_i32, _i32, _i32] + [_vp] * 4 + [ctypes.c_float] + [_vp] * 4 + [_sz, _vp], ctypes.c_int),
     "moe_get_device_status": ([_vp, ctypes.POINTER(_i32), _vp], ctypes.c_int),
     "moe_clear_device_status": ([_vp, _vp], ctypes.c_int),
 }
@@ -556,3 +569,133 @@ def moe_forward_mx(cfg, scoring, x, residual, norm_weight, eps, w_gate, router_b
         float(eps), _ptr(w_gate), _ptr(router_bias), _ptr(score_bias), _ptr(w13), _ptr(w13_scales),
         _ptr(w2), _ptr(w2_scales), _ptr(w13_shared), _ptr(w13_shared_scales), _ptr(w2_shared),
         _ptr(w2_shared_scales), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+# ---- the layer's training step on bf16 experts
+
+def moe_workspace_bytes_grouped(cfg, max_tokens: int) -> int:
+    return int(_lib.moe_workspace_bytes_grouped(ctypes.byref(_cfg(cfg)), max_tokens))
+
+
+def workspace_grouped(cfg, max_tokens: int, device="cuda"):
+    """A torch uint8 tensor for moe_grouped_gemm and moe_grouped_wgrad with up to max_tokens tokens,
+    its status word cleared."""
+    import torch
+    n = moe_workspace_bytes_grouped(cfg, max_tokens)
+    if n == 0:
+        raise MoEError("moe_workspace_bytes_grouped", MOE_ERR_UNSUPPORTED)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _slots(c):
+    return c.num_experts if c.routing == MOE_ROUTING_EXPERT_CHOICE else c.top_k
+
+
+def _want_rows(name, t, c, T, gathered):
+    """The address and the columns of a [T, columns] (gathered) or [padded rows, columns] bf16 tensor."""
+    if t is None or t.dim() != 2:
+        raise ValueError(f"{name}: a 2-D tensor is needed")
+    return _want(name, t, "bfloat16", (T if gathered else moe_max_padded_rows(c, T), t.shape[1])), t.shape[1]
+
+
+def _want_groups(c, T, sorted_route_ids, expert_counts, ws, gathered):
+    ids = None
+    if gathered or sorted_route_ids is not None:
+        ids = _want_at_least("sorted_route_ids", sorted_route_ids, "int32", moe_max_padded_rows(c, T))
+    return (ids, _want("expert_counts", expert_counts, "int32", (c.num_experts,)),
+            _want_at_least("ws", ws, "uint8", 1))
+
+
+def moe_grouped_gemm(cfg, T, x, w, sorted_route_ids, expert_counts, y_perm, ws, gather=False, transposed=False,
+                     stream=None):
+    """y_perm [rows, F] = x . w[e] for every row of expert e's segment; x [T, K] (gather) or
+    [rows, K], w [N, K, F] (transposed: [N, F, K], the product with its transpose), all bf16."""
+    c = _cfg(cfg)
+    px, K = _want_rows("x", x, c, T, gather)
+    py, F = _want_rows("y_perm", y_perm, c, T, False)
+    pw = _want("w", w, "bfloat16", (c.num_experts, F, K) if transposed else (c.num_experts, K, F))
+    ids, counts, pws = _want_groups(c, T, sorted_route_ids, expert_counts, ws, gather)
+    flags = (MOE_GROUPED_GATHER if gather else 0) | (MOE_GROUPED_TRANSPOSED if transposed else 0)
+    _check("moe_grouped_gemm", _lib.moe_grouped_gemm(ctypes.byref(c), T, K, F, flags, px, pw, ids, counts, py, pws,
+                                                     ws.numel(), _stream(stream)))
+
+
+def moe_grouped_wgrad(cfg, T, x, dy, sorted_route_ids, expert_counts, dw, ws, dw_add=None, gather_x=False,
+                      gather_dy=False, stream=None):
+    """dw [N, K, F] (fp32 or bf16) = dw_add + x^T dy over every expert's rows; x [T, K] (gather_x)
+    or [rows, K], dy [T, F] (gather_dy) or [rows, F] bf16; dw_add fp32 (dw fp32), may be dw."""
+    c = _cfg(cfg)
+    px, K = _want_rows("x", x, c, T, gather_x)
+    pdy, F = _want_rows("dy", dy, c, T, gather_dy)
+    shape = (c.num_experts, K, F)
+    bf16 = dw is not None and dw.dtype is _dtypes["bfloat16"]
+    pdw = _want("dw", dw, "bfloat16" if bf16 else "float32", shape)
+    padd = _want("dw_add", dw_add, "float32", shape, optional=True)
+    ids, counts, pws = _want_groups(c, T, sorted_route_ids, expert_counts, ws, gather_x or gather_dy)
+    flags = ((MOE_WGRAD_GATHER_X if gather_x else 0) | (MOE_WGRAD_GATHER_DY if gather_dy else 0)
+             | (MOE_WGRAD_BF16 if bf16 else 0))
+    _check("moe_grouped_wgrad", _lib.moe_grouped_wgrad(ctypes.byref(c), T, K, F, flags, px, pdy, ids, counts, padd,
+                                                       pdw, pws, ws.numel(), _stream(stream)))
+
+
+def _want_swiglu(c, T, gu, topk_gate, sorted_route_ids, num_padded):
+    rows = moe_max_padded_rows(c, T)
+    return (rows, _want("gu", gu, "bfloat16", (rows, 2 * c.intermediate)),
+            _want("topk_gate", topk_gate, "float32", (T, _slots(c)), True),
+            _want_at_least("sorted_route_ids", sorted_route_ids, "int32", rows),
+            _want_at_least("num_padded", num_padded, "int32", 1))
+
+
+def moe_swiglu(cfg, T, gu, topk_gate, sorted_route_ids, num_padded, a, stream=None):
+    """a [rows, I] = gate * silu(g) * u from gu [rows, 2I]; topk_gate [T, S] or None."""
+    c = _cfg(cfg)
+    rows, pgu, gate, ids, npad = _want_swiglu(c, T, gu, topk_gate, sorted_route_ids, num_padded)
+    _check("moe_swiglu", _lib.moe_swiglu(ctypes.byref(c), T, pgu, gate, ids, npad,
+                                         _want("a", a, "bfloat16", (rows, c.intermediate)), _stream(stream)))
+
+
+def moe_swiglu_backward(cfg, T, gu, topk_gate, da, sorted_route_ids, num_padded, dgu, dgate=None, a=None, stream=None):
+    """dgu [rows, 2I], dgate [T, S] fp32 and the activation a from da [rows, I]; dgate and a may be None."""
+    c = _cfg(cfg)
+    rows, pgu, gate, ids, npad = _want_swiglu(c, T, gu, topk_gate, sorted_route_ids, num_padded)
+    one = (rows, c.intermediate)
+    _check("moe_swiglu_backward", _lib.moe_swiglu_backward(
+        ctypes.byref(c), T, pgu, gate, _want("da", da, "bfloat16", one), ids, npad,
+        _want("dgu", dgu, "bfloat16", (rows, 2 * c.intermediate)),
+        _want("dgate", dgate, "float32", (T, _slots(c)), True), _want("a", a, "bfloat16", one, True), _stream(stream)))
+
+
+def moe_add_layer_norm(x, residual, weight, bias, eps, residual_out, out, stream=None):
+    """x [T, H] bf16 (+ residual) -> residual_out and the layer norm out, [T, H] bf16; residual, bias
+    and residual_out may be None."""
+    shape = T, H = x.shape
+    _check("moe_add_layer_norm", _lib.moe_add_layer_norm(
+        T, H, _want("x", x, "bfloat16", shape), _want("residual", residual, "bfloat16", shape, True),
+        _want("weight", weight, "bfloat16", (H,)), _want("bias", bias, "bfloat16", (H,), True), eps,
+        _want("residual_out", residual_out, "bfloat16", shape, True), _want("out", out, "bfloat16", shape),
+        _stream(stream)))
+
+
+def moe_workspace_bytes_norm_backward(max_tokens: int, H: int) -> int:
+    return int(_lib.moe_workspace_bytes_norm_backward(max_tokens, H))
+
+
+def workspace_norm_backward(max_tokens: int, H: int, device="cuda"):
+    """A torch uint8 tensor for moe_norm_backward with up to max_tokens rows."""
+    import torch
+    n = moe_workspace_bytes_norm_backward(max_tokens, H)
+    if n == 0:
+        raise MoEError("moe_workspace_bytes_norm_backward", MOE_ERR_UNSUPPORTED)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_norm_backward(v, dout, dresidual, weight, eps, dx, dweight, dbias, ws, centre=True, stream=None):
+    """Gradients of the layer norm (centre) or the RMS norm of v [T, H]: dx [T, H] bf16, dweight and
+    dbias [H] fp32; dresidual, dweight and dbias may be None."""
+    shape = T, H = v.shape
+    _check("moe_norm_backward", _lib.moe_norm_backward(
+        T, H, int(centre), _want("v", v, "bfloat16", shape), _want("dout", dout, "bfloat16", shape),
+        _want("dresidual", dresidual, "bfloat16", shape, True), _want("weight", weight, "bfloat16", (H,)), eps,
+        _want("dx", dx, "bfloat16", shape), _want("dweight", dweight, "float32", (H,), True),
+        _want("dbias", dbias, "float32", (H,), True), _want_at_least("ws", ws, "uint8", 1), ws.numel(),
+        _stream(stream)))

@@ -209,6 +209,20 @@ void launch_pack_scales_mx(const uint8_t* scales, int experts, int rows, int K, 
 void launch_add_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps, int T, int H,
                      uint16_t* residual_out, uint16_t* out, uint8_t* codes, uint8_t* scales, int sms,
                      cudaStream_t s);
+// layer norm; residual, bias and residual_out may be null
+void launch_add_layer_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, const uint16_t* bias,
+                           float eps, int T, int H, uint16_t* residual_out, uint16_t* out, int sms, cudaStream_t s);
+// gradients of the layer norm (centre) or the RMS norm of v; dresidual, dweight and dbias may be null
+size_t norm_backward_scratch_bytes(int T, int H);
+void launch_norm_backward(const uint16_t* v, const uint16_t* dout, const uint16_t* dresidual, const uint16_t* weight,
+                          float eps, int T, int H, bool centre, uint16_t* dx, float* dweight, float* dbias, void* scratch,
+                          int sms, cudaStream_t s);
+// SwiGLU with gates over grouped rows (R routes; gates, dgate and backward's a may be null)
+void launch_swiglu(const uint16_t* gu, const float* gates, const int32_t* ids, const int32_t* num_padded,
+                   int64_t max_rows, int R, int I, uint16_t* a, cudaStream_t s);
+void launch_swiglu_backward(const uint16_t* gu, const float* gates, const uint16_t* da, const int32_t* ids,
+                            const int32_t* num_padded, int64_t max_rows, int R, int I, uint16_t* dgu, float* dgate,
+                            uint16_t* a, cudaStream_t s);
 int route_scored_max_groups();
 void launch_route_scored(const float* logits, const float* bias, int T, int N, int k, bool sigmoid, int groups,
                          int top_groups, bool top2, bool renormalize, float scale, int32_t* topk_idx,

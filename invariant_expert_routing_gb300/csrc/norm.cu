@@ -14,6 +14,7 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "bf16x8.cuh"
 #include "kernels.h"
 #include "mx.cuh"
 #include "pdl.cuh"
@@ -23,24 +24,6 @@ namespace {
 
 constexpr int kNormChunk = 256;      // elements a warp takes at once (eight a lane)
 constexpr int kNormMaxChunks = 128;  // H <= 32768
-
-__device__ __forceinline__ void unpack8(const uint4& p, float (&v)[8]) {
-  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ uint4 pack_bf16(const float (&v)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&p);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // NV: 256-element chunks a warp holds.  residual_out and out may be x or
 // residual (no __restrict__ on the four): a row is read before the barrier and

@@ -1,0 +1,102 @@
+// The activation between the two expert products, with the routes' gates, and
+// its gradient, over grouped rows:
+//   a = w silu(g) u           g, u = the halves of a row of gu [rows, 2I]
+//   dg = w da u s (1 + g (1 - s)),  du = w da silu(g),  s = 1 / (1 + e^-g)
+//   dw = sum over I of da silu(g) u
+// w is the gate of the row's route (1 without gates).  Memory bound: 6 bytes an
+// element of a forward, 10 backward, 12 with a written again.
+//
+// One CTA a row: dw is summed in one order for every batch (a thread's
+// elements in turn, its warp's lanes by a fixed tree, then the warps in turn;
+// the threads follow I alone).
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "bf16x8.cuh"
+#include "kernels.h"
+#include "pdl.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kSwigluThreads = 256;
+
+// gu may be dgu and da may be a: each element is read before the same thread
+// writes it (no __restrict__ on the four).
+template <bool kBackward>
+__global__ void __launch_bounds__(kSwigluThreads)
+    swiglu_kernel(const uint16_t* gu, const float* __restrict__ gates, const uint16_t* da,
+                  const int32_t* __restrict__ ids, const int32_t* __restrict__ num_padded, long long max_rows, int R,
+                  int I, uint16_t* a, uint16_t* dgu, float* __restrict__ dgate) {
+  __shared__ float s_sum[kSwigluThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  pdl_trigger();
+  const long long P = min((long long)*num_padded, max_rows);
+  for (long long p = blockIdx.x; p < P; p += gridDim.x) {
+    const int r = ids[p];
+    if (r < 0 || r >= R) continue;   // the same for the whole CTA
+    const float w = gates ? gates[r] : 1.0f;
+    const size_t row = (size_t)p * I, row2 = 2 * row;
+    float sum = 0.0f;
+    for (int c = threadIdx.x * 8; c < I; c += blockDim.x * 8) {
+      float g[8], u[8], d[8], o[8], og[8], ou[8];
+      unpack8(__ldcs(reinterpret_cast<const uint4*>(gu + row2 + c)), g);
+      unpack8(__ldcs(reinterpret_cast<const uint4*>(gu + row2 + I + c)), u);
+      if (kBackward) unpack8(__ldcs(reinterpret_cast<const uint4*>(da + row + c)), d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float s = __fdividef(1.0f, 1.0f + __expf(-g[j]));
+        const float silu = g[j] * s, wu = w * u[j];
+        o[j] = silu * wu;
+        if (kBackward) {
+          sum = fmaf(d[j], silu * u[j], sum);
+          og[j] = d[j] * wu * (s * fmaf(g[j], 1.0f - s, 1.0f));
+          ou[j] = w * d[j] * silu;
+        }
+      }
+      if (a) *reinterpret_cast<uint4*>(a + row + c) = pack_bf16(o);
+      if (kBackward) {
+        *reinterpret_cast<uint4*>(dgu + row2 + c) = pack_bf16(og);
+        *reinterpret_cast<uint4*>(dgu + row2 + I + c) = pack_bf16(ou);
+      }
+    }
+    if (kBackward && dgate) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      __syncthreads();   // the row before is done with s_sum
+      if (lane == 0) s_sum[warp] = sum;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        float t = 0.0f;
+        for (int i = 0; i < (int)blockDim.x / 32; ++i) t += s_sum[i];
+        dgate[r] = t;
+      }
+    }
+  }
+}
+
+template <bool kBackward>
+void launch(const uint16_t* gu, const float* gates, const uint16_t* da, const int32_t* ids, const int32_t* num_padded,
+            int64_t max_rows, int R, int I, uint16_t* a, uint16_t* dgu, float* dgate, cudaStream_t s) {
+  const int want = (I / 8 + 31) / 32 * 32;
+  const int threads = want < kSwigluThreads ? want : kSwigluThreads;
+  const int64_t grid = max_rows < (1 << 20) ? max_rows : (1 << 20);
+  launch_pdl(swiglu_kernel<kBackward>, dim3((unsigned)grid), dim3(threads), 0, s, gu, gates, da, ids, num_padded,
+             (long long)max_rows, R, I, a, dgu, dgate);
+}
+
+}  // namespace
+
+void launch_swiglu(const uint16_t* gu, const float* gates, const int32_t* ids, const int32_t* num_padded,
+                   int64_t max_rows, int R, int I, uint16_t* a, cudaStream_t s) {
+  launch<false>(gu, gates, nullptr, ids, num_padded, max_rows, R, I, a, nullptr, nullptr, s);
+}
+
+void launch_swiglu_backward(const uint16_t* gu, const float* gates, const uint16_t* da, const int32_t* ids,
+                            const int32_t* num_padded, int64_t max_rows, int R, int I, uint16_t* dgu, float* dgate,
+                            uint16_t* a, cudaStream_t s) {
+  launch<true>(gu, gates, da, ids, num_padded, max_rows, R, I, a, dgu, dgate, s);
+}
+
+}  // namespace moe
