@@ -3,6 +3,7 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <cstdint>
 
 namespace moe {
@@ -35,7 +36,8 @@ struct GroupedWgradArgs {
   int gather_x, gather_dy, fp32;
 };
 
-void launch_grouped_gemm(const GroupedGemmArgs& a, cudaStream_t s);
-void launch_grouped_wgrad(const GroupedWgradArgs& a, cudaStream_t s);
+// false: a tensor map could not be made
+bool launch_grouped_gemm(const GroupedGemmArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, int sms, cudaStream_t s);
+bool launch_grouped_wgrad(const GroupedWgradArgs& a, PFN_cuTensorMapEncodeTiled_v12000 encode, int sms, cudaStream_t s);
 
 }  // namespace moe

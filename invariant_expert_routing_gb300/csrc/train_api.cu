@@ -89,7 +89,8 @@ moe_status moe_grouped_gemm(const moe_config* cfg, int32_t T, int32_t K, int32_t
   a.y = y_perm;
   a.gather = gather;
   a.transposed = (flags & MOE_GROUPED_TRANSPOSED) != 0;
-  moe::launch_grouped_gemm(a, static_cast<cudaStream_t>(stream));
+  const int sms = api::sm_count();
+  if (sms <= 0 || !moe::launch_grouped_gemm(a, api::tensor_map_encode(), sms, static_cast<cudaStream_t>(stream))) return MOE_ERR_CUDA;
   return api::last_error();
 }
 
@@ -131,7 +132,8 @@ moe_status moe_grouped_wgrad(const moe_config* cfg, int32_t T, int32_t K, int32_
   a.gather_x = gx;
   a.gather_dy = gd;
   a.fp32 = !bf16;
-  moe::launch_grouped_wgrad(a, s);
+  const int sms = api::sm_count();
+  if (sms <= 0 || !moe::launch_grouped_wgrad(a, api::tensor_map_encode(), sms, s)) return MOE_ERR_CUDA;
   return api::last_error();
 }
 
