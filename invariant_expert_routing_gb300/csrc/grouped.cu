@@ -14,15 +14,20 @@
 //             a row's bits depend neither on N nor on the batch.
 //   gradient: A = 256 columns of x, B = 256 columns of dy, both MN-major, K
 //             the expert's rows in ascending order.
-// Rows gathered by route come by TMA gather4 (four rows a request, one request
-// a lane), straight from the token tensor: no copy in segment order.  A row
-// index outside the tensor reads zeros, which is what the gradient's last
-// stage of a segment takes past its end: the padding is never read.
+// Rows gathered by route come by TMA gather4, four rows a request, straight from
+// the token tensor: no copy in segment order.  A row index outside the tensor
+// reads zeros, which is what the gradient's last rows of a segment ask for past
+// its end: the padding is never read.
 //
-// Ten warps a CTA: warp 0 requests operands, warp 1 (even CTA) issues the MMAs,
-// warps 2..9 store sums: two accumulators of 256 columns each let a tile's
-// stores overlap the next one's MMAs.  Segments are found from the counts by
-// every CTA, so a product is one launch and no list lives in memory.
+// Warps 0 and 10..14 request operands (10..14 in launches that may gather: they
+// take the stages in turn), warp 1 (even CTA) issues the MMAs, warps 2..9 store
+// sums.  The requesting and issuing warps run converged and elect a lane for a
+// stage's requests, all in one block: descriptors and coordinates stay in
+// uniform registers, and a warp that came together after each request took 300
+// cycles more for it (the MMAs of a stage take 512; a loop of one lane took 85
+// for a request).  Two accumulators of 256 columns each let a tile's stores overlap the
+// next one's MMAs.  Segments are found from the counts by every CTA, so a
+// product is one launch and no list lives in memory.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 #include <cstdint>
@@ -30,6 +35,7 @@
 #include "gemm.h"
 #include "grouped.h"
 #include "kernels.h"
+#include "mx.cuh"
 #include "pdl.cuh"
 #include "ptx.cuh"
 
@@ -41,31 +47,35 @@ constexpr int kBK = 64;                              // K per stage: one 128-byt
 constexpr uint32_t kBoxBytes = 64 * 64 * 2;          // 64 x 64 bf16
 constexpr int kTile = 256;                           // features and rows of a pair's tile
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = (2 + kEpiWarps) * 32;
+constexpr int kThreads = (2 + kEpiWarps) * 32;       // with one requesting warp
+constexpr int kParts = 6;                            // requesting warps of a launch that may gather
+constexpr int kMaxThreads = kThreads + (kParts - 1) * 32;
 constexpr int kStages = 6;
 constexpr uint32_t kOperandBytes = 2 * kBoxBytes;    // a CTA's 128 rows of one operand
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
 constexpr int kRowBox = 16;                          // rows of a box of a ragged tile
+constexpr uint32_t kRowBoxBytes = kRowBox * 128 * 2;   // of an MN-major operand: 128 columns
 constexpr uint32_t kSmemBytes = kStages * kStageBytes + 256 + 1024;
 
 enum Mode { kGemm, kGemmTransposed, kWgrad };
 
 struct Maps {
   CUtensorMap a;        // product: W_e [experts][K][F] or [experts][F][K]; gradient: x
-  CUtensorMap a_rows;   // gradient: x, one row a box (gather4)
   CUtensorMap b;        // rows of x / dy, full boxes
-  CUtensorMap b_small;  // product: boxes of kRowBox rows
-  CUtensorMap b_rows;   // one row a box (gather4)
+  CUtensorMap a_small, b_small;   // kRowBox rows a box (a: gradient)
+  CUtensorMap a_rows, b_rows;     // one row a box: gather4 (a: gradient)
 };
 
 struct Args {
   GroupArgs g;
   int gather_a, gather_b;
+  int wide_a, wide_b;   // MN-major operands whose 128 features are one box (two otherwise)
   uint32_t div_mul;     // id / slots
   int div_sh1, div_sh2;
   const float* add;
   void* out;
   int fp32;
+  int wide_out;         // add and out take 32-byte accesses
   int na, nb;           // 256-wide tiles of the output: product: 1, features; gradient: columns of x, of dy
   int pairs;            // CTA pairs of the grid
 };
@@ -152,7 +162,20 @@ __device__ __forceinline__ Item item_of(const Args& a, const Segments& s, int it
     it.row0 = s.start[lo] + tile * kTile;
     it.rows = min(kTile, s.count[lo] - tile * kTile);
   }
+  it.e = mx::uniform(it.e);
+  it.row0 = mx::uniform(it.row0);
+  it.rows = mx::uniform(it.rows);
+  it.a = mx::uniform(it.a);
+  it.b = mx::uniform(it.b);
   return it;
+}
+
+// A wait of a converged warp: every lane sees the barrier, and they agree.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit));
+}
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit) {
+  return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort, limit));
 }
 
 // Rows of the tile that one CTA of the pair loads (half of the MMA's N).
@@ -165,8 +188,7 @@ __device__ __forceinline__ int token_of(const Args& a, int r) {
   return (int)((t + ((n - t) >> a.div_sh1)) >> a.div_sh2);
 }
 
-// Rows p .. p + 3 of a gathered (or, with ids not wanted, in-place) operand;
-// rows from `end` on are none.  p is a multiple of 4.
+// Four rows for a gather4, p on; p is a multiple of 4 (a segment's start is one of 8).
 __device__ __forceinline__ int4 rows_of(const Args& a, bool gather, int p, int end) {
   int4 r = make_int4(-1, -1, -1, -1);
   if (p >= end) return r;
@@ -182,26 +204,84 @@ __device__ __forceinline__ int4 rows_of(const Args& a, bool gather, int p, int e
   return r;
 }
 
-__device__ __forceinline__ void store_bf16x8(uint16_t* p, const float* v) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+// One operand of a gradient's stage: 64 rows p0 on, 128 columns col on.  The
+// whole box if 64 rows in place are left; otherwise 16 rows at a time, by box if
+// they are in place and all there, by gather4 if not (rows: the 64 rows).
+struct Operand {
+  const CUtensorMap *box, *small, *rows;
+  bool gather, wide;
+};
+__device__ __forceinline__ uint32_t operand_bytes(bool gather, int left) {
+  return !gather && left >= kBK ? kOperandBytes : (uint32_t)min(kBK / kRowBox, (left + kRowBox - 1) / kRowBox) * kRowBoxBytes;
+}
+__device__ __forceinline__ void request_operand(const Operand& o, uint32_t dst, int col, int p0, int left, const int4* rows,
+                                                uint32_t bar, uint64_t policy) {
+  if (!o.gather && left >= kBK) {
+    if (o.wide) {
+      mx::tma_load_3d_pair(dst, o.box, 0, p0, col >> 6, bar, policy);
+    } else {
+      tma_load_2d_pair(dst, o.box, col, p0, bar, policy);
+      tma_load_2d_pair(dst + kBoxBytes, o.box, col + 64, p0, bar, policy);
+    }
+    return;
   }
-  __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+  for (int r0 = 0; r0 < min(left, kBK); r0 += kRowBox) {
+    const uint32_t at = dst + r0 * 128;
+    if (!o.gather && r0 + kRowBox <= left) {
+      // (one box of 128 columns would put its halves 2 KB apart)
+      tma_load_2d_pair(at, o.small, col, p0 + r0, bar, policy);
+      tma_load_2d_pair(at + kBoxBytes, o.small, col + 64, p0 + r0, bar, policy);
+      continue;
+    }
+#pragma unroll
+    for (int i = 0; i < kRowBox / 4; ++i) {
+      const int4 r = rows[r0 / 4 + i];
+      tma_gather4_pair(at + i * 512, o.rows, col, r.x, r.y, r.z, r.w, bar, policy);
+      tma_gather4_pair(at + i * 512 + kBoxBytes, o.rows, col + 64, r.x, r.y, r.z, r.w, bar, policy);
+    }
+  }
+}
+
+// How a CTA's requesting warps ended, told to the other CTA of the pair.
+struct PartsEnd {
+  int issued[kParts], gave_up;
+};
+
+// 32 bytes of a row: one access where the addresses are 32-byte aligned (a
+// sector each: half sectors doubled the write traffic), two otherwise.
+__device__ __forceinline__ void load8(const float* p, bool wide, float* v) {
+  if (wide) {
+    asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "l"(p)
+                 : "memory");
+  } else {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+}
+__device__ __forceinline__ void store8(void* p, bool wide, const uint32_t* w) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+    __stcs(reinterpret_cast<uint4*>(p) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+  }
 }
 
 template <Mode kMode>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
     grouped_kernel(const __grid_constant__ Maps maps, const Args args) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Segments seg;
   __shared__ uint32_t s_tmem_base;
   __shared__ volatile int s_abort;
-  __shared__ int s_issued;            // stages the producer asked for
+  __shared__ PartsEnd s_end;          // stages that each requesting warp asked for
   __shared__ uint32_t s_tx[kStages];  // bytes of this CTA's last load into each stage
-  __shared__ volatile PairEnd s_peer;
+  __shared__ volatile PartsEnd s_peer;
+  __shared__ int4 s_rows[kParts][32]; // rows of a requesting warp's gather4 requests
 
   const uint32_t rank = cluster_ctarank();   // 0: issues the MMAs
   const bool lead = rank == 0;
@@ -214,6 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tfull0 = empty0 + 8 * kStages;
   const uint32_t tempty0 = tfull0 + 16;
   const uint32_t drain = tempty0 + 16;
+  const int parts = kMode == kWgrad || args.gather_b ? kParts : 1;   // requesting warps
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t wlim = args.g.wait_ns ? args.g.wait_ns : kWaitLimitNs;
@@ -230,6 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(drain, 1);
     s_abort = 0;
     s_peer.gave_up = 0;
+    for (int w = 0; w < kParts; ++w) s_end.issued[w] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -242,7 +324,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       prefetch_tmap(&maps.a);
       prefetch_tmap(&maps.b);
       prefetch_tmap(&maps.b_small);
-      prefetch_tmap(&maps.b_rows);
     }
     __syncwarp();
     // The set-up reads nothing an earlier kernel writes: it overlaps the end
@@ -259,102 +340,107 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // every CTA of this persistent grid is resident: the next kernel may launch
   // now (it waits for this grid to finish)
   pdl_trigger();
-  const uint32_t tmem = s_tmem_base;
-  const int total = !seg.ok ? 0 : kMode == kWgrad ? args.g.N * args.na * args.nb : seg.first[args.g.N] * args.nb;
+  const uint32_t tmem = (uint32_t)mx::uniform((int)s_tmem_base);
+  const int total = mx::uniform(!seg.ok ? 0 : kMode == kWgrad ? args.g.N * args.na * args.nb : seg.first[args.g.N] * args.nb);
   const int ksteps_fixed = (args.g.K + kBK - 1) / kBK;
   auto ksteps_of = [&](const Item& it) { return kMode == kWgrad ? (it.rows + kBK - 1) / kBK : ksteps_fixed; };
-
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer (both CTAs)
+  if (warp == 0 || warp >= 2 + kEpiWarps) {
+    // ------------------------------------------------------------ producers (both CTAs)
+    const int part = warp == 0 ? 0 : mx::uniform(warp - (1 + kEpiWarps));
     const uint64_t pol_w = policy_evict_normal();
     const uint64_t pol_x = policy_evict_last();
-    int stage = 0, issued = 0;
-    uint32_t phase = 0;
+    const uint32_t s0 = smem_u32(smem);
+    const int me = mx::uniform((int)rank);
+    const uint32_t full_lead = mapa_shared(full0, 0);   // the even CTA's full barriers
+    const Operand oa{&maps.a, &maps.a_small, &maps.a_rows, args.gather_a != 0, args.wide_a != 0};
+    const Operand ob{&maps.b, &maps.b_small, &maps.b_rows, args.gather_b != 0, args.wide_b != 0};
+    int4* rows = s_rows[part];
+    int n0 = 0, issued = 0;   // stages of the items before; this warp's
     bool ok = true;
     for (int item = pair0; item < total && ok; item += pairs) {
       const Item it = item_of<kMode>(args, seg, item);
       const int ksteps = ksteps_of(it), end = it.row0 + it.rows;
       // product: this CTA's rows of the tile; gradient: this CTA's columns
       const int half = half_rows(it.rows);
-      const int brow0 = it.row0 + (int)rank * half;
-      const int acol = it.a * kTile + (int)rank * 128, bcol = it.b * kTile + (int)rank * 128;
-      int4 rows = {}, arows = {}, next = {}, anext = {};
-      if (kMode != kWgrad) {
-        if (args.gather_b && lane * 4 < half) rows = rows_of(args, true, brow0 + lane * 4, end);
-      } else {
-        const int p = it.row0 + (lane & 15) * 4;
-        if (args.gather_a) anext = rows_of(args, true, p, end);
-        if (args.gather_b) next = rows_of(args, true, p, end);
+      const int brow0 = it.row0 + me * half;
+      const int acol = it.a * kTile + me * 128, bcol = it.b * kTile + me * 128;
+      const int first = (part + parts - n0 % parts) % parts;   // this warp's first stage of the item
+      int4 next = {};   // gradient: rows of the next stage, x in lanes 0..15, dy in lanes 16..31
+      const bool gather_mine = lane < 16 ? oa.gather : ob.gather;
+      if (kMode == kWgrad) {
+        next = rows_of(args, gather_mine, it.row0 + first * kBK + (lane & 15) * 4, end);
+      } else if (args.gather_b) {
+        __syncwarp();
+        if (4 * lane < half) rows[lane] = rows_of(args, true, brow0 + 4 * lane, end);
+        __syncwarp();
       }
-      const uint32_t tx = kMode == kWgrad ? kStageBytes : kOperandBytes + (uint32_t)half * kBK * 2;
-      for (int ks = 0; ks < ksteps; ++ks) {
-        int got = 1;
-        if (lane == 0) got = mbar_wait_cluster(empty0 + 8 * stage, phase ^ 1u, &s_abort, wlim) ? 1 : 0;
-        got = __shfl_sync(0xffffffffu, got, 0);
-        if (!got) {
+      for (int ks = first; ks < ksteps; ks += parts) {
+        const int n = n0 + ks, stage = n % kStages;
+        const uint32_t phase = (uint32_t)(n / kStages) & 1u;
+        if (!warp_wait(empty0 + 8 * stage, phase ^ 1u, &s_abort, wlim)) {
           ok = false;
           break;
         }
-        const uint32_t sA = smem_u32(smem + stage * kStageBytes), sB = sA + kOperandBytes;
-        const uint32_t fb = mapa_shared(full0 + 8 * stage, 0);   // the even CTA's full barrier
+        const uint32_t sA = s0 + stage * kStageBytes, sB = sA + kOperandBytes;
+        const uint32_t fb = full_lead + 8 * stage;
         const int k0 = ks * kBK;
-        if (lane == 0) {
-          s_tx[stage] = tx;
-          if (lead) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * tx);
-        }
         if (kMode != kWgrad) {
-          if (lane == 0) {
-            if (kMode == kGemm) {
-              tma_load_3d_pair(sA, &maps.a, bcol, k0, it.e, fb, pol_w);
-              tma_load_3d_pair(sA + kBoxBytes, &maps.a, bcol + 64, k0, it.e, fb, pol_w);
+          if (mx::elect_one()) {
+            const uint32_t tx = kOperandBytes + (uint32_t)half * kBK * 2;
+            s_tx[stage] = tx;
+            if (lead) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * tx);
+            if (kMode == kGemmTransposed) {
+              mx::tma_load_3d_pair(sA, &maps.a, k0, bcol, it.e, fb, pol_w);
+            } else if (args.wide_a) {
+              tma_load_4d_pair(sA, &maps.a, 0, k0, bcol >> 6, it.e, fb, pol_w);
             } else {
-              tma_load_3d_pair(sA, &maps.a, k0, bcol, it.e, fb, pol_w);
+              mx::tma_load_3d_pair(sA, &maps.a, bcol, k0, it.e, fb, pol_w);
+              mx::tma_load_3d_pair(sA + kBoxBytes, &maps.a, bcol + 64, k0, it.e, fb, pol_w);
+            }
+            if (args.gather_b) {
+#pragma unroll 8
+              for (int i = 0; i < half / 4; ++i) {
+                const int4 r = rows[i];
+                tma_gather4_pair(sB + i * 512, &maps.b_rows, k0, r.x, r.y, r.z, r.w, fb, pol_x);
+              }
+            } else if (half == 128) {
+              tma_load_2d_pair(sB, &maps.b, k0, brow0, fb, pol_x);
+            } else {
+              for (int r = 0; r < half; r += kRowBox)
+                tma_load_2d_pair(sB + r * 128, &maps.b_small, k0, brow0 + r, fb, pol_x);
             }
           }
-          if (args.gather_b) {
-            if (lane * 4 < half) tma_gather4_pair(sB + lane * 512, &maps.b_rows, k0, rows, fb, pol_x);
-          } else if (half == 128) {
-            if (lane == 0) tma_load_2d_pair(sB, &maps.b, k0, brow0, fb, pol_x);
-          } else if (lane * kRowBox < half) {
-            tma_load_2d_pair(sB + lane * kRowBox * 128, &maps.b_small, k0, brow0 + lane * kRowBox, fb, pol_x);
-          }
         } else {
-          // the segment's last rows, too, one row at a time: rows past its end
-          // are none and read zeros
-          const int p0 = it.row0 + k0, p = p0 + (lane & 15) * 4;
-          const bool tail = p0 + kBK > end;
-          arows = args.gather_a ? anext : rows_of(args, false, p, end);
-          rows = args.gather_b ? next : rows_of(args, false, p, end);
-          const uint32_t at = (uint32_t)(lane >> 4) * kBoxBytes + (uint32_t)(lane & 15) * 512;
-          const int box = (lane >> 4) * 64;
-          if (args.gather_a || tail)
-            tma_gather4_pair(sA + at, &maps.a_rows, acol + box, arows, fb, pol_x);
-          else if (lane < 2)
-            tma_load_2d_pair(sA + lane * kBoxBytes, &maps.a, acol + lane * 64, p0, fb, pol_x);
-          if (args.gather_b || tail)
-            tma_gather4_pair(sB + at, &maps.b_rows, bcol + box, rows, fb, pol_x);
-          else if (lane < 2)
-            tma_load_2d_pair(sB + lane * kBoxBytes, &maps.b, bcol + lane * 64, p0, fb, pol_x);
-          // the next stage's routes, asked for a stage ahead
-          if (args.gather_a) anext = rows_of(args, true, p + kBK, end);
-          if (args.gather_b) next = rows_of(args, true, p + kBK, end);
+          const int p0 = it.row0 + k0, left = it.rows - k0;
+          if (oa.gather || ob.gather || left < kBK) {
+            rows[lane] = next;
+            __syncwarp();
+          }
+          if (mx::elect_one()) {
+            const uint32_t tx = operand_bytes(oa.gather, left) + operand_bytes(ob.gather, left);
+            s_tx[stage] = tx;
+            if (lead) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * tx);
+            request_operand(oa, sA, acol, p0, left, rows, fb, pol_x);
+            request_operand(ob, sB, bcol, p0, left, rows + 16, fb, pol_x);
+          }
+          // the next stage's routes are asked for now
+          next = rows_of(args, gather_mine, p0 + parts * kBK + (lane & 15) * 4, end);
         }
         __syncwarp();
         ++issued;
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
+      n0 += ksteps;
     }
     if (!ok) {
       s_abort = 1;
       if (lane == 0) atomicOr(args.g.status, kDevErrTimeout);
     }
-    if (lane == 0) s_issued = issued;
+    if (lane == 0) s_end.issued[part] = issued;
+    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
-    if (lead && lane == 0) {
+    if (lead) {
+      const bool leader = mx::elect_one();
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -371,24 +457,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int ksteps = ksteps_of(it);
         if (ksteps == 0) continue;   // an expert without rows: nothing to sum
         const uint32_t idesc = idesc_bf16(kTile, kMode == kWgrad ? kTile : 2 * half_rows(it.rows), kAMn, kBMn);
-        if (!mbar_wait_cluster(tempty0 + 8 * acc, acc_phase ^ 1u, &s_abort, wlim)) {
+        if (!warp_wait_cluster(tempty0 + 8 * acc, acc_phase ^ 1u, &s_abort, wlim)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t d0 = tmem + acc * kTile;
         for (int ks = 0; ks < ksteps; ++ks) {
-          if (!mbar_wait_cluster(full0 + 8 * stage, phase, &s_abort, wlim)) {
+          if (!warp_wait_cluster(full0 + 8 * stage, phase, &s_abort, wlim)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint64_t ad = adesc0 + soff, bd = bdesc0 + soff;
           const int left = (kMode == kWgrad ? it.rows : args.g.K) - ks * kBK;   // K left: zeros from there on
+          if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            if (kk * 16 < left) mma_bf16_pair(d0, ad + kk * kAStep, bd + kk * kBStep, idesc, (ks | kk) != 0 ? 1u : 0u);
-          mma_commit_pair(empty0 + 8 * stage, 0x3);
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              if (kk * 16 < left) mma_bf16_pair(d0, ad + kk * kAStep, bd + kk * kBStep, idesc, (ks | kk) != 0 ? 1u : 0u);
+            mma_commit_pair(empty0 + 8 * stage, 0x3);
+            if (ks + 1 == ksteps) mma_commit_pair(tfull0 + 8 * acc, 0x3);
+          }
+          __syncwarp();
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
@@ -398,7 +488,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        mma_commit_pair(tfull0 + 8 * acc, 0x3);
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
@@ -406,10 +495,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!ok) {
         s_abort = 1;
-        atomicOr(args.g.status, kDevErrTimeout);
+        if (lane == 0) atomicOr(args.g.status, kDevErrTimeout);
       }
       // all issued MMAs must be complete before TMEM is released
-      mma_commit_pair(drain, 0x3);
+      if (leader) mma_commit_pair(drain, 0x3);
+      __syncwarp();
       volatile int no_abort = 0;
       mbar_wait(drain, 0, &no_abort);
     }
@@ -424,6 +514,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int item = pair0; item < total; item += pairs) {
       const Item it = item_of<kMode>(args, seg, item);
       const bool empty = kMode == kWgrad && it.rows == 0;
+      // gradient: a lane is a column of x, a column one of dy: contiguous in dw
+      const int m = it.a * kTile + (int)rank * 128 + quarter * 32 + lane;
+      const int n0 = it.b * kTile + col0;
+      const size_t at = ((size_t)it.e * args.g.K + m) * F + n0;
+      const bool wide = args.wide_out != 0;
+      float z[32];   // what the sums of the next 32 columns are added to, asked for before they are there
+      auto load_add = [&](int c) {
+#pragma unroll
+        for (int h = 0; h < 32; h += 8)
+          if (m < args.g.K && n0 + c + h < F) load8(args.add + at + c + h, wide, z + h);
+      };
+      if (kMode == kWgrad && args.add) load_add(0);
       if (!empty) {
         int got = 1;
         if (lane == 0) got = mbar_wait_cluster(tfull0 + 8 * acc, acc_phase, &s_abort, wlim) ? 1 : 0;
@@ -454,50 +556,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();   // tmem_ld16 is one instruction of the whole warp
         }
       } else {
-        // a lane is a column of x, a column one of dy: contiguous in dw
-        const int m = it.a * kTile + (int)rank * 128 + quarter * 32 + lane;
-        const size_t row = ((size_t)it.e * args.g.K + m) * F;
-        for (int c = col0; c < col0 + kTile / 2; c += 16) {
-          const int n = it.b * kTile + c;
-          if (n >= F) break;   // the same for the whole warp
-          float v[16];
-          if (!empty) {
-            tmem_ld16(tbase + c, v);
-            tmem_wait_ld();
-          } else {
+        for (int c = 0; c < kTile / 2 && n0 + c < F; c += 32) {   // the same for the whole warp
+          float v[32] = {};
+          if (!empty) mx::tmem_load32(tbase + col0 + c, v);
+          if (args.add) {   // add may be out: each element is read before the same thread writes it
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+            for (int j = 0; j < 32; ++j) v[j] += z[j];
+            if (c + 32 < kTile / 2) load_add(c + 32);
           }
           if (m < args.g.K) {
+            if (args.fp32) {
+              float* o = reinterpret_cast<float*>(args.out) + at + c;
 #pragma unroll
-            for (int h = 0; h < 16; h += 8) {
-              if (n + h >= F) break;
-              if (!args.fp32) {
-                store_bf16x8(reinterpret_cast<uint16_t*>(args.out) + row + n + h, v + h);
-              } else {
-                float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(args.out) + row + n + h);
-                float4 q[2] = {make_float4(v[h], v[h + 1], v[h + 2], v[h + 3]),
-                               make_float4(v[h + 4], v[h + 5], v[h + 6], v[h + 7])};
-                if (args.add) {   // add may be out (no __restrict__): read before it is written
-                  const float4* d = reinterpret_cast<const float4*>(args.add + row + n + h);
+              for (int h = 0; h < 32; h += 8)
+                if (n0 + c + h < F) store8(o + h, wide, reinterpret_cast<const uint32_t*>(v + h));
+            } else {
+              uint16_t* o = reinterpret_cast<uint16_t*>(args.out) + at + c;
+              uint32_t w[16];
 #pragma unroll
-                  for (int i = 0; i < 2; ++i) {
-                    const float4 z = __ldcs(d + i);
-                    q[i] = make_float4(z.x + q[i].x, z.y + q[i].y, z.z + q[i].z, z.w + q[i].w);
-                  }
-                }
-                __stcs(o, q[0]);
-                __stcs(o + 1, q[1]);
+              for (int j = 0; j < 16; ++j) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                w[j] = *reinterpret_cast<const uint32_t*>(&b);
+              }
+#pragma unroll
+              for (int h = 0; h < 32; h += 16) {
+                if (n0 + c + h + 8 < F)
+                  store8(o + h, wide, w + h / 2);
+                else if (n0 + c + h < F)
+                  __stcs(reinterpret_cast<uint4*>(o + h), make_uint4(w[h / 2], w[h / 2 + 1], w[h / 2 + 2], w[h / 2 + 3]));
               }
             }
           }
-          __syncwarp();
+          __syncwarp();   // tmem_load32 is one instruction of the whole warp
         }
       }
       if (empty) continue;
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(mapa_shared(tempty0 + 8 * acc, 0));
+      if (lane == 0) mx::mbar_arrive_remote_relaxed(mapa_shared(tempty0 + 8 * acc, 0));
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
@@ -507,22 +603,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  end_pair(lead, full0, drain, kStages, s_issued, s_abort, &s_peer, [&](int i) {
-    // a load that only the other CTA asked for: a pair's loads have the same size
-    return s_tx[i % kStages];
-  });
+  // Nothing targets either CTA's shared memory from here on (pipeline_end.h; the
+  // same steps as end_pair, with the requests of several warps).
+  {
+    volatile int no_abort = 0;
+    const int gave_up = s_abort;
+    const uint32_t there = mapa_shared(smem_u32(const_cast<PartsEnd*>(&s_peer)), lead ? 1 : 0);
+    if (threadIdx.x == 0 && gave_up) store_cluster(there + 4 * kParts, 1);
+    __syncwarp();
+    cluster_sync();   // also: neither CTA issues anything from here on
+    if (gave_up || s_peer.gave_up) {   // the same in every thread of both CTAs
+      if (threadIdx.x == 0)
+        for (int w = 0; w < kParts; ++w) store_cluster(there + 4 * w, s_end.issued[w]);
+      __syncwarp();
+      cluster_sync();
+      if (threadIdx.x == 0) {
+        int mine[kParts], peer[kParts];
+        for (int w = 0; w < kParts; ++w) mine[w] = s_end.issued[w], peer[w] = s_peer.issued[w];
+        settle_pair_parts(
+            lead, mine, peer, parts, kStages, [&](int i) { mbar_complete_tx(full0 + 8 * (i % kStages), s_tx[i % kStages]); },
+            [&](int i) { mbar_arrive_expect_tx_remote(mapa_shared(full0 + 8 * (i % kStages), 0), s_tx[i % kStages]); });
+        if (lead)
+          wait_pair_parts(mine, peer, parts, kStages, [&](int st, uint32_t parity) {
+            mbar_wait_cluster(full0 + 8 * st, parity, &no_abort);
+          });
+      }
+      __syncwarp();
+      cluster_sync();
+    }
+    if (threadIdx.x == 0) mbar_wait_cluster(drain, 0, &no_abort);
+    __syncwarp();
+  }
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
 // ------------------------------------------------------------------ host
-bool encode(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* m, const void* base, int rank, uint64_t d0, uint64_t d1,
-            uint64_t d2, uint32_t b0, uint32_t b1) {
-  const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {2 * d0, 2 * d0 * d1};
-  const cuuint32_t box[3] = {b0, b1, 1}, estr[3] = {1, 1, 1};
+bool encode(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [outer][rows][cols] in boxes of box_rows rows and 64 columns.
+bool map_rows(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
+              uint64_t outer, uint32_t box_rows) {
+  const cuuint64_t dims[3] = {cols, rows, outer}, strides[2] = {2 * cols, 2 * cols * rows};
+  const cuuint32_t box[3] = {64, box_rows, 1};
+  return encode(fn, m, base, outer ? 3 : 2, dims, strides, box);
+}
+
+// The same tensor as [outer][cols / 64][rows][64], 64 rows and 128 columns a
+// box: an MN-major operand's two halves in one request.
+bool map_wide(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
+              uint64_t outer) {
+  const cuuint64_t dims[4] = {64, rows, cols / 64, outer}, strides[3] = {2 * cols, 128, 2 * cols * rows};
+  const cuuint32_t box[4] = {64, kBK, 2, 1};
+  return encode(fn, m, base, outer ? 4 : 3, dims, strides, box);
 }
 
 // id / d = (t + ((id - t) >> sh1)) >> sh2, t = the upper half of mul * id
@@ -537,7 +676,7 @@ void set_divisor(Args& a, uint32_t d) {
 
 // Pairs of CTAs that can be resident at once, looked up once per device and kernel.
 template <Mode kMode>
-int resident_pairs(int sms) {
+int resident_pairs(int sms, int threads) {
   static int cache[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -546,7 +685,7 @@ int resident_pairs(int sms) {
   int n = 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (unsigned)(sms / 2), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -566,9 +705,10 @@ int resident_pairs(int sms) {
 
 template <Mode kMode>
 void launch(const Maps& m, Args& a, long long items, int sms, cudaStream_t s) {
-  const int cap = resident_pairs<kMode>(sms);
+  const bool gathers = kMode == kWgrad || a.gather_b;
+  const int cap = resident_pairs<kMode>(sms, kMaxThreads);
   a.pairs = (int)(items < cap ? items : cap);
-  launch_pdl(grouped_kernel<kMode>, dim3(2 * a.pairs), dim3(kThreads), kSmemBytes, s, m, a);
+  launch_pdl(grouped_kernel<kMode>, dim3(2 * a.pairs), dim3(gathers ? kMaxThreads : kThreads), kSmemBytes, s, m, a);
 }
 
 // The rows that experts hold in all, at most.
@@ -583,12 +723,15 @@ bool launch_grouped_gemm(const GroupedGemmArgs& in, PFN_cuTensorMapEncodeTiled_v
   const GroupArgs& g = in.g;
   const uint64_t K = g.K, F = g.F, N = g.N, rows = in.gather ? (uint64_t)g.T : (uint64_t)g.max_rows;
   Maps m{};
-  if (!(in.transposed ? encode(fn, &m.a, in.w, 3, K, F, N, kBK, 128) : encode(fn, &m.a, in.w, 3, F, K, N, 64, kBK)) ||
-      !encode(fn, &m.b, in.x, 2, K, rows, 1, kBK, 128) || !encode(fn, &m.b_small, in.x, 2, K, rows, 1, kBK, kRowBox) ||
-      !encode(fn, &m.b_rows, in.x, 2, K, rows, 1, kBK, 1))
-    return false;
-  m.a_rows = m.b_rows;
   Args a{};
+  a.wide_a = !in.transposed && F % 64 == 0;
+  if (!(in.transposed ? map_rows(fn, &m.a, in.w, K, F, N, 128)
+        : a.wide_a    ? map_wide(fn, &m.a, in.w, F, K, N)
+                      : map_rows(fn, &m.a, in.w, F, K, N, kBK)) ||
+      !map_rows(fn, &m.b, in.x, K, rows, 0, 128) || !map_rows(fn, &m.b_small, in.x, K, rows, 0, kRowBox) ||
+      !map_rows(fn, &m.b_rows, in.x, K, rows, 0, 1))
+    return false;
+  m.a_small = m.a_rows = m.b_rows;
   a.g = g;
   a.gather_b = in.gather;
   set_divisor(a, (uint32_t)g.slots);
@@ -608,11 +751,17 @@ bool launch_grouped_wgrad(const GroupedWgradArgs& in, PFN_cuTensorMapEncodeTiled
   const uint64_t K = g.K, F = g.F, xr = in.gather_x ? (uint64_t)g.T : (uint64_t)g.max_rows,
                  dr = in.gather_dy ? (uint64_t)g.T : (uint64_t)g.max_rows;
   Maps m{};
-  if (!encode(fn, &m.a, in.x, 2, K, xr, 1, 64, kBK) || !encode(fn, &m.a_rows, in.x, 2, K, xr, 1, 64, 1) ||
-      !encode(fn, &m.b, in.dy, 2, F, dr, 1, 64, kBK) || !encode(fn, &m.b_rows, in.dy, 2, F, dr, 1, 64, 1))
-    return false;
-  m.b_small = m.b_rows;
   Args a{};
+  a.wide_a = K % 64 == 0;
+  a.wide_b = F % 64 == 0;
+  auto maps_of = [&](const uint16_t* p, uint64_t cols, uint64_t rows, bool wide, CUtensorMap* box, CUtensorMap* small,
+                     CUtensorMap* one) {
+    return (wide ? map_wide(fn, box, p, cols, rows, 0) : map_rows(fn, box, p, cols, rows, 0, kBK)) &&
+           map_rows(fn, small, p, cols, rows, 0, kRowBox) && map_rows(fn, one, p, cols, rows, 0, 1);
+  };
+  if (!maps_of(in.x, K, xr, a.wide_a, &m.a, &m.a_small, &m.a_rows) ||
+      !maps_of(in.dy, F, dr, a.wide_b, &m.b, &m.b_small, &m.b_rows))
+    return false;
   a.g = g;
   a.gather_a = in.gather_x;
   a.gather_b = in.gather_dy;
@@ -620,6 +769,7 @@ bool launch_grouped_wgrad(const GroupedWgradArgs& in, PFN_cuTensorMapEncodeTiled
   a.add = in.add;
   a.out = in.dw;
   a.fp32 = in.fp32;
+  a.wide_out = (reinterpret_cast<uintptr_t>(in.dw) | reinterpret_cast<uintptr_t>(in.add)) % 32 == 0 && (in.fp32 || g.F % 16 == 0);
   a.na = (g.K + kTile - 1) / kTile;
   a.nb = (g.F + kTile - 1) / kTile;
   launch<kWgrad>(m, a, (long long)g.N * a.na * a.nb, sms, s);

@@ -42,4 +42,38 @@ MOE_HD void settle_pair_loads(bool even, int mine, int peer, Complete complete, 
   }
 }
 
+// The same where several warps of a CTA request loads in turn: load i is of warp
+// i % parts, and count[w] says how many of its own warp w issued.  An issued
+// load that no MMA has consumed is one of the `stages` before the highest.
+MOE_HD bool load_issued(const int* count, int parts, int i) { return i / parts < count[i % parts]; }
+MOE_HD int loads_top(const int* count, int parts) {
+  int top = 0;
+  for (int w = 0; w < parts; ++w) {
+    const int t = count[w] ? (count[w] - 1) * parts + w + 1 : 0;
+    top = t > top ? t : top;
+  }
+  return top;
+}
+MOE_HD int loads_top(const int* mine, const int* peer, int parts) {
+  const int a = loads_top(mine, parts), b = loads_top(peer, parts);
+  return a > b ? a : b;
+}
+template <class Complete, class Arm>
+MOE_HD void settle_pair_parts(bool even, const int* mine, const int* peer, int parts, int stages, Complete complete, Arm arm) {
+  const int top = loads_top(mine, peer, parts);
+  for (int i = top > stages ? top - stages : 0; i < top; ++i) {
+    if (!load_issued(mine, parts, i) || load_issued(peer, parts, i)) continue;
+    if (even)
+      complete(i);
+    else
+      arm(i);
+  }
+}
+template <class Wait>
+MOE_HD void wait_pair_parts(const int* mine, const int* peer, int parts, int stages, Wait wait) {
+  const int top = loads_top(mine, peer, parts);
+  for (int i = top > stages ? top - stages : 0; i < top; ++i)
+    if (load_issued(mine, parts, i) || load_issued(peer, parts, i)) wait(i % stages, (unsigned)(i / stages) & 1u);
+}
+
 }  // namespace moe
