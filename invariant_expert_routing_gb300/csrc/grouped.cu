@@ -48,16 +48,32 @@ constexpr uint32_t kBoxBytes = 64 * 64 * 2;          // 64 x 64 bf16
 constexpr int kTile = 256;                           // features and rows of a pair's tile
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (2 + kEpiWarps) * 32;       // with one requesting warp
-constexpr int kParts = 6;                            // requesting warps of a launch that may gather
-constexpr int kMaxThreads = kThreads + (kParts - 1) * 32;
-constexpr int kStages = 6;
 constexpr uint32_t kOperandBytes = 2 * kBoxBytes;    // a CTA's 128 rows of one operand
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
 constexpr int kRowBox = 16;                          // rows of a box of a ragged tile
 constexpr uint32_t kRowBoxBytes = kRowBox * 128 * 2;   // of an MN-major operand: 128 columns
-constexpr uint32_t kSmemBytes = kStages * kStageBytes + 256 + 1024;
 
-enum Mode { kGemm, kGemmTransposed, kWgrad };
+enum Mode { kGemm, kGemmTransposed, kWgrad, kWgradAdd };
+__host__ __device__ constexpr bool wgrad(Mode m) { return m >= kWgrad; }
+
+// kWgradAdd reads and writes fp32 gradients at the rate of memory: four stages
+// keep its MMAs fed, and 64 KB hold what the next sums are added to (two blocks
+// of 32 rows x 128 bytes an epilogue warp; 32 registers a lane instead, half as
+// much in flight: 730 us for 8192 tokens in the 128-expert layer).
+constexpr uint32_t kAddBlock = 32 * 128;
+template <Mode kMode>
+struct Cfg {
+  static constexpr int kStages = kMode == kWgradAdd ? 4 : 6;
+  // Requesting warps of a launch that may gather.  A warp that asked for stage
+  // number n goes on to n + kParts knowing that n - kStages was consumed; for the
+  // parity of the stage's barrier to tell its phases apart, n + kParts - 2 kStages
+  // has to be.
+  static constexpr int kParts = kStages;
+  static_assert(kParts <= kStages, "a requesting warp could overwrite a stage in use");
+  static constexpr int kMaxThreads = kThreads + (kParts - 1) * 32;
+  static constexpr uint32_t kAddBytes = kMode == kWgradAdd ? kEpiWarps * 2 * kAddBlock : 0;
+  static constexpr uint32_t kSmemBytes = kStages * kStageBytes + kAddBytes + 256 + 1024;
+};
 
 struct Maps {
   CUtensorMap a;        // product: W_e [experts][K][F] or [experts][F][K]; gradient: x
@@ -133,7 +149,7 @@ struct Item {
 template <Mode kMode>
 __device__ __forceinline__ Item item_of(const Args& a, const Segments& s, int item) {
   Item it;
-  if (kMode == kWgrad) {
+  if (wgrad(kMode)) {
     const int per = a.na * a.nb;
     it.e = item / per;
     const int l = item - it.e * per;
@@ -243,8 +259,9 @@ __device__ __forceinline__ void request_operand(const Operand& o, uint32_t dst, 
 }
 
 // How a CTA's requesting warps ended, told to the other CTA of the pair.
+constexpr int kMostParts = 6;
 struct PartsEnd {
-  int issued[kParts], gave_up;
+  int issued[kMostParts], gave_up;
 };
 
 // Among four lanes in turn, each with a row of four 32-byte blocks: lane q's
@@ -271,19 +288,8 @@ __device__ __forceinline__ void transpose4(float (&v)[32], int lane) {
   }
 }
 
-// 32 bytes: one access where the addresses are 32-byte aligned (a whole
-// sector), two otherwise.
-__device__ __forceinline__ void load8(const float* p, bool wide, float* v) {
-  if (wide) {
-    asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
-                 : "l"(p)
-                 : "memory");
-  } else {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  }
-}
+// 32 bytes: one access where the address is 32-byte aligned (a whole sector), two
+// otherwise.
 __device__ __forceinline__ void store8(void* p, bool wide, const uint32_t* w) {
   if (wide) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
@@ -296,8 +302,9 @@ __device__ __forceinline__ void store8(void* p, bool wide, const uint32_t* w) {
 }
 
 template <Mode kMode>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThreads, 1)
     grouped_kernel(const __grid_constant__ Maps maps, const Args args) {
+  constexpr int kStages = Cfg<kMode>::kStages, kParts = Cfg<kMode>::kParts;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Segments seg;
   __shared__ uint32_t s_tmem_base;
@@ -312,13 +319,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
   const int pair0 = (int)(blockIdx.x >> 1), pairs = args.pairs;
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+  uint8_t* adds = smem + kStages * kStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(adds + Cfg<kMode>::kAddBytes);
   const uint32_t full0 = smem_u32(bars);
   const uint32_t empty0 = full0 + 8 * kStages;
   const uint32_t tfull0 = empty0 + 8 * kStages;
   const uint32_t tempty0 = tfull0 + 16;
   const uint32_t drain = tempty0 + 16;
-  const int parts = kMode == kWgrad || args.gather_b ? kParts : 1;   // requesting warps
+  const int parts = wgrad(kMode) || args.gather_b ? kParts : 1;   // requesting warps
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t wlim = args.g.wait_ns ? args.g.wait_ns : kWaitLimitNs;
@@ -365,9 +373,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
   // now (it waits for this grid to finish)
   pdl_trigger();
   const uint32_t tmem = (uint32_t)mx::uniform((int)s_tmem_base);
-  const int total = mx::uniform(!seg.ok ? 0 : kMode == kWgrad ? args.g.N * args.na * args.nb : seg.first[args.g.N] * args.nb);
+  const int total = mx::uniform(!seg.ok ? 0 : wgrad(kMode) ? args.g.N * args.na * args.nb : seg.first[args.g.N] * args.nb);
   const int ksteps_fixed = (args.g.K + kBK - 1) / kBK;
-  auto ksteps_of = [&](const Item& it) { return kMode == kWgrad ? (it.rows + kBK - 1) / kBK : ksteps_fixed; };
+  auto ksteps_of = [&](const Item& it) { return wgrad(kMode) ? (it.rows + kBK - 1) / kBK : ksteps_fixed; };
   if (warp == 0 || warp >= 2 + kEpiWarps) {
     // ------------------------------------------------------------ producers (both CTAs)
     const int part = warp == 0 ? 0 : mx::uniform(warp - (1 + kEpiWarps));
@@ -391,7 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
       const int first = (part + parts - n0 % parts) % parts;   // this warp's first stage of the item
       int4 next = {};   // gradient: rows of the next stage, x in lanes 0..15, dy in lanes 16..31
       const bool gather_mine = lane < 16 ? oa.gather : ob.gather;
-      if (kMode == kWgrad) {
+      if (wgrad(kMode)) {
         next = rows_of(args, gather_mine, it.row0 + first * kBK + (lane & 15) * 4, end);
       } else if (args.gather_b) {
         __syncwarp();
@@ -400,7 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
       }
       for (int ks = first; ks < ksteps; ks += parts) {
         const int p0 = it.row0 + ks * kBK, left = it.rows - ks * kBK;
-        if (kMode == kWgrad) {
+        if (wgrad(kMode)) {
           // the stage's rows are in the table before the stage is free, the next one's asked for
           __syncwarp();
           rows[lane] = next;
@@ -416,7 +424,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
         const uint32_t sA = s0 + stage * kStageBytes, sB = sA + kOperandBytes;
         const uint32_t fb = full_lead + 8 * stage;
         const int k0 = ks * kBK;
-        if (kMode != kWgrad) {
+        if (!wgrad(kMode)) {
           if (mx::elect_one()) {
             const uint32_t tx = kOperandBytes + (uint32_t)half * kBK * 2;
             s_tx[stage] = tx;
@@ -472,7 +480,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
       // descriptors of stage 0, K step 0; a K = 16 step adds 2 KB to an
       // MN-major operand (64-wide atoms 8 KB apart, 8-row K groups 1 KB) and
       // 32 B to a K-major one, in the 16-byte units of the address field
-      constexpr bool kAMn = kMode != kGemmTransposed, kBMn = kMode == kWgrad;
+      constexpr bool kAMn = kMode != kGemmTransposed, kBMn = wgrad(kMode);
       constexpr uint32_t kAStep = kAMn ? 128 : 2, kBStep = kBMn ? 128 : 2;
       const uint64_t adesc0 = sdesc_sw128(smem_u32(smem), kAMn ? kBoxBytes : 16, 1024);
       const uint64_t bdesc0 = sdesc_sw128(smem_u32(smem) + kOperandBytes, kBMn ? kBoxBytes : 16, 1024);
@@ -481,7 +489,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
         const Item it = item_of<kMode>(args, seg, item);
         const int ksteps = ksteps_of(it);
         if (ksteps == 0) continue;   // an expert without rows: nothing to sum
-        const uint32_t idesc = idesc_bf16(kTile, kMode == kWgrad ? kTile : 2 * half_rows(it.rows), kAMn, kBMn);
+        const uint32_t idesc = idesc_bf16(kTile, wgrad(kMode) ? kTile : 2 * half_rows(it.rows), kAMn, kBMn);
         if (!warp_wait_cluster(tempty0 + 8 * acc, acc_phase ^ 1u, &s_abort, wlim)) {
           ok = false;
           break;
@@ -495,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
           }
           tc_fence_after();
           const uint64_t ad = adesc0 + soff, bd = bdesc0 + soff;
-          const int left = (kMode == kWgrad ? it.rows : args.g.K) - ks * kBK;   // K left: zeros from there on
+          const int left = (wgrad(kMode) ? it.rows : args.g.K) - ks * kBK;   // K left: zeros from there on
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk)
@@ -536,9 +544,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
     const int F = args.g.F;
     int acc = 0;
     uint32_t acc_phase = 0;
+    // kWgradAdd: what the sums are added to comes two blocks (of 32 columns) ahead,
+    // the first two of an item during the one before.  Whole lines are requested, 8
+    // lanes a row; the chunks of a row's 128 bytes are swapped in pairs by bit 2 of
+    // the row, so that the lanes that read a block meet different banks.
+    const uint32_t add0 = smem_u32(adds) + (uint32_t)(warp - 2) * 2 * kAddBlock;
+    auto request_add = [&](const Item& of, int block) {
+      const int n = of.b * kTile + col0 + block * 32 + (lane & 7) * 4;
+      const int m = of.a * kTile + (int)rank * 128 + quarter * 32;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        const bool in = m + r < args.g.K && n < F;
+        const float* src = in ? args.add + ((size_t)of.e * args.g.K + m + r) * F + n : args.add;
+        cp_async16(add0 + (block & 1) * kAddBlock + r * 128 + (((lane & 7) ^ (i & 1)) << 4), src, in ? 16 : 0);
+      }
+      cp_async_commit();
+    };
+    if (kMode == kWgradAdd && pair0 < total) {
+      const Item it = item_of<kMode>(args, seg, pair0);
+      request_add(it, 0);
+      request_add(it, 1);
+    }
     for (int item = pair0; item < total; item += pairs) {
       const Item it = item_of<kMode>(args, seg, item);
-      const bool empty = kMode == kWgrad && it.rows == 0;
+      const bool empty = wgrad(kMode) && it.rows == 0;
       // Gradient: TMEM lanes are columns of x, its columns those of dy, contiguous
       // in dw.  After transpose4 a lane has 32 bytes (block lane & 3 of 128) of rows
       // m0 .. m0 + 3.
@@ -547,13 +577,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
       const int n0 = it.b * kTile + col0, nl = n0 + (lane & 3) * per;
       const size_t at = ((size_t)it.e * args.g.K + m0) * F + nl;
       const bool wide = args.wide_out != 0;
-      float z[32];   // what the next sums are added to, asked for before they are there
-      auto load_add = [&](int c) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (m0 + j < args.g.K && nl + c < F) load8(args.add + at + c + (size_t)j * F, wide, z + 8 * j);
-      };
-      if (kMode == kWgrad && args.add) load_add(0);
       if (!empty) {
         int got = 1;
         if (lane == 0) got = mbar_wait_cluster(tfull0 + 8 * acc, acc_phase, &s_abort, wlim) ? 1 : 0;
@@ -568,7 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
         tc_fence_after();
       }
       const uint32_t tbase = tmem + ((uint32_t)(quarter * 32) << 16) + acc * kTile;
-      if (kMode != kWgrad) {
+      if (!wgrad(kMode)) {
         // a lane is an output feature, a column a row of y
         const int feat = it.b * kTile + (int)rank * 128 + quarter * 32 + lane;
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(args.out) + (size_t)it.row0 * F + feat;
@@ -584,7 +607,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
           __syncwarp();   // tmem_ld16 is one instruction of the whole warp
         }
       } else {
-        for (int c = 0; c < kTile / 2 && n0 + c < F; c += 4 * per) {   // the same for the whole warp
+        Item ahead = it;
+        if (kMode == kWgradAdd && item + pairs < total) ahead = item_of<kMode>(args, seg, item + pairs);
+        // (every block where they are counted, the same for the whole warp)
+        for (int c = 0; c < kTile / 2 && (kMode == kWgradAdd || n0 + c < F); c += 4 * per) {
           float v[32] = {};
           if (!empty) mx::tmem_load32(tbase + col0 + c, v);
           if (!args.fp32) {
@@ -600,10 +626,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
             for (int j = 0; j < 16; ++j) v[16 + j] = pair(u[2 * j], u[2 * j + 1]);
           }
           transpose4(v, lane);
-          if (args.add) {   // add may be out: each element is read before the same thread writes it
+          if (kMode == kWgradAdd) {
+            const int block = c >> 5;
+            cp_async_wait<1>();
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] += z[j];
-            if (c + 32 < kTile / 2) load_add(c + 32);
+            for (int j = 0; j < 4; ++j) {
+              const int r = (lane & ~3) + j, ch = 2 * (lane & 3);
+              const uint8_t* row = adds + (warp - 2) * 2 * kAddBlock + (block & 1) * kAddBlock + r * 128;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float4 d = *reinterpret_cast<const float4*>(row + (((ch + h) ^ ((r >> 2) & 1)) << 4));
+                v[8 * j + 4 * h] += d.x;
+                v[8 * j + 4 * h + 1] += d.y;
+                v[8 * j + 4 * h + 2] += d.z;
+                v[8 * j + 4 * h + 3] += d.w;
+              }
+            }
+            __syncwarp();
+            // (add may be out: a block is read two before it is written, by the same warp)
+            if (block < 2)
+              request_add(it, block + 2);
+            else if (item + pairs < total)
+              request_add(ahead, block - 2);
+            else
+              cp_async_commit();
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -630,6 +677,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
     }
   }
 
+  if (kMode == kWgradAdd) cp_async_wait<0>();   // (a wait that ran out left some in flight)
   tc_fence_before();
   __syncthreads();
   // Nothing targets either CTA's shared memory from here on (pipeline_end.h; the
@@ -638,7 +686,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMaxThreads, 1)
     volatile int no_abort = 0;
     const int gave_up = s_abort;
     const uint32_t there = mapa_shared(smem_u32(const_cast<PartsEnd*>(&s_peer)), lead ? 1 : 0);
-    if (threadIdx.x == 0 && gave_up) store_cluster(there + 4 * kParts, 1);
+    if (threadIdx.x == 0 && gave_up) store_cluster(there + 4 * kMostParts, 1);
     __syncwarp();
     cluster_sync();   // also: neither CTA issues anything from here on
     if (gave_up || s_peer.gave_up) {   // the same in every thread of both CTAs
@@ -710,12 +758,12 @@ int resident_pairs(int sms, int threads) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
-  cudaFuncSetAttribute(grouped_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  cudaFuncSetAttribute(grouped_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<kMode>::kSmemBytes);
   int n = 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (unsigned)(sms / 2), 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = Cfg<kMode>::kSmemBytes;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -734,10 +782,10 @@ int resident_pairs(int sms, int threads) {
 
 template <Mode kMode>
 void launch(const Maps& m, Args& a, long long items, int sms, cudaStream_t s) {
-  const bool gathers = kMode == kWgrad || a.gather_b;
-  const int cap = resident_pairs<kMode>(sms, kMaxThreads);
+  const bool gathers = wgrad(kMode) || a.gather_b;
+  const int cap = resident_pairs<kMode>(sms, Cfg<kMode>::kMaxThreads);
   a.pairs = (int)(items < cap ? items : cap);
-  launch_pdl(grouped_kernel<kMode>, dim3(2 * a.pairs), dim3(gathers ? kMaxThreads : kThreads), kSmemBytes, s, m, a);
+  launch_pdl(grouped_kernel<kMode>, dim3(2 * a.pairs), dim3(gathers ? Cfg<kMode>::kMaxThreads : kThreads), Cfg<kMode>::kSmemBytes, s, m, a);
 }
 
 // The rows that experts hold in all, at most.
@@ -801,7 +849,10 @@ bool launch_grouped_wgrad(const GroupedWgradArgs& in, PFN_cuTensorMapEncodeTiled
   a.wide_out = (reinterpret_cast<uintptr_t>(in.dw) | reinterpret_cast<uintptr_t>(in.add)) % 32 == 0 && (in.fp32 || g.F % 16 == 0);
   a.na = (g.K + kTile - 1) / kTile;
   a.nb = (g.F + kTile - 1) / kTile;
-  launch<kWgrad>(m, a, (long long)g.N * a.na * a.nb, sms, s);
+  if (in.add)
+    launch<kWgradAdd>(m, a, (long long)g.N * a.na * a.nb, sms, s);
+  else
+    launch<kWgrad>(m, a, (long long)g.N * a.na * a.nb, sms, s);
   return true;
 }
 

@@ -268,6 +268,16 @@ __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+// 16 bytes into shared memory by the thread itself; read 0: zeros, src is not read.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t read) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
 // Four rows (any of the tensor's; an index outside reads zeros) of a map whose
 // box is one row high, one after another in shared memory.
 __device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap* m, int32_t c0, int32_t r0, int32_t r1,

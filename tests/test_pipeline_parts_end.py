@@ -76,3 +76,55 @@ def test_no_copy_outlives_the_wait(tmp_path):
     subprocess.check_call(["g++", "-std=c++17", "-O2", "-Wall", "-Werror", "-I", CSRC, str(src), "-o", str(exe)])
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout
+
+
+PARITY = r"""
+#include <cstdio>
+#include <random>
+#include <vector>
+// Warps w, w + parts, ... of one CTA wait for a stage by the parity of its empty barrier alone.  Returns the loads that
+// went into a stage whose load before had not been consumed.
+long early(std::mt19937& g, int S, int parts, int n) {
+  auto rnd = [&](int k) { return (int)(g() % (unsigned)k); };
+  std::vector<int> freed(S), count(parts);   // phases completed of each empty barrier
+  std::vector<bool> full(n);
+  int used = 0;
+  long bad = 0;
+  for (int idle = 0; used < n && idle < 100000; ++idle) {
+    const int w = rnd(parts), i = count[w] * parts + w;
+    if (rnd(3) && i < n) {
+      const int s = i % S;
+      const unsigned parity = ((unsigned)(i / S) & 1u) ^ 1u;
+      if (((unsigned)(freed[s] - 1) & 1u) == parity) {   // the last completed phase has this parity
+        bad += i >= used + S;
+        full[i] = true;
+        ++count[w];
+      }
+    } else if (full[used]) {
+      ++freed[used % S];
+      ++used;
+    }
+  }
+  return bad;
+}
+int main() {
+  std::mt19937 g(3);
+  long good = 0, over = 0;
+  for (int i = 0; i < 20000; ++i) {
+    const int S = 2 + (int)(g() % 7);
+    good += early(g, S, 1 + (int)(g() % (unsigned)S), 60);
+    over += early(g, S, S + 1 + (int)(g() % 3), 60);
+  }
+  std::printf("%ld %ld\n", good, over);
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="no host compiler")
+def test_as_many_requesting_warps_as_stages_at_most(tmp_path):
+    """What the kernels assert: up to that many a stage's parity is never mistaken; more of them do overwrite stages."""
+    src, exe = tmp_path / "parity.cpp", tmp_path / "parity"
+    src.write_text(PARITY)
+    subprocess.check_call(["g++", "-std=c++17", "-O2", "-Wall", "-Werror", str(src), "-o", str(exe)])
+    good, over = map(int, subprocess.run([str(exe)], capture_output=True, text=True, timeout=120, check=True).stdout.split())
+    assert good == 0 and over > 0
