@@ -56,6 +56,14 @@ constexpr uint32_t kRowBoxBytes = kRowBox * 128 * 2;   // of an MN-major operand
 enum Mode { kGemm, kGemmTransposed, kWgrad, kWgradAdd };
 __host__ __device__ constexpr bool wgrad(Mode m) { return m >= kWgrad; }
 
+// A gradient sums at most this many stages of 64 rows in an accumulator.  The
+// tensor cores truncate each 16-row step's sum to fp32: 1e-6 of the result for
+// 1024 rows, 1e-5 for 8192 (2-norms; rounded sums would stay at 3e-7).  Longer
+// segments are summed part by part, the parts added (rounded to nearest) in the
+// other accumulator's columns, and the MMAs wait for that.  For bf16 results 1e-5
+// is nothing.
+constexpr int kPartStagesFp32 = 12, kPartStagesBf16 = 128;
+
 // kWgradAdd reads and writes fp32 gradients at the rate of memory: four stages
 // keep its MMAs fed, and 64 KB hold what the next sums are added to (two blocks
 // of 32 rows x 128 bytes an epilogue warp; 32 registers a lane instead, half as
@@ -376,6 +384,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
   const int total = mx::uniform(!seg.ok ? 0 : wgrad(kMode) ? args.g.N * args.na * args.nb : seg.first[args.g.N] * args.nb);
   const int ksteps_fixed = (args.g.K + kBK - 1) / kBK;
   auto ksteps_of = [&](const Item& it) { return wgrad(kMode) ? (it.rows + kBK - 1) / kBK : ksteps_fixed; };
+  // Stages that go into one accumulator of a tile (all of them, or a part's).
+  auto part_of = [&](int ksteps) {
+    const int most = args.fp32 ? kPartStagesFp32 : kPartStagesBf16;
+    return !wgrad(kMode) || ksteps <= most ? ksteps : most;
+  };
+
   if (warp == 0 || warp >= 2 + kEpiWarps) {
     // ------------------------------------------------------------ producers (both CTAs)
     const int part = warp == 0 ? 0 : mx::uniform(warp - (1 + kEpiWarps));
@@ -475,8 +489,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
     if (lead) {
       const bool leader = mx::elect_one();
       int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
+      uint32_t phase = 0, taken = 0;   // taken: parity of each accumulator's uses
       bool ok = true;
+      auto take = [&](int b) {         // the accumulator's sums have been read
+        const bool got = warp_wait_cluster(tempty0 + 8 * b, ((taken >> b) & 1u) ^ 1u, &s_abort, wlim);
+        taken ^= 1u << b;
+        tc_fence_after();
+        return got;
+      };
       // descriptors of stage 0, K step 0; a K = 16 step adds 2 KB to an
       // MN-major operand (64-wide atoms 8 KB apart, 8-row K groups 1 KB) and
       // 32 B to a K-major one, in the 16-byte units of the address field
@@ -490,13 +510,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
         const int ksteps = ksteps_of(it);
         if (ksteps == 0) continue;   // an expert without rows: nothing to sum
         const uint32_t idesc = idesc_bf16(kTile, wgrad(kMode) ? kTile : 2 * half_rows(it.rows), kAMn, kBMn);
-        if (!warp_wait_cluster(tempty0 + 8 * acc, acc_phase ^ 1u, &s_abort, wlim)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
+        const int part_stages = part_of(ksteps);
+        int left_in_part = 0;
         const uint32_t d0 = tmem + acc * kTile;
-        for (int ks = 0; ks < ksteps; ++ks) {
+        for (int ks = 0; ok && ks < ksteps; ++ks) {
+          const bool first = left_in_part == 0;
+          if (first) {
+            left_in_part = min(part_stages, ksteps - ks);
+            ok = take(acc);
+            if (!ok) break;
+          }
+          --left_in_part;
           if (!warp_wait_cluster(full0 + 8 * stage, phase, &s_abort, wlim)) {
             ok = false;
             break;
@@ -507,9 +531,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk)
-              if (kk * 16 < left) mma_bf16_pair(d0, ad + kk * kAStep, bd + kk * kBStep, idesc, (ks | kk) != 0 ? 1u : 0u);
+              if (kk * 16 < left) mma_bf16_pair(d0, ad + kk * kAStep, bd + kk * kBStep, idesc, !first || kk != 0 ? 1u : 0u);
             mma_commit_pair(empty0 + 8 * stage, 0x3);
-            if (ks + 1 == ksteps) mma_commit_pair(tfull0 + 8 * acc, 0x3);
+            if (left_in_part == 0) mma_commit_pair(tfull0 + 8 * acc, 0x3);
           }
           __syncwarp();
           if (++stage == kStages) {
@@ -521,10 +545,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
           }
         }
         if (!ok) break;
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
+        // A segment in parts is added up in the other accumulator, which the epilogue
+        // warps had read before they came to it: it counts as taken once all its parts
+        // have been issued (all warps are past the first then), and the next item
+        // starts in this one while they store from that one.
+        if (ksteps > part_stages)
+          ok = take(acc ^ 1);
+        else
+          acc ^= 1;
       }
       if (!ok) {
         s_abort = 1;
@@ -543,7 +571,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
     const int col0 = ((warp - 2) / 4) * (kTile / 2);    // its half of the 256 columns
     const int F = args.g.F;
     int acc = 0;
-    uint32_t acc_phase = 0;
+    uint32_t seen = 0;   // parity of each accumulator's full phases
+    auto wait_full = [&]() {
+      int got = 1;
+      if (lane == 0) got = mbar_wait_cluster(tfull0 + 8 * acc, (seen >> acc) & 1u, &s_abort, wlim) ? 1 : 0;
+      got = __shfl_sync(0xffffffffu, got, 0);
+      seen ^= 1u << acc;
+      if (!got && lane == 0) {
+        s_abort = 1;
+        atomicOr(args.g.status, kDevErrTimeout);
+      }
+      tc_fence_after();
+      return got != 0;
+    };
+    auto release = [&](int b) {   // this warp has read what it needs of accumulator b
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mx::mbar_arrive_remote_relaxed(mapa_shared(tempty0 + 8 * b, 0));
+    };
     // kWgradAdd: what the sums are added to comes two blocks (of 32 columns) ahead,
     // the first two of an item during the one before.  Whole lines are requested, 8
     // lanes a row; the chunks of a row's 128 bytes are swapped in pairs by bit 2 of
@@ -577,19 +622,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
       const int n0 = it.b * kTile + col0, nl = n0 + (lane & 3) * per;
       const size_t at = ((size_t)it.e * args.g.K + m0) * F + nl;
       const bool wide = args.wide_out != 0;
-      if (!empty) {
-        int got = 1;
-        if (lane == 0) got = mbar_wait_cluster(tfull0 + 8 * acc, acc_phase, &s_abort, wlim) ? 1 : 0;
-        got = __shfl_sync(0xffffffffu, got, 0);
-        if (!got) {
-          if (lane == 0) {
-            s_abort = 1;
-            atomicOr(args.g.status, kDevErrTimeout);
+      const uint32_t tlane = tmem + ((uint32_t)(quarter * 32) << 16) + col0;
+      // the parts of a long segment, added in the other accumulator
+      const int ksteps = ksteps_of(it), part_stages = part_of(ksteps);
+      const bool in_parts = ksteps > part_stages;
+      bool got = true;
+      for (int ks = 0; got && in_parts && ks < ksteps; ks += part_stages) {
+        got = wait_full();
+        for (int c = 0; got && c < kTile / 2; c += 32) {
+          float v[32];
+          mx::tmem_load32(tlane + acc * kTile + c, v);
+          if (ks > 0) {
+            float u[32];
+            mx::tmem_load32(tlane + (acc ^ 1) * kTile + c, u);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = u[j] + v[j];
           }
-          break;
+          tmem_st32(tlane + (acc ^ 1) * kTile + c, v);
         }
-        tc_fence_after();
+        tmem_wait_st();
+        if (got) release(acc);
       }
+      if (!in_parts && !empty) got = wait_full();
+      if (!got) break;
+      if (in_parts) acc ^= 1;   // where the sum is
       const uint32_t tbase = tmem + ((uint32_t)(quarter * 32) << 16) + acc * kTile;
       if (!wgrad(kMode)) {
         // a lane is an output feature, a column a row of y
@@ -667,13 +723,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
         }
       }
       if (empty) continue;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mx::mbar_arrive_remote_relaxed(mapa_shared(tempty0 + 8 * acc, 0));
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1u;
-      }
+      release(acc);
+      acc ^= 1;
     }
   }
 

@@ -364,3 +364,35 @@ def test_nothing_without_tokens(moe):
     moe.moe_norm_backward(v, v, None, w, 1e-5, v, gw, gb, moe.workspace_norm_backward(1, 64))
     assert (gw == 0).all() and (gb == 0).all()
     moe.moe_add_layer_norm(v, None, w, None, 1e-5, None, v)
+
+
+@pytest.mark.parametrize("n", [768, 769, 1537, 9000, 30_001])
+@pytest.mark.parametrize("add", [False, True])
+def test_long_segments_keep_fp32_sums(moe, n, add):
+    """A part of a long segment takes 48 MMA steps at most, each truncated by less than 2^-23 of the sum so far, and the
+    parts are added rounded: 48 of 2^-23, however long the segment (without parts 30000 rows are 4e-5 to 8e-5 off)."""
+    torch = torch_()
+    N, K, F = 2, 264, 520
+    cfg = moe.make_config(128, N, 1, 128, 8)
+    g = _gen(n)
+    counts = torch.tensor([n, 3], dtype=torch.int32, device="cuda")
+    T = n + 3
+    rows = moe.moe_max_padded_rows(cfg, T)
+    ids = torch.full((rows,), T, dtype=torch.int32, device="cuda")
+    start = (n + 7) // 8 * 8
+    ids[:n], ids[start:start + 3] = torch.arange(n, device="cuda"), n + torch.arange(3, device="cuda")
+    x = (torch.randn(T, K, generator=g, device="cuda") + 1).bfloat16()
+    dy = torch.full((rows, F), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dy[:n], dy[start:start + 3] = (torch.randn(n, F, generator=g, device="cuda") + 1).bfloat16(), 1
+    extra = torch.randn(N, K, F, generator=g, device="cuda") if add else None
+    dw, ws = torch.empty(N, K, F, device="cuda"), moe.workspace_grouped(cfg, T)
+    moe.moe_grouped_wgrad(cfg, T, x, dy, ids, counts, dw, ws, dw_add=extra, gather_x=True)
+    half = torch.empty(N, K, F, dtype=torch.bfloat16, device="cuda")
+    moe.moe_grouped_wgrad(cfg, T, x, dy, ids, counts, half, ws, gather_x=True)
+    assert moe.moe_get_device_status(ws) == 0
+    want = torch.stack([x[:n].double().t() @ dy[:n].double(), x[n:].double().t() @ dy[start:start + 3].double()])
+    got = dw.double() - (extra.double() if add else 0)
+    assert float((got[0] - want[0]).norm() / want[0].norm()) <= 48 * 2.0 ** -23 + (2.0 ** -23 if add else 0)
+    assert float((got[1] - want[1]).norm() / want[1].norm()) <= 4 * 2.0 ** -23 + (2.0 ** -23 if add else 0)
+    # a bf16 gradient is rounded once; its parts are 512 steps long
+    assert float((half[0].double() - want[0]).norm() / want[0].norm()) <= 2.0 ** -8 + 512 * 2.0 ** -23
