@@ -688,8 +688,8 @@ size_t moe_workspace_bytes_norm_backward(int32_t max_tokens, int32_t H);
  *   [T, H] bf16, dresidual [T, H] bf16 or NULL (the gradient of residual_out),
  *   weight [H] bf16, dx [T, H] bf16 out, dweight, dbias [H] fp32 out or NULL.
  * The statistics are computed again from v.  dx may be dresidual; no other
- * overlap.  The sums over rows have one order for a given T, H and number of
- * SMs, without atomics.  T = 0 sets dweight and dbias to zero.  H as above. */
+ * overlap.  The sums over rows have one order for a given T and H, without
+ * atomics.  T = 0 sets dweight and dbias to zero.  H as above. */
 moe_status moe_norm_backward(int32_t T, int32_t H, int32_t centre, const uint16_t* v, const uint16_t* dout,
                              const uint16_t* dresidual, const uint16_t* weight, float eps, uint16_t* dx, float* dweight,
                              float* dbias, void* ws, size_t ws_bytes, void* stream);

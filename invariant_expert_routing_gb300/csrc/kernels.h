@@ -216,7 +216,7 @@ void launch_add_layer_norm(const uint16_t* x, const uint16_t* residual, const ui
 size_t norm_backward_scratch_bytes(int T, int H);
 void launch_norm_backward(const uint16_t* v, const uint16_t* dout, const uint16_t* dresidual, const uint16_t* weight,
                           float eps, int T, int H, bool centre, uint16_t* dx, float* dweight, float* dbias, void* scratch,
-                          int sms, cudaStream_t s);
+                          cudaStream_t s);
 // SwiGLU with gates over grouped rows (R routes; gates, dgate and backward's a may be null)
 void launch_swiglu(const uint16_t* gu, const float* gates, const int32_t* ids, const int32_t* num_padded,
                    int64_t max_rows, int R, int I, uint16_t* a, cudaStream_t s);

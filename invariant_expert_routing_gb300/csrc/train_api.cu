@@ -229,9 +229,7 @@ moe_status moe_norm_backward(int32_t T, int32_t H, int32_t centre, const uint16_
   const size_t n = 2 * (size_t)T * H;
   if (overlap(dx, n, v, n) || overlap(dx, n, dout, n) || (dx != dresidual && overlap(dx, n, dresidual, n)))
     return MOE_ERR_INVALID_ARG;
-  const int sms = api::sm_count();
-  if (sms <= 0) return MOE_ERR_CUDA;
-  moe::launch_norm_backward(v, dout, dresidual, weight, eps, T, H, centre != 0, dx, dweight, dbias, ws, sms, s);
+  moe::launch_norm_backward(v, dout, dresidual, weight, eps, T, H, centre != 0, dx, dweight, dbias, ws, s);
   return api::last_error();
 }
 
