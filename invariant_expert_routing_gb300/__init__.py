@@ -179,7 +179,9 @@ def _stream(stream):
     if _current_stream is None:
         import torch
         # the raw handle where torch offers it: building a Stream object costs about as much as a launch
-        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        torch.cuda.current_device()   # (initialises CUDA; the raw form does not)
+        device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _current_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
     return _current_stream()
 
@@ -421,7 +423,7 @@ def _want(name, t, dtype, shape, optional=False):
         if optional:
             return None
         raise ValueError(f"{name}: a tensor is needed")
-    if t.dtype is not _dtypes[dtype] or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype is not _dtypes[dtype] or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous CUDA tensor of {dtype} {tuple(shape)} is needed, got "
                          f"{t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'} on {t.device}")
     return t.data_ptr()
@@ -591,17 +593,26 @@ def _slots(c):
     return c.num_experts if c.routing == MOE_ROUTING_EXPERT_CHOICE else c.top_k
 
 
-def _want_rows(name, t, c, T, gathered):
-    """The address and the columns of a [T, columns] (gathered) or [padded rows, columns] bf16 tensor."""
+def _rows(c, T):
+    """moe_max_padded_rows, without the call for token choice (half a microsecond, where a small product takes seven)."""
+    if c.routing == MOE_ROUTING_TOKEN_CHOICE:
+        return T * c.top_k + c.num_experts * (c.block_size - 1)
+    return moe_max_padded_rows(c, T)
+
+
+def _want_rows(name, t, rows):
+    """The address and the columns of a [rows, columns] bf16 tensor."""
     if t is None or t.dim() != 2:
         raise ValueError(f"{name}: a 2-D tensor is needed")
-    return _want(name, t, "bfloat16", (T if gathered else moe_max_padded_rows(c, T), t.shape[1])), t.shape[1]
+    shape = t.shape
+    columns = shape[1]
+    return _want(name, t, "bfloat16", (rows, columns)), columns
 
 
-def _want_groups(c, T, sorted_route_ids, expert_counts, ws, gathered):
+def _want_groups(c, rows, sorted_route_ids, expert_counts, ws, gathered):
     ids = None
     if gathered or sorted_route_ids is not None:
-        ids = _want_at_least("sorted_route_ids", sorted_route_ids, "int32", moe_max_padded_rows(c, T))
+        ids = _want_at_least("sorted_route_ids", sorted_route_ids, "int32", rows)
     return (ids, _want("expert_counts", expert_counts, "int32", (c.num_experts,)),
             _want_at_least("ws", ws, "uint8", 1))
 
@@ -611,10 +622,11 @@ def moe_grouped_gemm(cfg, T, x, w, sorted_route_ids, expert_counts, y_perm, ws, 
     """y_perm [rows, F] = x . w[e] for every row of expert e's segment; x [T, K] (gather) or
     [rows, K], w [N, K, F] (transposed: [N, F, K], the product with its transpose), all bf16."""
     c = _cfg(cfg)
-    px, K = _want_rows("x", x, c, T, gather)
-    py, F = _want_rows("y_perm", y_perm, c, T, False)
+    rows = _rows(c, T)
+    px, K = _want_rows("x", x, T if gather else rows)
+    py, F = _want_rows("y_perm", y_perm, rows)
     pw = _want("w", w, "bfloat16", (c.num_experts, F, K) if transposed else (c.num_experts, K, F))
-    ids, counts, pws = _want_groups(c, T, sorted_route_ids, expert_counts, ws, gather)
+    ids, counts, pws = _want_groups(c, rows, sorted_route_ids, expert_counts, ws, gather)
     flags = (MOE_GROUPED_GATHER if gather else 0) | (MOE_GROUPED_TRANSPOSED if transposed else 0)
     _check("moe_grouped_gemm", _lib.moe_grouped_gemm(ctypes.byref(c), T, K, F, flags, px, pw, ids, counts, py, pws,
                                                      ws.numel(), _stream(stream)))
@@ -625,13 +637,14 @@ def moe_grouped_wgrad(cfg, T, x, dy, sorted_route_ids, expert_counts, dw, ws, dw
     """dw [N, K, F] (fp32 or bf16) = dw_add + x^T dy over every expert's rows; x [T, K] (gather_x)
     or [rows, K], dy [T, F] (gather_dy) or [rows, F] bf16; dw_add fp32 (dw fp32), may be dw."""
     c = _cfg(cfg)
-    px, K = _want_rows("x", x, c, T, gather_x)
-    pdy, F = _want_rows("dy", dy, c, T, gather_dy)
+    rows = _rows(c, T)
+    px, K = _want_rows("x", x, T if gather_x else rows)
+    pdy, F = _want_rows("dy", dy, T if gather_dy else rows)
     shape = (c.num_experts, K, F)
     bf16 = dw is not None and dw.dtype is _dtypes["bfloat16"]
     pdw = _want("dw", dw, "bfloat16" if bf16 else "float32", shape)
     padd = _want("dw_add", dw_add, "float32", shape, optional=True)
-    ids, counts, pws = _want_groups(c, T, sorted_route_ids, expert_counts, ws, gather_x or gather_dy)
+    ids, counts, pws = _want_groups(c, rows, sorted_route_ids, expert_counts, ws, gather_x or gather_dy)
     flags = ((MOE_WGRAD_GATHER_X if gather_x else 0) | (MOE_WGRAD_GATHER_DY if gather_dy else 0)
              | (MOE_WGRAD_BF16 if bf16 else 0))
     _check("moe_grouped_wgrad", _lib.moe_grouped_wgrad(ctypes.byref(c), T, K, F, flags, px, pdy, ids, counts, padd,
@@ -639,7 +652,7 @@ def moe_grouped_wgrad(cfg, T, x, dy, sorted_route_ids, expert_counts, dw, ws, dw
 
 
 def _want_swiglu(c, T, gu, topk_gate, sorted_route_ids, num_padded):
-    rows = moe_max_padded_rows(c, T)
+    rows = _rows(c, T)
     return (rows, _want("gu", gu, "bfloat16", (rows, 2 * c.intermediate)),
             _want("topk_gate", topk_gate, "float32", (T, _slots(c)), True),
             _want_at_least("sorted_route_ids", sorted_route_ids, "int32", rows),

@@ -361,9 +361,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
   }
   if (warp == 0) {
     if (lane == 0) {
-      prefetch_tmap(&maps.a);
-      prefetch_tmap(&maps.b);
-      prefetch_tmap(&maps.b_small);
+      prefetch_tmap(args.gather_a ? &maps.a_rows : &maps.a);
+      prefetch_tmap(args.gather_b ? &maps.b_rows : &maps.b);
     }
     __syncwarp();
     // The set-up reads nothing an earlier kernel writes: it overlaps the end
@@ -856,10 +855,9 @@ bool launch_grouped_gemm(const GroupedGemmArgs& in, PFN_cuTensorMapEncodeTiled_v
   if (!(in.transposed ? map_rows(fn, &m.a, in.w, K, F, N, 128)
         : a.wide_a    ? map_wide(fn, &m.a, in.w, F, K, N)
                       : map_rows(fn, &m.a, in.w, F, K, N, kBK)) ||
-      !map_rows(fn, &m.b, in.x, K, rows, 0, 128) || !map_rows(fn, &m.b_small, in.x, K, rows, 0, kRowBox) ||
-      !map_rows(fn, &m.b_rows, in.x, K, rows, 0, 1))
+      !(in.gather ? map_rows(fn, &m.b_rows, in.x, K, rows, 0, 1)
+                  : map_rows(fn, &m.b, in.x, K, rows, 0, 128) && map_rows(fn, &m.b_small, in.x, K, rows, 0, kRowBox)))
     return false;
-  m.a_small = m.a_rows = m.b_rows;
   a.g = g;
   a.gather_b = in.gather;
   set_divisor(a, (uint32_t)g.slots);
@@ -882,13 +880,14 @@ bool launch_grouped_wgrad(const GroupedWgradArgs& in, PFN_cuTensorMapEncodeTiled
   Args a{};
   a.wide_a = K % 64 == 0;
   a.wide_b = F % 64 == 0;
-  auto maps_of = [&](const uint16_t* p, uint64_t cols, uint64_t rows, bool wide, CUtensorMap* box, CUtensorMap* small,
-                     CUtensorMap* one) {
-    return (wide ? map_wide(fn, box, p, cols, rows, 0) : map_rows(fn, box, p, cols, rows, 0, kBK)) &&
-           map_rows(fn, small, p, cols, rows, 0, kRowBox) && map_rows(fn, one, p, cols, rows, 0, 1);
+  auto maps_of = [&](const uint16_t* p, uint64_t cols, uint64_t rows, bool gather, bool wide, CUtensorMap* box,
+                     CUtensorMap* small, CUtensorMap* one) {
+    if (!map_rows(fn, one, p, cols, rows, 0, 1)) return false;
+    return gather || ((wide ? map_wide(fn, box, p, cols, rows, 0) : map_rows(fn, box, p, cols, rows, 0, kBK)) &&
+                      map_rows(fn, small, p, cols, rows, 0, kRowBox));
   };
-  if (!maps_of(in.x, K, xr, a.wide_a, &m.a, &m.a_small, &m.a_rows) ||
-      !maps_of(in.dy, F, dr, a.wide_b, &m.b, &m.b_small, &m.b_rows))
+  if (!maps_of(in.x, K, xr, in.gather_x, a.wide_a, &m.a, &m.a_small, &m.a_rows) ||
+      !maps_of(in.dy, F, dr, in.gather_dy, a.wide_b, &m.b, &m.b_small, &m.b_rows))
     return false;
   a.g = g;
   a.gather_a = in.gather_x;

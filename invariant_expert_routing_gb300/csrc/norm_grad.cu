@@ -113,12 +113,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 }
 
 // ---- the gradients of rows up to 8192 wide
-// A warp holds one chunk of two rows at a time, and its columns' sums over all
-// rows of the CTA, in registers; the rows behind them are on their way into
-// shared memory (cp.async: a thread copies what it reads itself, so no barrier
-// is needed for them).  Each byte moves once: bound by memory.
-constexpr int kRing = 4;              // rows in shared memory
-constexpr int kRowsAtOnce = 2;
+// A warp holds one chunk of a row, and its columns' sums over all rows of the
+// CTA, in registers; the rows behind it are on their way into shared memory
+// (cp.async: a thread copies what it reads itself, so no barrier is needed for
+// them), as many as fit: two rows at a time with two behind them left memory idle
+// (192 us for 16448 rows of 7168).  One barrier a row: it carries the row's
+// second moments together with the next row's sums.  Each byte moves once: bound
+// by memory.
 constexpr int kFusedMaxChunks = 32;
 
 // Sums of four values over the CTA, known to every thread: lane halves and
@@ -146,113 +147,164 @@ __device__ __forceinline__ void block_sum4(float (&q)[4], int warp, int lane, in
   for (int i = 0; i < 4; ++i) q[i] = __shfl_sync(0xffffffffu, t, 8 * i);
 }
 
+// Two fp32 values in one 64-bit register: an add, product or fma of both is one
+// instruction (the kernel issues two thirds of what it would one by one).
+struct F2 {
+  unsigned long long v = 0;
+};
+__device__ __forceinline__ F2 pair(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 both(float x) { return pair(x, x); }
+__device__ __forceinline__ float2 parts(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ float total(F2 a) {
+  const float2 p = parts(a);
+  return p.x + p.y;
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ void unpack(const uint4& p, F2 (&v)[4]) {
+  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint4 pack(const F2 (&v)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = parts(v[i]);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // part [grid][2][H]: each CTA's sums over its rows (blockIdx.x + i gridDim.x) of
 // dout n and dout.  dx may be dresidual (no __restrict__): a row is copied
 // before it is written, by the same thread.
-template <bool kCentre, bool kParams, int kThreads>
+template <bool kCentre, bool kParams, int kThreads, int kRing>
 __global__ void __launch_bounds__(kThreads)
     norm_backward_kernel(const uint16_t* v_in, const uint16_t* dout, const uint16_t* dresidual,
                          const uint16_t* __restrict__ weight, float eps, int T, int H, uint16_t* dx,
                          float* __restrict__ part) {
   extern __shared__ __align__(16) uint8_t ring[];   // [kRing][3][threads] of 16 bytes
-  __shared__ float s_sum[2][2][4][kFusedMaxChunks];  // [pair parity][round]
+  __shared__ float s_sum[2][4][kFusedMaxChunks];    // by the parity of the row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chunks = blockDim.x >> 5;
   const int c = threadIdx.x * 8;
   const bool in = c < H;
   const int rows = (int)blockIdx.x < T ? (T - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
-  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16;
-  auto slot = [&](int i, int tensor) { return (uint32_t)(((i % kRing) * 3 + tensor) * blockDim.x * 16); };
+  const uint8_t* own = ring + threadIdx.x * 16;
+  const uint32_t mine = smem_u32(own), plane = blockDim.x * 16;
   auto at = [&](int i) { return ((size_t)blockIdx.x + (size_t)i * gridDim.x) * H + c; };
-  auto request = [&](int i) {   // two rows i, i + 1
-#pragma unroll
-    for (int k = i; k < i + kRowsAtOnce; ++k) {
-      const bool have = in && k < rows;
-      const size_t a = have ? at(k) : 0;
-      cp_async16(mine + slot(k, 0), v_in + a, have ? 16 : 0);
-      cp_async16(mine + slot(k, 1), dout + a, have ? 16 : 0);
-      if (dresidual) cp_async16(mine + slot(k, 2), dresidual + a, have ? 16 : 0);
-    }
+  auto request = [&](int i, uint32_t slot) {
+    const bool have = in && i < rows;
+    const size_t a = have ? at(i) : 0;
+    const uint32_t dst = mine + slot * 3 * plane, n = have ? 16 : 0;
+    cp_async16(dst, v_in + a, n);
+    cp_async16(dst + plane, dout + a, n);
+    if (dresidual) cp_async16(dst + 2 * plane, dresidual + a, n);
     cp_async_commit();
+  };
+  auto piece = [&](uint32_t slot, int tensor, F2 (&v)[4]) {
+    unpack(*reinterpret_cast<const uint4*>(own + (slot * 3 + tensor) * plane), v);
   };
   pdl_wait();
   pdl_trigger();
-  request(0);
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) request(i, i);
   const uint4 wv = in ? __ldg(reinterpret_cast<const uint4*>(weight + c)) : make_uint4(0, 0, 0, 0);
   const float per = 1.0f / (float)H;
-  float dw[8] = {}, db[8] = {};
-  for (int i = 0; i < rows; i += kRowsAtOnce) {
-    request(i + kRowsAtOnce);
-    cp_async_wait<1>();
-    const uint8_t* own = ring + threadIdx.x * 16;
-    auto sums = s_sum[(i / kRowsAtOnce) & 1];
-    float d[2][8], g[2][8], w[8], q[4];
-    unpack8(wv, w);
+  F2 dw[4] = {}, db[4] = {};
+  // the sums of v and g of the row in a slot
+  auto row_sums = [&](uint32_t slot, float& sv, float& sg) {
+    F2 v[4], g[4], w[4];
+    piece(slot, 0, v);
+    piece(slot, 1, g);
+    unpack(wv, w);
+    sv = total(add(add(v[0], v[1]), add(v[2], v[3])));
+    F2 t = mul(g[0], w[0]);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      unpack8(*reinterpret_cast<const uint4*>(own + slot(i + k, 0)), d[k]);
-      unpack8(*reinterpret_cast<const uint4*>(own + slot(i + k, 1)), g[k]);
+    for (int j = 1; j < 4; ++j) t = fma(g[j], w[j], t);
+    sg = total(t);
+  };
+  float mean = 0.0f, mean_g = 0.0f;
+  if (kCentre) {
+    cp_async_wait<kRing - 2>();
+    float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    row_sums(0, q[2], q[3]);
+    block_sum4(q, warp, lane, chunks, s_sum[1]);
+    mean = q[2] * per;
+    mean_g = q[3] * per;
+  }
+  uint32_t slot = 0;
+  for (int i = 0; i < rows; ++i) {
+    const uint32_t behind = slot == 0 ? kRing - 1 : slot - 1, next = slot == kRing - 1 ? 0 : slot + 1;
+    request(i + kRing - 1, behind);   // into the slot of the row before
+    cp_async_wait<kRing - 2>();       // this row and the next
+    F2 d[4], g[4], w[4];
+    piece(slot, 0, d);
+    piece(slot, 1, g);
+    unpack(wv, w);
+    const F2 minus = both(in ? -mean : 0.0f);   // (past H everything stays zero)
+    F2 dd = both(0.0f), dg = both(0.0f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (kParams) db[j] += g[k][j];
-        g[k][j] *= w[j];
-      }
+    for (int j = 0; j < 4; ++j) {
+      if (kParams) db[j] = add(db[j], g[j]);
+      g[j] = mul(g[j], w[j]);
+      if (kCentre) d[j] = add(d[j], minus);
+      dd = fma(d[j], d[j], dd);
+      dg = fma(d[j], g[j], dg);
     }
-    float mean_g[2] = {0.0f, 0.0f};
-    if (kCentre) {
+    float q[4] = {total(dd), total(dg), 0.0f, 0.0f};
+    if (kCentre) row_sums(next, q[2], q[3]);
+    block_sum4(q, warp, lane, chunks, s_sum[i & 1]);
+    const float inv = 1.0f / sqrtf(q[0] * per + eps);
+    const float slope = q[1] * per * inv * inv;   // mean(g n) / root
+    const F2 inv2 = both(inv), slope2 = both(-slope), minus_g = both(-mean_g);
+    if (kParams) {
+      F2 o[4];
+      piece(slot, 1, o);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        q[2 * k] = q[2 * k + 1] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          q[2 * k] += d[k][j];
-          q[2 * k + 1] += g[k][j];
-        }
-      }
-      block_sum4(q, warp, lane, chunks, sums[0]);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float mean = q[2 * k] * per;
-        mean_g[k] = q[2 * k + 1] * per;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[k][j] = in ? d[k][j] - mean : 0.0f;
-      }
+      for (int j = 0; j < 4; ++j) dw[j] = fma(o[j], mul(d[j], inv2), dw[j]);
     }
+    F2 r[4] = {};
+    if (dresidual) piece(slot, 2, r);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      q[2 * k] = q[2 * k + 1] = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        q[2 * k] = fmaf(d[k][j], d[k][j], q[2 * k]);
-        q[2 * k + 1] = fmaf(d[k][j], g[k][j], q[2 * k + 1]);
-      }
+    for (int j = 0; j < 4; ++j) {
+      if (kCentre) g[j] = add(g[j], minus_g);
+      r[j] = fma(fma(d[j], slope2, g[j]), inv2, r[j]);
     }
-    block_sum4(q, warp, lane, chunks, sums[1]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (i + k >= rows) break;
-      const float inv = 1.0f / sqrtf(q[2 * k] * per + eps);
-      const float slope = q[2 * k + 1] * per * inv * inv;   // mean(g n) / root
-      if (kParams) {
-        float o[8];
-        unpack8(*reinterpret_cast<const uint4*>(own + slot(i + k, 1)), o);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dw[j] = fmaf(o[j], d[k][j] * inv, dw[j]);
-      }
-      float r[8] = {};
-      if (dresidual) unpack8(*reinterpret_cast<const uint4*>(own + slot(i + k, 2)), r);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) r[j] = fmaf(g[k][j] - mean_g[k] - d[k][j] * slope, inv, r[j]);
-      if (in) __stcs(reinterpret_cast<uint4*>(dx + at(i + k)), pack_bf16(r));
-    }
+    if (in) __stcs(reinterpret_cast<uint4*>(dx + at(i)), pack(r));
+    mean = q[2] * per;
+    mean_g = q[3] * per;
+    slot = next;
   }
   cp_async_wait<0>();
   if (kParams && in) {
-    float4* p = reinterpret_cast<float4*>(part + (size_t)blockIdx.x * 2 * H + c);
-    p[0] = make_float4(dw[0], dw[1], dw[2], dw[3]);
-    p[1] = make_float4(dw[4], dw[5], dw[6], dw[7]);
-    p = reinterpret_cast<float4*>(part + ((size_t)blockIdx.x * 2 + 1) * H + c);
-    p[0] = make_float4(db[0], db[1], db[2], db[3]);
-    p[1] = make_float4(db[4], db[5], db[6], db[7]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      *reinterpret_cast<F2*>(part + (size_t)blockIdx.x * 2 * H + c + 2 * j) = dw[j];
+      *reinterpret_cast<F2*>(part + ((size_t)blockIdx.x * 2 + 1) * H + c + 2 * j) = db[j];
+    }
   }
 }
 
@@ -407,10 +459,10 @@ size_t norm_backward_scratch_bytes(int T, int H) {
   return sizeof(float2) * (size_t)T + sizeof(float) * 2 * (size_t)H * kMaxSlabs;
 }
 
-template <bool kCentre, bool kParams, int kThreads>
+template <bool kCentre, bool kParams, int kThreads, int kRing>
 void launch_fused(const uint16_t* v, const uint16_t* dout, const uint16_t* dresidual, const uint16_t* weight, float eps,
                   int T, int H, uint16_t* dx, float* part, int ctas, cudaStream_t s) {
-  auto kernel = norm_backward_kernel<kCentre, kParams, kThreads>;
+  auto kernel = norm_backward_kernel<kCentre, kParams, kThreads, kRing>;
   const int threads = 32 * ((H + kChunk - 1) / kChunk), smem = kRing * 3 * 16 * threads;
   static bool attr_set[64] = {false};
   int dev = 0;
@@ -432,14 +484,14 @@ void launch_norm_backward(const uint16_t* v, const uint16_t* dout, const uint16_
   if (chunks <= kFusedMaxChunks) {
     slabs = fused_ctas(H, T);
     auto go = [&](auto kernel) { kernel(v, dout, dresidual, weight, eps, T, H, dx, part, slabs, s); };
-    // (compiled for the threads it needs: more registers a thread for fewer)
+    // rows in shared memory: what 227 KB hold, of the CTAs on an SM together
     auto sized = [&](auto c, auto p) {
       if (chunks <= 16)
-        go(launch_fused<decltype(c)::value, decltype(p)::value, 512>);
+        go(launch_fused<decltype(c)::value, decltype(p)::value, 512, 4>);
       else if (chunks <= 28)
-        go(launch_fused<decltype(c)::value, decltype(p)::value, 896>);
+        go(launch_fused<decltype(c)::value, decltype(p)::value, 896, 5>);
       else
-        go(launch_fused<decltype(c)::value, decltype(p)::value, 1024>);
+        go(launch_fused<decltype(c)::value, decltype(p)::value, 1024, 4>);
     };
     if (centre)
       params ? sized(std::true_type{}, std::true_type{}) : sized(std::true_type{}, std::false_type{});
