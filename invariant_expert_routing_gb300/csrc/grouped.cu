@@ -272,6 +272,11 @@ struct PartsEnd {
   int issued[kMostParts], gave_up;
 };
 
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
 // Among four lanes in turn, each with a row of four 32-byte blocks: lane q's
 // block j becomes lane j's block q, so that four lanes hold 128 bytes of a row
 // (an access of 32 bytes a row is a request of its own to L2: 454 us for the
@@ -647,19 +652,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
       if (in_parts) acc ^= 1;   // where the sum is
       const uint32_t tbase = tmem + ((uint32_t)(quarter * 32) << 16) + acc * kTile;
       if (!wgrad(kMode)) {
-        // a lane is an output feature, a column a row of y
-        const int feat = it.b * kTile + (int)rank * 128 + quarter * 32 + lane;
-        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(args.out) + (size_t)it.row0 * F + feat;
-        for (int c = col0; c < col0 + kTile / 2 && c < it.rows; c += 16) {
-          float v[16];
-          tmem_ld16(tbase + c, v);
-          tmem_wait_ld();
-          if (feat < F) {
+        // A lane is an output feature, a column a row of y.  Neighbouring lanes
+        // exchange halves, so that an even lane has two features of the even rows,
+        // an odd one of the odd rows: half the stores and addresses.
+        const int odd = lane & 1;
+        const int feat = it.b * kTile + (int)rank * 128 + quarter * 32 + (lane & ~1);
+        const size_t step = 4 * (size_t)F;   // bytes of two rows
+        for (int c = col0; c < col0 + kTile / 2 && c < it.rows; c += 32) {
+          float v[32];
+          mx::tmem_load32(tbase + c, v);
+          uint8_t* out = reinterpret_cast<uint8_t*>(args.out) + 2 * ((size_t)(it.row0 + c + odd) * F + feat);
+          const int left = feat < F ? it.rows - c - odd : 0;   // rows from this lane's first on
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (c + j < it.rows) out[(size_t)(c + j) * F] = __float2bfloat16_rn(v[j]);
+          for (int j = 0; j < 32; j += 4) {
+            const uint32_t p = pack2(v[j], v[j + 1]), q = pack2(v[j + 2], v[j + 3]);
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, __byte_perm(p, q, odd ? 0x5410 : 0x7632), 1);
+            const uint32_t lo = __byte_perm(p, got, odd ? 0x3254 : 0x5410), hi = __byte_perm(q, got, odd ? 0x3276 : 0x7610);
+            if (j < left) *reinterpret_cast<uint32_t*>(out) = lo;
+            if (j + 2 < left) *reinterpret_cast<uint32_t*>(out + step) = hi;
+            out += 2 * step;
           }
-          __syncwarp();   // tmem_ld16 is one instruction of the whole warp
+          __syncwarp();   // the next columns are loaded by the whole warp
         }
       } else {
         Item ahead = it;
@@ -671,14 +684,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
           if (!args.fp32) {
             float u[32] = {};
             if (!empty) mx::tmem_load32(tbase + col0 + c + 32, u);
-            auto pair = [](float lo, float hi) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-              return __uint_as_float(*reinterpret_cast<const uint32_t*>(&b));
-            };
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = pair(v[2 * j], v[2 * j + 1]);
+            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(pack2(v[2 * j], v[2 * j + 1]));
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[16 + j] = pair(u[2 * j], u[2 * j + 1]);
+            for (int j = 0; j < 16; ++j) v[16 + j] = __uint_as_float(pack2(u[2 * j], u[2 * j + 1]));
           }
           transpose4(v, lane);
           if (kMode == kWgradAdd) {
