@@ -8,8 +8,8 @@
 // M = 256, K = 16 a step, 64 a stage); each CTA holds half of the rows of A
 // and of B in its shared memory and half of the sums in its tensor memory.
 //   product:  A = 256 output features of W_e (K rows of features, MN-major; its
-//             transpose, features of K: K-major), B = up to 256 rows of x
-//             (K-major).  The MMA's N is the tile's rows rounded up to 32:
+//             transpose, features of K: K-major), twice for items of two groups
+//             (wide_items), B = up to 256 rows of x (K-major).  The MMA's N is the tile's rows rounded up to 32:
 //             columns of an MMA are independent sums over the same K steps, so
 //             a row's bits depend neither on N nor on the batch.
 //   gradient: A = 256 columns of x, B = 256 columns of dy, both MN-major, K
@@ -30,6 +30,7 @@
 // product is one launch and no list lives in memory.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
+#include <cmath>
 #include <cstdint>
 
 #include "gemm.h"
@@ -49,11 +50,12 @@ constexpr int kTile = 256;                           // features and rows of a p
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (2 + kEpiWarps) * 32;       // with one requesting warp
 constexpr uint32_t kOperandBytes = 2 * kBoxBytes;    // a CTA's 128 rows of one operand
-constexpr uint32_t kStageBytes = 2 * kOperandBytes;
 constexpr int kRowBox = 16;                          // rows of a box of a ragged tile
 constexpr uint32_t kRowBoxBytes = kRowBox * 128 * 2;   // of an MN-major operand: 128 columns
 
-enum Mode { kGemm, kGemmTransposed, kWgrad, kWgradAdd };
+enum Mode { kGemm, kGemmWide, kGemmTransposed, kGemmTransposedWide, kWgrad, kWgradAdd };
+__host__ __device__ constexpr bool transposed(Mode m) { return m == kGemmTransposed || m == kGemmTransposedWide; }
+__host__ __device__ constexpr int groups(Mode m) { return m == kGemmWide || m == kGemmTransposedWide ? 2 : 1; }
 __host__ __device__ constexpr bool wgrad(Mode m) { return m >= kWgrad; }
 
 // A gradient sums at most this many stages of 64 rows in an accumulator.  The
@@ -71,7 +73,9 @@ constexpr int kPartStagesFp32 = 12, kPartStagesBf16 = 128;
 constexpr uint32_t kAddBlock = 32 * 128;
 template <Mode kMode>
 struct Cfg {
-  static constexpr int kStages = kMode == kWgradAdd ? 4 : 6;
+  static constexpr int kGroups = groups(kMode);   // 256-feature groups of an item
+  static constexpr uint32_t kABytes = kGroups * kOperandBytes, kStageBytes = kABytes + kOperandBytes;
+  static constexpr int kStages = kMode == kWgradAdd || kGroups > 1 ? 4 : 6;
   // Requesting warps of a launch that may gather.  A warp that asked for stage
   // number n goes on to n + kParts knowing that n - kStages was consumed; for the
   // parity of the stage's barrier to tell its phases apart, n + kParts - 2 kStages
@@ -317,7 +321,8 @@ __device__ __forceinline__ void store8(void* p, bool wide, const uint32_t* w) {
 template <Mode kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThreads, 1)
     grouped_kernel(const __grid_constant__ Maps maps, const Args args) {
-  constexpr int kStages = Cfg<kMode>::kStages, kParts = Cfg<kMode>::kParts;
+  constexpr int kStages = Cfg<kMode>::kStages, kParts = Cfg<kMode>::kParts, kGroups = Cfg<kMode>::kGroups;
+  constexpr uint32_t kABytes = Cfg<kMode>::kABytes, kStageBytes = Cfg<kMode>::kStageBytes;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Segments seg;
   __shared__ uint32_t s_tmem_base;
@@ -413,7 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
       // product: this CTA's rows of the tile; gradient: this CTA's columns
       const int half = half_rows(it.rows);
       const int brow0 = it.row0 + me * half;
-      const int acol = it.a * kTile + me * 128, bcol = it.b * kTile + me * 128;
+      const int acol = it.a * kTile + me * 128, bcol = it.b * kGroups * kTile + me * 128;
       const int first = (part + parts - n0 % parts) % parts;   // this warp's first stage of the item
       int4 next = {};   // gradient: rows of the next stage, x in lanes 0..15, dy in lanes 16..31
       const bool gather_mine = lane < 16 ? oa.gather : ob.gather;
@@ -439,21 +444,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
           ok = false;
           break;
         }
-        const uint32_t sA = s0 + stage * kStageBytes, sB = sA + kOperandBytes;
+        const uint32_t sA = s0 + stage * kStageBytes, sB = sA + kABytes;
         const uint32_t fb = full_lead + 8 * stage;
         const int k0 = ks * kBK;
         if (!wgrad(kMode)) {
           if (mx::elect_one()) {
-            const uint32_t tx = kOperandBytes + (uint32_t)half * kBK * 2;
+            const uint32_t tx = kABytes + (uint32_t)half * kBK * 2;
             s_tx[stage] = tx;
             if (lead) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * tx);
-            if (kMode == kGemmTransposed) {
-              mx::tma_load_3d_pair(sA, &maps.a, k0, bcol, it.e, fb, pol_w);
-            } else if (args.wide_a) {
-              tma_load_4d_pair(sA, &maps.a, 0, k0, bcol >> 6, it.e, fb, pol_w);
-            } else {
-              mx::tma_load_3d_pair(sA, &maps.a, bcol, k0, it.e, fb, pol_w);
-              mx::tma_load_3d_pair(sA + kBoxBytes, &maps.a, bcol + 64, k0, it.e, fb, pol_w);
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+              const uint32_t to = sA + g * kOperandBytes;
+              const int col = bcol + g * kTile;
+              if (transposed(kMode)) {
+                mx::tma_load_3d_pair(to, &maps.a, k0, col, it.e, fb, pol_w);
+              } else if (args.wide_a) {
+                tma_load_4d_pair(to, &maps.a, 0, k0, col >> 6, it.e, fb, pol_w);
+              } else {
+                mx::tma_load_3d_pair(to, &maps.a, col, k0, it.e, fb, pol_w);
+                mx::tma_load_3d_pair(to + kBoxBytes, &maps.a, col + 64, k0, it.e, fb, pol_w);
+              }
             }
             if (args.gather_b) {
 #pragma unroll 8
@@ -504,10 +514,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
       // descriptors of stage 0, K step 0; a K = 16 step adds 2 KB to an
       // MN-major operand (64-wide atoms 8 KB apart, 8-row K groups 1 KB) and
       // 32 B to a K-major one, in the 16-byte units of the address field
-      constexpr bool kAMn = kMode != kGemmTransposed, kBMn = wgrad(kMode);
+      constexpr bool kAMn = !transposed(kMode), kBMn = wgrad(kMode);
       constexpr uint32_t kAStep = kAMn ? 128 : 2, kBStep = kBMn ? 128 : 2;
       const uint64_t adesc0 = sdesc_sw128(smem_u32(smem), kAMn ? kBoxBytes : 16, 1024);
-      const uint64_t bdesc0 = sdesc_sw128(smem_u32(smem) + kOperandBytes, kBMn ? kBoxBytes : 16, 1024);
+      const uint64_t bdesc0 = sdesc_sw128(smem_u32(smem) + kABytes, kBMn ? kBoxBytes : 16, 1024);
       uint32_t soff = 0;
       for (int item = pair0; item < total && ok; item += pairs) {
         const Item it = item_of<kMode>(args, seg, item);
@@ -535,7 +545,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk)
-              if (kk * 16 < left) mma_bf16_pair(d0, ad + kk * kAStep, bd + kk * kBStep, idesc, !first || kk != 0 ? 1u : 0u);
+              if (kk * 16 < left) {
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g)
+                  mma_bf16_pair(d0 + g * kTile, ad + g * (kOperandBytes >> 4) + kk * kAStep, bd + kk * kBStep, idesc,
+                                !first || kk != 0 ? 1u : 0u);
+              }
             mma_commit_pair(empty0 + 8 * stage, 0x3);
             if (left_in_part == 0) mma_commit_pair(tfull0 + 8 * acc, 0x3);
           }
@@ -555,7 +570,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
         // starts in this one while they store from that one.
         if (ksteps > part_stages)
           ok = take(acc ^ 1);
-        else
+        else if (kGroups == 1)
           acc ^= 1;
       }
       if (!ok) {
@@ -656,11 +671,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
         // exchange halves, so that an even lane has two features of the even rows,
         // an odd one of the odd rows: half the stores and addresses.
         const int odd = lane & 1;
-        const int feat = it.b * kTile + (int)rank * 128 + quarter * 32 + (lane & ~1);
         const size_t step = 4 * (size_t)F;   // bytes of two rows
-        for (int c = col0; c < col0 + kTile / 2 && c < it.rows; c += 32) {
+        for (int n = 0; n < kGroups * kTile / 2; n += 32) {
+          const int g = n / (kTile / 2), c = col0 + n % (kTile / 2);
+          const int feat = (it.b * kGroups + g) * kTile + (int)rank * 128 + quarter * 32 + (lane & ~1);
+          if (c >= it.rows) continue;   // the same for the whole warp
           float v[32];
-          mx::tmem_load32(tbase + c, v);
+          mx::tmem_load32(tbase + g * kTile + c, v);
           uint8_t* out = reinterpret_cast<uint8_t*>(args.out) + 2 * ((size_t)(it.row0 + c + odd) * F + feat);
           const int left = feat < F ? it.rows - c - odd : 0;   // rows from this lane's first on
 #pragma unroll
@@ -732,7 +749,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
       }
       if (empty) continue;
       release(acc);
-      acc ^= 1;
+      if (kGroups == 1) acc ^= 1;
     }
   }
 
@@ -853,6 +870,21 @@ long long routes_of(const GroupArgs& g) {
   return r < g.max_rows ? r : g.max_rows;
 }
 
+// Whether a product's items have two groups of 256 features.  They request a
+// row tile once for both, but keep one accumulator, whose stores nothing overlaps,
+// and leave the last wave of items emptier.  The time of a wave of double items
+// over that of two waves of single ones was 0.94 for gathered rows (whose requests
+// bound: W2's input gradient of 4096 tokens in the 8-expert layer 659 -> 608 us),
+// 1.03 for rows in place, 0.9 where experts average at most 128 rows; the waves
+// follow from the tiles to be expected, half of an expert's last one filled.
+bool wide_items(const GroupArgs& g, bool gather, int sms) {
+  const double routes = (double)routes_of(g), experts = routes < g.N ? routes : g.N;
+  const double tiles = routes / kTile + 0.5 * experts, units = sms / 2;
+  const double one = std::ceil(tiles * ((g.F + kTile - 1) / kTile) / units);
+  const double two = std::ceil(tiles * ((g.F + 2 * kTile - 1) / (2 * kTile)) / units);
+  return 2.0 * two * (routes <= 128.0 * g.N ? 0.9 : gather ? 0.94 : 1.03) < one;
+}
+
 }  // namespace
 
 bool launch_grouped_gemm(const GroupedGemmArgs& in, PFN_cuTensorMapEncodeTiled_v12000 fn, int sms, cudaStream_t s) {
@@ -872,9 +904,14 @@ bool launch_grouped_gemm(const GroupedGemmArgs& in, PFN_cuTensorMapEncodeTiled_v
   set_divisor(a, (uint32_t)g.slots);
   a.out = in.y;
   a.na = 1;
-  a.nb = (g.F + kTile - 1) / kTile;
   const long long routes = routes_of(g), tiles = routes / kTile + (routes < g.N ? routes : g.N);
-  if (in.transposed)
+  const bool wide = wide_items(g, in.gather, sms);
+  a.nb = wide ? (g.F + 2 * kTile - 1) / (2 * kTile) : (g.F + kTile - 1) / kTile;
+  if (wide && in.transposed)
+    launch<kGemmTransposedWide>(m, a, tiles * a.nb, sms, s);
+  else if (wide)
+    launch<kGemmWide>(m, a, tiles * a.nb, sms, s);
+  else if (in.transposed)
     launch<kGemmTransposed>(m, a, tiles * a.nb, sms, s);
   else
     launch<kGemm>(m, a, tiles * a.nb, sms, s);

@@ -396,3 +396,19 @@ def test_long_segments_keep_fp32_sums(moe, n, add):
     assert float((got[1] - want[1]).norm() / want[1].norm()) <= 4 * 2.0 ** -23 + (2.0 ** -23 if add else 0)
     # a bf16 gradient is rounded once; its parts are 512 steps long
     assert float((half[0].double() - want[0]).norm() / want[0].norm()) <= 2.0 ** -8 + 512 * 2.0 ** -23
+
+
+@pytest.mark.parametrize("F", [2048, 2056, 1800])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_one_and_two_groups_of_features_give_the_same_bits(moe, transposed, F):
+    """4000 tokens, 2 of 4 experts, F about 2048: items of two groups for gathered rows, of one for rows in place."""
+    torch = torch_()
+    from tests import train_ref as R
+    G, K, g = R.Groups(4000, 4, 2, 8, seed=5), 136, _gen(F)
+    x, w = _randn(g, G.T, K), _randn(g, *((4, F, K) if transposed else (4, K, F)), scale=0.1)
+    xp = torch.full((G.rows, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+    xp[G.real] = x[G.ids[G.real].long() // G.k]
+    y, yp = _gemm(moe, G, x, w, True, transposed), _gemm(moe, G, xp, w, False, transposed)
+    assert torch.equal(y, yp)
+    want, mag = R.gemm(G, x, w, True, transposed)
+    R.check(y[G.real], want[G.real], R.BF * want[G.real].abs() + R.sum_tol(K) * mag[G.real])

@@ -7,7 +7,7 @@ from tests.test_gpu_train import _gen, _randn
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("T,K,F", [(64, 128, 512), (700, 1096, 1032)])
+@pytest.mark.parametrize("T,K,F", [(64, 128, 512), (700, 1096, 1032), (8000, 136, 2048)])
 @pytest.mark.parametrize("form", ["in place", "gather", "transposed", "wgrad", "wgrad gather"])
 def test_wait_runs_out_and_reports(moe, form, T, K, F):
     torch = torch_()
