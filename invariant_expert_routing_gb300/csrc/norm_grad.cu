@@ -113,19 +113,20 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 }
 
 // ---- the gradients of rows up to 8192 wide
-// A warp holds one chunk of a row, and its columns' sums over all rows of the
+// A warp holds two chunks of a row, and its columns' sums over all rows of the
 // CTA, in registers; the rows behind it are on their way into shared memory
 // (cp.async: a thread copies what it reads itself, so no barrier is needed for
 // them), as many as fit: two rows at a time with two behind them left memory idle
 // (192 us for 16448 rows of 7168).  One barrier a row: it carries the row's
-// second moments together with the next row's sums.  Each byte moves once: bound
-// by memory.
-constexpr int kFusedMaxChunks = 32;
+// second moments together with the next row's sums, whose values stay in
+// registers (one chunk a warp, read twice: 173 us, by instruction issue).  Each
+// byte moves once.
+constexpr int kFusedMaxChunks = 32, kFusedMaxWarps = 16;
 
 // Sums of four values over the CTA, known to every thread: lane halves and
 // quarters exchange values, so that each eighth lane group ends with one of the
-// four; then 8 lanes a value add the chunks' sums.  s_sum: one array a call.
-__device__ __forceinline__ void block_sum4(float (&q)[4], int warp, int lane, int chunks, float (*s_sum)[kFusedMaxChunks]) {
+// four; then 8 lanes a value add the warps' sums.  s_sum: one array a call.
+__device__ __forceinline__ void block_sum4(float (&q)[4], int warp, int lane, int warps, float (*s_sum)[kFusedMaxWarps]) {
   const bool hi = lane & 16;
   float a = hi ? q[2] : q[0], b = hi ? q[3] : q[1];
   a += __shfl_xor_sync(0xffffffffu, hi ? q[0] : q[2], 16);
@@ -139,8 +140,8 @@ __device__ __forceinline__ void block_sum4(float (&q)[4], int warp, int lane, in
   __syncthreads();
   t = 0.0f;
 #pragma unroll
-  for (int c = 0; c < kFusedMaxChunks; c += 8)
-    if (c + (lane & 7) < chunks) t += s_sum[lane >> 3][c + (lane & 7)];
+  for (int c = 0; c < kFusedMaxWarps; c += 8)
+    if (c + (lane & 7) < warps) t += s_sum[lane >> 3][c + (lane & 7)];
 #pragma unroll
   for (int off = 4; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
 #pragma unroll
@@ -198,113 +199,135 @@ __device__ __forceinline__ uint4 pack(const F2 (&v)[4]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// What is summed over the rows: nothing, dout n (16 registers fewer, without which
+// the RMS norm's sums would spill: 192 us for 151), and dout.
+enum Sums { kNone, kWeight, kBoth };
+
 // part [grid][2][H]: each CTA's sums over its rows (blockIdx.x + i gridDim.x) of
 // dout n and dout.  dx may be dresidual (no __restrict__): a row is copied
 // before it is written, by the same thread.
-template <bool kCentre, bool kParams, int kThreads, int kRing>
+template <bool kCentre, Sums kSums, int kThreads, int kRing>
 __global__ void __launch_bounds__(kThreads)
     norm_backward_kernel(const uint16_t* v_in, const uint16_t* dout, const uint16_t* dresidual,
                          const uint16_t* __restrict__ weight, float eps, int T, int H, uint16_t* dx,
                          float* __restrict__ part) {
-  extern __shared__ __align__(16) uint8_t ring[];   // [kRing][3][threads] of 16 bytes
-  __shared__ float s_sum[2][4][kFusedMaxChunks];    // by the parity of the row
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chunks = blockDim.x >> 5;
-  const int c = threadIdx.x * 8;
-  const bool in = c < H;
+  extern __shared__ __align__(16) uint8_t ring[];   // [kRing][3][2][threads] of 16 bytes
+  __shared__ float s_sum[2][4][kFusedMaxWarps];     // by the parity of the row
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int c[2] = {(int)threadIdx.x * 8, (int)(threadIdx.x + blockDim.x) * 8};   // this thread's columns
+  const bool in[2] = {c[0] < H, c[1] < H};
   const int rows = (int)blockIdx.x < T ? (T - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
   const uint8_t* own = ring + threadIdx.x * 16;
   const uint32_t mine = smem_u32(own), plane = blockDim.x * 16;
-  auto at = [&](int i) { return ((size_t)blockIdx.x + (size_t)i * gridDim.x) * H + c; };
-  auto request = [&](int i, uint32_t slot) {
-    const bool have = in && i < rows;
-    const size_t a = have ? at(i) : 0;
-    const uint32_t dst = mine + slot * 3 * plane, n = have ? 16 : 0;
-    cp_async16(dst, v_in + a, n);
-    cp_async16(dst + plane, dout + a, n);
-    if (dresidual) cp_async16(dst + 2 * plane, dresidual + a, n);
+  const size_t stride = (size_t)gridDim.x * H;
+  size_t ahead = (size_t)blockIdx.x * H;   // the row to request next
+  int asked = 0;
+  auto request = [&](uint32_t slot) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool have = in[h] && asked < rows;
+      const size_t a = have ? ahead + c[h] : 0;
+      const uint32_t dst = mine + (slot * 6 + h) * plane, n = have ? 16 : 0;
+      cp_async16(dst, v_in + a, n);
+      cp_async16(dst + 2 * plane, dout + a, n);
+      if (dresidual) cp_async16(dst + 4 * plane, dresidual + a, n);
+    }
     cp_async_commit();
+    ahead += stride;
+    ++asked;
   };
-  auto piece = [&](uint32_t slot, int tensor, F2 (&v)[4]) {
-    unpack(*reinterpret_cast<const uint4*>(own + (slot * 3 + tensor) * plane), v);
+  auto piece = [&](uint32_t slot, int tensor, int h, F2 (&v)[4]) {
+    unpack(*reinterpret_cast<const uint4*>(own + (slot * 6 + tensor * 2 + h) * plane), v);
   };
   pdl_wait();
   pdl_trigger();
 #pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) request(i, i);
-  const uint4 wv = in ? __ldg(reinterpret_cast<const uint4*>(weight + c)) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < kRing - 1; ++i) request(i);
   const float per = 1.0f / (float)H;
-  F2 dw[4] = {}, db[4] = {};
-  // the sums of v and g of the row in a slot
-  auto row_sums = [&](uint32_t slot, float& sv, float& sg) {
-    F2 v[4], g[4], w[4];
-    piece(slot, 0, v);
-    piece(slot, 1, g);
-    unpack(wv, w);
-    sv = total(add(add(v[0], v[1]), add(v[2], v[3])));
-    F2 t = mul(g[0], w[0]);
+  F2 w[2][4], dw[2][4] = {}, db[2][4] = {};
 #pragma unroll
-    for (int j = 1; j < 4; ++j) t = fma(g[j], w[j], t);
-    sg = total(t);
+  for (int h = 0; h < 2; ++h)
+    unpack(in[h] ? __ldg(reinterpret_cast<const uint4*>(weight + c[h])) : make_uint4(0, 0, 0, 0), w[h]);
+  // the row in a slot, and the sums of v and g = dout w (unused for the RMS norm)
+  auto read = [&](uint32_t slot, F2 (&v)[2][4], F2 (&o)[2][4], float& sv, float& sg) {
+    F2 tv = both(0.0f), tg = both(0.0f);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      piece(slot, 0, h, v[h]);
+      piece(slot, 1, h, o[h]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        tv = add(tv, v[h][j]);
+        tg = fma(o[h][j], w[h][j], tg);
+        if (kSums == kBoth) db[h][j] = add(db[h][j], o[h][j]);
+      }
+    }
+    sv = total(tv);
+    sg = total(tg);
   };
-  float mean = 0.0f, mean_g = 0.0f;
-  if (kCentre) {
-    cp_async_wait<kRing - 2>();
-    float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    row_sums(0, q[2], q[3]);
-    block_sum4(q, warp, lane, chunks, s_sum[1]);
-    mean = q[2] * per;
-    mean_g = q[3] * per;
-  }
+  F2 d[2][4], o[2][4];
+  float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  cp_async_wait<kRing - 2>();
+  read(0, d, o, q[2], q[3]);
+  if (kCentre) block_sum4(q, warp, lane, warps, s_sum[1]);
+  float mean = q[2] * per, mean_g = q[3] * per;
   uint32_t slot = 0;
+  size_t at = (size_t)blockIdx.x * H;
   for (int i = 0; i < rows; ++i) {
     const uint32_t behind = slot == 0 ? kRing - 1 : slot - 1, next = slot == kRing - 1 ? 0 : slot + 1;
-    request(i + kRing - 1, behind);   // into the slot of the row before
-    cp_async_wait<kRing - 2>();       // this row and the next
-    F2 d[4], g[4], w[4];
-    piece(slot, 0, d);
-    piece(slot, 1, g);
-    unpack(wv, w);
-    const F2 minus = both(in ? -mean : 0.0f);   // (past H everything stays zero)
+    request(behind);              // into the slot of the row before
+    cp_async_wait<kRing - 2>();   // this row and the next
     F2 dd = both(0.0f), dg = both(0.0f);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (kParams) db[j] = add(db[j], g[j]);
-      g[j] = mul(g[j], w[j]);
-      if (kCentre) d[j] = add(d[j], minus);
-      dd = fma(d[j], d[j], dd);
-      dg = fma(d[j], g[j], dg);
+    for (int h = 0; h < 2; ++h) {
+      const F2 minus = both(in[h] ? -mean : 0.0f);   // (past H everything stays zero)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (kCentre) d[h][j] = add(d[h][j], minus);
+        dd = fma(d[h][j], d[h][j], dd);
+        dg = fma(d[h][j], mul(o[h][j], w[h][j]), dg);
+      }
     }
-    float q[4] = {total(dd), total(dg), 0.0f, 0.0f};
-    if (kCentre) row_sums(next, q[2], q[3]);
-    block_sum4(q, warp, lane, chunks, s_sum[i & 1]);
+    q[0] = total(dd);
+    q[1] = total(dg);
+    F2 dn[2][4], on[2][4];
+    read(next, dn, on, q[2], q[3]);
+    block_sum4(q, warp, lane, warps, s_sum[i & 1]);
     const float inv = 1.0f / sqrtf(q[0] * per + eps);
     const float slope = q[1] * per * inv * inv;   // mean(g n) / root
     const F2 inv2 = both(inv), slope2 = both(-slope), minus_g = both(-mean_g);
-    if (kParams) {
-      F2 o[4];
-      piece(slot, 1, o);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) dw[j] = fma(o[j], mul(d[j], inv2), dw[j]);
-    }
-    F2 r[4] = {};
-    if (dresidual) piece(slot, 2, r);
+    for (int h = 0; h < 2; ++h) {
+      F2 r[4] = {};
+      if (dresidual) piece(slot, 2, h, r);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (kCentre) g[j] = add(g[j], minus_g);
-      r[j] = fma(fma(d[j], slope2, g[j]), inv2, r[j]);
+      for (int j = 0; j < 4; ++j) {
+        if (kSums != kNone) dw[h][j] = fma(o[h][j], mul(d[h][j], inv2), dw[h][j]);
+        const F2 g = kCentre ? fma(o[h][j], w[h][j], minus_g) : mul(o[h][j], w[h][j]);
+        r[j] = fma(fma(d[h][j], slope2, g), inv2, r[j]);
+      }
+      if (in[h]) __stcs(reinterpret_cast<uint4*>(dx + at + c[h]), pack(r));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        d[h][j] = dn[h][j];
+        o[h][j] = on[h][j];
+      }
     }
-    if (in) __stcs(reinterpret_cast<uint4*>(dx + at(i)), pack(r));
     mean = q[2] * per;
     mean_g = q[3] * per;
     slot = next;
+    at += stride;
   }
   cp_async_wait<0>();
-  if (kParams && in) {
+  if (kSums != kNone) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      *reinterpret_cast<F2*>(part + (size_t)blockIdx.x * 2 * H + c + 2 * j) = dw[j];
-      *reinterpret_cast<F2*>(part + ((size_t)blockIdx.x * 2 + 1) * H + c + 2 * j) = db[j];
-    }
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (!in[h]) break;
+        *reinterpret_cast<F2*>(part + (size_t)blockIdx.x * 2 * H + c[h] + 2 * j) = dw[h][j];
+        if (kSums == kBoth) *reinterpret_cast<F2*>(part + ((size_t)blockIdx.x * 2 + 1) * H + c[h] + 2 * j) = db[h][j];
+      }
   }
 }
 
@@ -447,10 +470,11 @@ void launch_add_layer_norm(const uint16_t* x, const uint16_t* residual, const ui
     go(add_layer_norm_kernel<4, 1024, 1>, 4);
 }
 
-// CTAs of the fused kernel for rows of H: as many as fill 152 SMs once (a
-// constant, so that the columns' sums have one order for a size).
+// The fused kernel's threads for rows of H, and CTAs: as many as fill 152 SMs
+// once (a constant, so that the columns' sums have one order for a size).
+int fused_threads(int H) { return 32 * ((H + 2 * kChunk - 1) / (2 * kChunk)); }
 int fused_ctas(int H, int T) {
-  const int threads = 32 * ((H + kChunk - 1) / kChunk), most = 152 * (1024 / threads);
+  const int most = 152 * (512 / fused_threads(H));
   return T < most ? T : most;
 }
 
@@ -459,16 +483,16 @@ size_t norm_backward_scratch_bytes(int T, int H) {
   return sizeof(float2) * (size_t)T + sizeof(float) * 2 * (size_t)H * kMaxSlabs;
 }
 
-template <bool kCentre, bool kParams, int kThreads, int kRing>
+template <bool kCentre, Sums kSums, int kThreads, int kRing>
 void launch_fused(const uint16_t* v, const uint16_t* dout, const uint16_t* dresidual, const uint16_t* weight, float eps,
                   int T, int H, uint16_t* dx, float* part, int ctas, cudaStream_t s) {
-  auto kernel = norm_backward_kernel<kCentre, kParams, kThreads, kRing>;
-  const int threads = 32 * ((H + kChunk - 1) / kChunk), smem = kRing * 3 * 16 * threads;
+  auto kernel = norm_backward_kernel<kCentre, kSums, kThreads, kRing>;
+  const int threads = fused_threads(H), smem = kRing * 6 * 16 * threads;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing * 3 * 16 * kThreads);
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing * 6 * 16 * kThreads);
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   launch_pdl(kernel, dim3(ctas), dim3(threads), smem, s, v, dout, dresidual, weight, eps, T, H, dx, part);
@@ -485,18 +509,25 @@ void launch_norm_backward(const uint16_t* v, const uint16_t* dout, const uint16_
     slabs = fused_ctas(H, T);
     auto go = [&](auto kernel) { kernel(v, dout, dresidual, weight, eps, T, H, dx, part, slabs, s); };
     // rows in shared memory: what 227 KB hold, of the CTAs on an SM together
-    auto sized = [&](auto c, auto p) {
+    auto sized = [&](auto c, auto n) {
+      constexpr bool kCentre = decltype(c)::value;
+      constexpr Sums kSums = decltype(n)::value;
       if (chunks <= 16)
-        go(launch_fused<decltype(c)::value, decltype(p)::value, 512, 4>);
+        go(launch_fused<kCentre, kSums, 256, 4>);
       else if (chunks <= 28)
-        go(launch_fused<decltype(c)::value, decltype(p)::value, 896, 5>);
+        go(launch_fused<kCentre, kSums, 448, 5>);
       else
-        go(launch_fused<decltype(c)::value, decltype(p)::value, 1024, 4>);
+        go(launch_fused<kCentre, kSums, 512, 4>);
     };
+    using No = std::integral_constant<Sums, kNone>;
+    using W = std::integral_constant<Sums, kWeight>;
+    using WB = std::integral_constant<Sums, kBoth>;
     if (centre)
-      params ? sized(std::true_type{}, std::true_type{}) : sized(std::true_type{}, std::false_type{});
+      params ? sized(std::true_type{}, WB{}) : sized(std::true_type{}, No{});
+    else if (dbias)
+      sized(std::false_type{}, WB{});
     else
-      params ? sized(std::false_type{}, std::true_type{}) : sized(std::false_type{}, std::false_type{});
+      dweight ? sized(std::false_type{}, W{}) : sized(std::false_type{}, No{});
   } else {
     float2* stats = reinterpret_cast<float2*>(part + 2 * (size_t)H * kMaxSlabs);
     launch_pdl(norm_dx_kernel<4>, dim3((unsigned)T), dim3(32 * ((chunks + 3) / 4)), 0, s, v, dout, dresidual, weight, eps,
