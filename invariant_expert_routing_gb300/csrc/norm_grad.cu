@@ -207,7 +207,7 @@ enum Sums { kNone, kWeight, kBoth };
 // dout n and dout.  dx may be dresidual (no __restrict__): a row is copied
 // before it is written, by the same thread.
 template <bool kCentre, Sums kSums, int kThreads, int kRing>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 512 / kThreads)
     norm_backward_kernel(const uint16_t* v_in, const uint16_t* dout, const uint16_t* dresidual,
                          const uint16_t* __restrict__ weight, float eps, int T, int H, uint16_t* dx,
                          float* __restrict__ part) {
@@ -335,8 +335,8 @@ __global__ void __launch_bounds__(kThreads)
 // element instead of 8)
 // dv of one row a CTA, and the row's (mean, 1 / root) for the weight's gradient.
 // dx may be dresidual (no __restrict__): a row is read before the first barrier.
-template <int NV>
-__global__ void __launch_bounds__(1024)
+template <int NV, int kThreads>
+__global__ void __launch_bounds__(kThreads)
     norm_dx_kernel(const uint16_t* v_in, const uint16_t* dout, const uint16_t* dresidual,
                    const uint16_t* __restrict__ weight, float eps, int H, int centre, uint16_t* dx, float2* stats) {
   __shared__ float s_sum[4][kMaxChunks];
@@ -466,6 +466,8 @@ void launch_add_layer_norm(const uint16_t* x, const uint16_t* residual, const ui
     go(add_layer_norm_kernel<1, 1024, 1>, 1);
   else if (chunks <= 32)
     go(add_layer_norm_kernel<4, 256, 4>, 4);
+  else if (chunks <= 64)
+    go(add_layer_norm_kernel<4, 512, 2>, 4);
   else
     go(add_layer_norm_kernel<4, 1024, 1>, 4);
 }
@@ -530,7 +532,7 @@ void launch_norm_backward(const uint16_t* v, const uint16_t* dout, const uint16_
       dweight ? sized(std::false_type{}, W{}) : sized(std::false_type{}, No{});
   } else {
     float2* stats = reinterpret_cast<float2*>(part + 2 * (size_t)H * kMaxSlabs);
-    launch_pdl(norm_dx_kernel<4>, dim3((unsigned)T), dim3(32 * ((chunks + 3) / 4)), 0, s, v, dout, dresidual, weight, eps,
+    launch_pdl(chunks <= 64 ? norm_dx_kernel<4, 512> : norm_dx_kernel<4, 1024>, dim3((unsigned)T), dim3(32 * ((chunks + 3) / 4)), 0, s, v, dout, dresidual, weight, eps,
                H, (int)centre, dx, stats);
     const int slab_rows = (T + kMaxSlabs - 1) / kMaxSlabs;
     slabs = (T + slab_rows - 1) / slab_rows;
