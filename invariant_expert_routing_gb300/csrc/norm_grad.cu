@@ -350,9 +350,9 @@ __global__ void __launch_bounds__(kThreads)
   for (int i = 0; i < NV; ++i) {
     const int c = (warp + i * warps) * kChunk + lane * 8;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    vv[i] = c < H ? *reinterpret_cast<const uint4*>(v_in + row + c) : zero;
-    gv[i] = c < H ? *reinterpret_cast<const uint4*>(dout + row + c) : zero;
-    rv[i] = c < H && dresidual ? *reinterpret_cast<const uint4*>(dresidual + row + c) : zero;
+    vv[i] = c < H ? __ldcs(reinterpret_cast<const uint4*>(v_in + row + c)) : zero;
+    gv[i] = c < H ? __ldcs(reinterpret_cast<const uint4*>(dout + row + c)) : zero;
+    rv[i] = c < H && dresidual ? __ldcs(reinterpret_cast<const uint4*>(dresidual + row + c)) : zero;
     wv[i] = c < H ? __ldg(reinterpret_cast<const uint4*>(weight + c)) : zero;
   }
   float v[NV][8], g[NV][8], q[NV], p[NV];
@@ -400,29 +400,48 @@ __global__ void __launch_bounds__(kThreads)
   if (threadIdx.x == 0) stats[blockIdx.x] = make_float2(mean, inv);
 }
 
-// part[slab][0 / 1][H]: sums over the rows of a slab of dout n and dout.
+// part[slab][0 / 1][H]: sums over the rows of a slab of dout n and dout; eight
+// columns a thread, four rows' loads in flight.
 __global__ void __launch_bounds__(128)
     norm_columns_kernel(const uint16_t* __restrict__ v_in, const uint16_t* __restrict__ dout,
                         const float2* __restrict__ stats, int T, int H, int slab_rows, float* __restrict__ part) {
-  const int c = (blockIdx.x * 128 + threadIdx.x) * 2;
+  const int c = (blockIdx.x * 128 + threadIdx.x) * 8;
   pdl_wait();
   pdl_trigger();
   if (c >= H) return;
   const int t0 = blockIdx.y * slab_rows, t1 = min(T, t0 + slab_rows);
-  float dw0 = 0.0f, dw1 = 0.0f, db0 = 0.0f, db1 = 0.0f;
-  for (int t = t0; t < t1; ++t) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(v_in + (size_t)t * H + c);
-    const uint32_t d = *reinterpret_cast<const uint32_t*>(dout + (size_t)t * H + c);
-    const float2 s = stats[t];
-    const float d0 = __uint_as_float(d << 16), d1 = __uint_as_float(d & 0xFFFF0000u);
-    dw0 = fmaf(d0, (__uint_as_float(v << 16) - s.x) * s.y, dw0);
-    dw1 = fmaf(d1, (__uint_as_float(v & 0xFFFF0000u) - s.x) * s.y, dw1);
-    db0 += d0;
-    db1 += d1;
+  F2 dw[4] = {}, db[4] = {};
+  for (int t = t0; t < t1; t += 4) {
+    uint4 vv[4], dd[4];
+    float2 st[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool have = t + k < t1;
+      const size_t at = (size_t)(have ? t + k : t) * H + c;
+      vv[k] = __ldcs(reinterpret_cast<const uint4*>(v_in + at));
+      dd[k] = have ? __ldcs(reinterpret_cast<const uint4*>(dout + at)) : make_uint4(0, 0, 0, 0);
+      st[k] = stats[have ? t + k : t];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (t + k >= t1) break;
+      F2 v[4], d[4];
+      unpack(vv[k], v);
+      unpack(dd[k], d);
+      const F2 minus = both(-st[k].x), inv = both(st[k].y);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        dw[j] = fma(d[j], mul(add(v[j], minus), inv), dw[j]);
+        db[j] = add(db[j], d[j]);
+      }
+    }
   }
   float* at = part + (size_t)blockIdx.y * 2 * H + c;
-  *reinterpret_cast<float2*>(at) = make_float2(dw0, dw1);
-  *reinterpret_cast<float2*>(at + H) = make_float2(db0, db1);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    *reinterpret_cast<F2*>(at + 2 * j) = dw[j];
+    *reinterpret_cast<F2*>(at + H + 2 * j) = db[j];
+  }
 }
 
 // 32 columns a CTA: 32 slabs in turn a warp lane column, then those by a tree.
@@ -537,7 +556,7 @@ void launch_norm_backward(const uint16_t* v, const uint16_t* dout, const uint16_
     const int slab_rows = (T + kMaxSlabs - 1) / kMaxSlabs;
     slabs = (T + slab_rows - 1) / slab_rows;
     if (params)
-      launch_pdl(norm_columns_kernel, dim3((H + 255) / 256, slabs), dim3(128), 0, s, v, dout, (const float2*)stats, T, H,
+      launch_pdl(norm_columns_kernel, dim3((H + 1023) / 1024, slabs), dim3(128), 0, s, v, dout, (const float2*)stats, T, H,
                  slab_rows, part);
   }
   if (params)
