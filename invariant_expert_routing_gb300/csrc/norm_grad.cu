@@ -457,8 +457,10 @@ __global__ void __launch_bounds__(1024)
   pdl_trigger();
   if (!out) return;
   float t = 0.0f;
-  if (c < H)
+  if (c < H) {
+#pragma unroll 8
     for (int i = y; i < slabs; i += 32) t += from[(size_t)i * 2 * H + c];
+  }
   s[y][lane] = t;
   __syncthreads();
   t = s[lane][y];   // lane: the slab group, y: the column
