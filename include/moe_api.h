@@ -608,7 +608,8 @@ moe_status moe_forward_mx(const moe_config* cfg, const moe_scoring* scoring, int
 
 /* Bytes of workspace of moe_grouped_gemm and moe_grouped_wgrad for up to
  * max_tokens tokens (0 if the configuration is invalid): the device status
- * word at its start, nothing kept from call to call. */
+ * word at its start, nothing kept from call to call (calls in flight at once
+ * may share it). */
 size_t moe_workspace_bytes_grouped(const moe_config* cfg, int32_t max_tokens);
 
 /* y_perm[p] = bf16(x[row(p)] . W_e), fp32 accumulation, for every row p of
@@ -674,7 +675,8 @@ moe_status moe_swiglu_backward(const moe_config* cfg, int32_t T, const uint16_t*
 moe_status moe_add_layer_norm(int32_t T, int32_t H, const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
                               const uint16_t* bias, float eps, uint16_t* residual_out, uint16_t* out, void* stream);
 
-/* Bytes of workspace of moe_norm_backward (0 if T or H is invalid). */
+/* Bytes of workspace of moe_norm_backward for up to max_tokens rows (0 if
+ * max_tokens or H is invalid).  Calls in flight at once need one each. */
 size_t moe_workspace_bytes_norm_backward(int32_t max_tokens, int32_t H);
 
 /* The gradient of moe_add_layer_norm (centre = 1) or moe_add_norm (centre =

@@ -170,6 +170,7 @@ def _ptr(t):
 
 
 _current_stream = None   # () -> handle of the current device's current stream; set at the first call
+_current_device = None   # () -> its number
 
 
 def _stream(stream):
@@ -179,11 +180,18 @@ def _stream(stream):
     if _current_stream is None:
         import torch
         # the raw handle where torch offers it: building a Stream object costs about as much as a launch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        torch.cuda.current_device()   # (initialises CUDA; the raw form does not)
-        device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), _device
         _current_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
     return _current_stream()
+
+
+def _device():
+    global _current_device
+    if _current_device is None:
+        import torch
+        torch.cuda.current_device()   # (initialises CUDA; the raw form does not)
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _current_device()
 
 
 def _check(fn, st):
@@ -589,6 +597,12 @@ def workspace_grouped(cfg, max_tokens: int, device="cuda"):
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
+def _here(name, t):
+    """The kernels run on the current device: a tensor of another one is refused."""
+    if t.get_device() != _device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{_device()}")
+
+
 def _slots(c):
     return c.num_experts if c.routing == MOE_ROUTING_EXPERT_CHOICE else c.top_k
 
@@ -627,6 +641,7 @@ def moe_grouped_gemm(cfg, T, x, w, sorted_route_ids, expert_counts, y_perm, ws, 
     py, F = _want_rows("y_perm", y_perm, rows)
     pw = _want("w", w, "bfloat16", (c.num_experts, F, K) if transposed else (c.num_experts, K, F))
     ids, counts, pws = _want_groups(c, rows, sorted_route_ids, expert_counts, ws, gather)
+    _here("x", x)
     flags = (MOE_GROUPED_GATHER if gather else 0) | (MOE_GROUPED_TRANSPOSED if transposed else 0)
     _check("moe_grouped_gemm", _lib.moe_grouped_gemm(ctypes.byref(c), T, K, F, flags, px, pw, ids, counts, py, pws,
                                                      ws.numel(), _stream(stream)))
@@ -645,6 +660,7 @@ def moe_grouped_wgrad(cfg, T, x, dy, sorted_route_ids, expert_counts, dw, ws, dw
     pdw = _want("dw", dw, "bfloat16" if bf16 else "float32", shape)
     padd = _want("dw_add", dw_add, "float32", shape, optional=True)
     ids, counts, pws = _want_groups(c, rows, sorted_route_ids, expert_counts, ws, gather_x or gather_dy)
+    _here("x", x)
     flags = ((MOE_WGRAD_GATHER_X if gather_x else 0) | (MOE_WGRAD_GATHER_DY if gather_dy else 0)
              | (MOE_WGRAD_BF16 if bf16 else 0))
     _check("moe_grouped_wgrad", _lib.moe_grouped_wgrad(ctypes.byref(c), T, K, F, flags, px, pdy, ids, counts, padd,
@@ -663,6 +679,7 @@ def moe_swiglu(cfg, T, gu, topk_gate, sorted_route_ids, num_padded, a, stream=No
     """a [rows, I] = gate * silu(g) * u from gu [rows, 2I]; topk_gate [T, S] or None."""
     c = _cfg(cfg)
     rows, pgu, gate, ids, npad = _want_swiglu(c, T, gu, topk_gate, sorted_route_ids, num_padded)
+    _here("gu", gu)
     _check("moe_swiglu", _lib.moe_swiglu(ctypes.byref(c), T, pgu, gate, ids, npad,
                                          _want("a", a, "bfloat16", (rows, c.intermediate)), _stream(stream)))
 
@@ -671,6 +688,7 @@ def moe_swiglu_backward(cfg, T, gu, topk_gate, da, sorted_route_ids, num_padded,
     """dgu [rows, 2I], dgate [T, S] fp32 and the activation a from da [rows, I]; dgate and a may be None."""
     c = _cfg(cfg)
     rows, pgu, gate, ids, npad = _want_swiglu(c, T, gu, topk_gate, sorted_route_ids, num_padded)
+    _here("gu", gu)
     one = (rows, c.intermediate)
     _check("moe_swiglu_backward", _lib.moe_swiglu_backward(
         ctypes.byref(c), T, pgu, gate, _want("da", da, "bfloat16", one), ids, npad,
@@ -682,8 +700,10 @@ def moe_add_layer_norm(x, residual, weight, bias, eps, residual_out, out, stream
     """x [T, H] bf16 (+ residual) -> residual_out and the layer norm out, [T, H] bf16; residual, bias
     and residual_out may be None."""
     shape = T, H = x.shape
+    px = _want("x", x, "bfloat16", shape)
+    _here("x", x)
     _check("moe_add_layer_norm", _lib.moe_add_layer_norm(
-        T, H, _want("x", x, "bfloat16", shape), _want("residual", residual, "bfloat16", shape, True),
+        T, H, px, _want("residual", residual, "bfloat16", shape, True),
         _want("weight", weight, "bfloat16", (H,)), _want("bias", bias, "bfloat16", (H,), True), eps,
         _want("residual_out", residual_out, "bfloat16", shape, True), _want("out", out, "bfloat16", shape),
         _stream(stream)))
@@ -706,8 +726,10 @@ def moe_norm_backward(v, dout, dresidual, weight, eps, dx, dweight, dbias, ws, c
     """Gradients of the layer norm (centre) or the RMS norm of v [T, H]: dx [T, H] bf16, dweight and
     dbias [H] fp32; dresidual, dweight and dbias may be None."""
     shape = T, H = v.shape
+    pv = _want("v", v, "bfloat16", shape)
+    _here("v", v)
     _check("moe_norm_backward", _lib.moe_norm_backward(
-        T, H, int(centre), _want("v", v, "bfloat16", shape), _want("dout", dout, "bfloat16", shape),
+        T, H, int(centre), pv, _want("dout", dout, "bfloat16", shape),
         _want("dresidual", dresidual, "bfloat16", shape, True), _want("weight", weight, "bfloat16", (H,)), eps,
         _want("dx", dx, "bfloat16", shape), _want("dweight", dweight, "float32", (H,), True),
         _want("dbias", dbias, "float32", (H,), True), _want_at_least("ws", ws, "uint8", 1), ws.numel(),

@@ -412,3 +412,68 @@ def test_one_and_two_groups_of_features_give_the_same_bits(moe, transposed, F):
     assert torch.equal(y, yp)
     want, mag = R.gemm(G, x, w, True, transposed)
     R.check(y[G.real], want[G.real], R.BF * want[G.real].abs() + R.sum_tol(K) * mag[G.real])
+
+
+def _at_16(t):
+    """The same tensor at an address that is a multiple of 16, not of 32."""
+    torch = torch_()
+    step = 16 // t.element_size()
+    flat = torch.empty(t.numel() + 2 * step, dtype=t.dtype, device="cuda")
+    at = next(i for i in (step, 2 * step) if (flat.data_ptr() + i * t.element_size()) % 32 == 16)
+    out = flat[at:at + t.numel()].view(t.shape)
+    assert out.data_ptr() % 32 == 16
+    return out.copy_(t)
+
+
+def test_addresses_aligned_to_16_bytes_only(moe):
+    torch = torch_()
+    from tests import train_ref as R
+    G, K, F, g = R.Groups(300, 5, 2, 8, seed=1, idle=(2,)), 200, 272, _gen(8)
+    x, dy, w = _randn(g, G.T, K), G.grouped(F, g), _randn(g, 5, K, F)
+    cfg, add = moe.make_config(128, 5, 2, 128, 8), torch.randn(5, K, F, generator=g, device="cuda")
+    ws = moe.workspace_grouped(cfg, G.T)
+    y = _gemm(moe, G, x, w, True, False)
+    got = _at_16(torch.full_like(y, 7.0))
+    moe.moe_grouped_gemm(cfg, G.T, _at_16(x), _at_16(w), _at_16(G.ids), _at_16(G.dcounts), got, ws, gather=True)
+    assert torch.equal(got, y)
+    for dtype, a in ((torch.float32, None), (torch.float32, add), (torch.bfloat16, None)):
+        dw = torch.empty(5, K, F, dtype=dtype, device="cuda")
+        moe.moe_grouped_wgrad(cfg, G.T, x, dy, G.ids, G.dcounts, dw, ws, dw_add=a, gather_x=True)
+        got = _at_16(torch.full_like(dw, 7.0))
+        moe.moe_grouped_wgrad(cfg, G.T, _at_16(x), _at_16(dy), _at_16(G.ids), G.dcounts, got, ws,
+                              dw_add=None if a is None else _at_16(a), gather_x=True)
+        assert torch.equal(got, dw)
+    v, d, nw = _randn(g, 300, 272), _randn(g, 300, 272), _randn(g, 272)
+    ref, out = torch.empty_like(v), _at_16(v)
+    moe.moe_add_layer_norm(v, d, nw, None, 1e-5, None, ref)
+    moe.moe_add_layer_norm(_at_16(v), _at_16(d), _at_16(nw), None, 1e-5, None, out)
+    assert torch.equal(out, ref)
+    nws = moe.workspace_norm_backward(300, 272)
+    sums = torch.empty(2, 272, device="cuda")
+    moe.moe_norm_backward(v, d, None, nw, 1e-5, ref, sums[0], sums[1], nws)
+    odd = _at_16(torch.zeros_like(sums))
+    moe.moe_norm_backward(_at_16(v), _at_16(d), None, _at_16(nw), 1e-5, out, odd[0], odd[1], nws)
+    assert torch.equal(out, ref) and torch.equal(odd, sums)
+
+
+def test_two_streams_share_a_grouped_workspace(moe):
+    torch = torch_()
+    from tests import train_ref as R
+    G, K, F, g = R.Groups(2000, 6, 2, 16, seed=3), 512, 1024, _gen(4)
+    x, dy, w = _randn(g, G.T, K), G.grouped(F, g), _randn(g, 6, K, F, scale=0.1)
+    cfg = moe.make_config(128, 6, 2, 128, 16)
+    ws = moe.workspace_grouped(cfg, G.T)
+    want_y, want = _gemm(moe, G, x, w, True, False), torch.empty(6, K, F, device="cuda")
+    moe.moe_grouped_wgrad(cfg, G.T, x, dy, G.ids, G.dcounts, want, ws, gather_x=True)
+    y, dw = torch.full_like(want_y, 7.0), torch.empty_like(want)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        y.fill_(7.0), dw.zero_()
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        moe.moe_grouped_gemm(cfg, G.T, x, w, G.ids, G.dcounts, y, ws, gather=True, stream=streams[0])
+        moe.moe_grouped_wgrad(cfg, G.T, x, dy, G.ids, G.dcounts, dw, ws, gather_x=True, stream=streams[1])
+        torch.cuda.synchronize()
+        assert torch.equal(y, want_y) and torch.equal(dw, want)
+    assert moe.moe_get_device_status(ws) == 0

@@ -121,3 +121,23 @@ def test_binding_checks_tensors(moe):
         moe.moe_add_layer_norm(x, None, x, None, 1e-5, None, x)
     with pytest.raises(ValueError, match="v"):
         moe.moe_norm_backward(x, x, None, x, 1e-5, x, None, None, None)
+
+
+def test_binding_refuses_another_device(moe, monkeypatch):
+    class Elsewhere:
+        device = "cuda:1"
+
+        def get_device(self):
+            return 1
+    monkeypatch.setattr(moe, "_current_device", lambda: 0)
+    with pytest.raises(ValueError, match="x: on cuda:1, but the current device is cuda:0"):
+        moe._here("x", Elsewhere())
+    monkeypatch.setattr(moe, "_current_device", lambda: 1)
+    moe._here("x", Elsewhere())
+
+
+def test_rows_of_the_binding_and_the_library(moe):
+    for kw in (dict(), dict(capacity_factor=1.5), dict(routing=1), dict(routing=1, capacity_factor=0.3)):
+        for T in (0, 1, 7, 1000):
+            c = moe.make_config(**CFG, **kw)
+            assert moe._rows(c, T) == moe.moe_max_padded_rows(c, T)
