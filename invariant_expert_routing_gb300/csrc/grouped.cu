@@ -614,6 +614,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
       __syncwarp();
       if (lane == 0) mx::mbar_arrive_remote_relaxed(mapa_shared(tempty0 + 8 * b, 0));
     };
+    // Gradient: this warp's blocks of 32 columns of a tile that lie in dw (the
+    // first ones; none if its rows do not).
+    auto blocks_of = [&](const Item& of) {
+      const int m = of.a * kTile + (int)rank * 128 + quarter * 32, n = F - of.b * kTile - col0;
+      return m >= args.g.K || n <= 0 ? 0 : min(4, (n + 31) / 32);
+    };
     // kWgradAdd: what the sums are added to comes two blocks (of 32 columns) ahead,
     // the first two of an item during the one before.  Whole lines are requested, 8
     // lanes a row; the chunks of a row's 128 bytes are swapped in pairs by bit 2 of
@@ -622,12 +628,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
     auto request_add = [&](const Item& of, int block) {
       const int n = of.b * kTile + col0 + block * 32 + (lane & 7) * 4;
       const int m = of.a * kTile + (int)rank * 128 + quarter * 32;
+      if (block < blocks_of(of)) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 3);
-        const bool in = m + r < args.g.K && n < F;
-        const float* src = in ? args.add + ((size_t)of.e * args.g.K + m + r) * F + n : args.add;
-        cp_async16(add0 + (block & 1) * kAddBlock + r * 128 + (((lane & 7) ^ (i & 1)) << 4), src, in ? 16 : 0);
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3);
+          const bool in = m + r < args.g.K && n < F;
+          const float* src = in ? args.add + ((size_t)of.e * args.g.K + m + r) * F + n : args.add;
+          cp_async16(add0 + (block & 1) * kAddBlock + r * 128 + (((lane & 7) ^ (i & 1)) << 4), src, in ? 16 : 0);
+        }
       }
       cp_async_commit();
     };
@@ -700,8 +708,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
       } else {
         Item ahead = it;
         if (kMode == kWgradAdd && item + pairs < total) ahead = item_of<kMode>(args, seg, item + pairs);
-        // (every block where they are counted, the same for the whole warp)
-        for (int c = 0; c < kTile / 2 && (kMode == kWgradAdd || n0 + c < F); c += 4 * per) {
+        const int columns = blocks_of(it) * 32;   // the same for the whole warp
+        // (kWgradAdd counts every block, for the requests)
+        for (int c = 0; c < (kMode == kWgradAdd ? kTile / 2 : columns); c += 4 * per) {
+          if (kMode == kWgradAdd && c >= columns) {
+            cp_async_wait<1>();
+            if (item + pairs < total && c >= 64) request_add(ahead, (c >> 5) - 2);
+            else cp_async_commit();
+            continue;
+          }
           float v[32] = {};
           if (!empty) mx::tmem_load32(tbase + col0 + c, v);
           if (!args.fp32) {

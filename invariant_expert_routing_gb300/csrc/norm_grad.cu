@@ -57,11 +57,14 @@ __device__ __forceinline__ float row_sum(float (&q)[NV], int warp, int warps, in
 template <int NV, int kThreads, int kBlocks>
 __global__ void __launch_bounds__(kThreads, kBlocks)
     add_layer_norm_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* __restrict__ weight,
-                          const uint16_t* __restrict__ bias, float eps, int H, uint16_t* residual_out, uint16_t* out) {
-  __shared__ float s_sum[2][kMaxChunks];
+                          const uint16_t* __restrict__ bias, float eps, int T, int H, uint16_t* residual_out, uint16_t* out) {
+  // (rows shorter than 2048 share a CTA of 256 threads, blockDim.y of them)
+  __shared__ float s_sums[kThreads == 256 ? 8 : 1][2][kThreads == 256 ? 32 : kMaxChunks];
+  auto s_sum = s_sums[threadIdx.y];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const int chunks = (H + kChunk - 1) / kChunk;
-  const size_t row = (size_t)blockIdx.x * H;
+  const int chunks = (H + kChunk - 1) / kChunk, t = blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= T) H = 0;   // nothing to read or write, but the barriers
+  const size_t row = (size_t)t * H;
   pdl_wait();
   pdl_trigger();
   const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -476,29 +479,31 @@ constexpr int kMaxSlabs = 128;
 void launch_add_layer_norm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, const uint16_t* bias,
                            float eps, int T, int H, uint16_t* residual_out, uint16_t* out, int sms, cudaStream_t s) {
   const int chunks = (H + kChunk - 1) / kChunk;
-  const dim3 grid((unsigned)T);
-  auto go = [&](auto kernel, int nv) {
-    launch_pdl(kernel, grid, dim3(32 * ((chunks + nv - 1) / nv)), 0, s, x, residual, weight, bias, eps, H, residual_out,
-               out);
+  auto go = [&](auto kernel, int nv, int rows) {
+    launch_pdl(kernel, dim3((unsigned)((T + rows - 1) / rows)), dim3(32 * ((chunks + nv - 1) / nv), rows), 0, s, x,
+               residual, weight, bias, eps, T, H, residual_out, out);
   };
   // few rows: one chunk a warp, for the shortest path; many: four, so that an
   // SM holds several rows and their loads overlap
   if (T < 4 * sms && chunks <= 32)
-    go(add_layer_norm_kernel<1, 1024, 1>, 1);
+    go(add_layer_norm_kernel<1, 1024, 1>, 1, 1);
   else if (chunks <= 32)
-    go(add_layer_norm_kernel<4, 256, 4>, 4);
+    go(add_layer_norm_kernel<4, 256, 4>, 4, 8 / ((chunks + 3) / 4));
   else if (chunks <= 64)
-    go(add_layer_norm_kernel<4, 512, 2>, 4);
+    go(add_layer_norm_kernel<4, 512, 2>, 4, 1);
   else
-    go(add_layer_norm_kernel<4, 1024, 1>, 4);
+    go(add_layer_norm_kernel<4, 1024, 1>, 4, 1);
 }
 
 // The fused kernel's threads for rows of H, and CTAs: as many as fill 152 SMs
 // once (a constant, so that the columns' sums have one order for a size).
 int fused_threads(int H) { return 32 * ((H + 2 * kChunk - 1) / (2 * kChunk)); }
+// Short rows take at least eight a CTA where there are many, so that the sums of
+// the CTAs stay few.
 int fused_ctas(int H, int T) {
-  const int most = 152 * (512 / fused_threads(H));
-  return T < most ? T : most;
+  const int most = 152 * (512 / fused_threads(H)), eighth = T / 8 > 152 ? T / 8 : 152;
+  const int ctas = most < eighth ? most : eighth;
+  return T < ctas ? T : ctas;
 }
 
 size_t norm_backward_scratch_bytes(int T, int H) {
