@@ -12,7 +12,10 @@
 //             (wide_items), B = up to 256 rows of x (K-major).  The MMA's N is
 //             the tile's rows rounded up to 32: columns of an MMA are
 //             independent sums over the same K steps, so a row's bits depend
-//             neither on N nor on the batch.
+//             neither on N nor on the batch.  An expert's tiles are of one
+//             height, to 32 rows: full ones and a short last one took 297 us
+//             for 281 (W13 of 8192 tokens in the 128-expert layer), 608 for 570
+//             (W2's input gradient in the 8-expert layer).
 //   gradient: A = 256 columns of x, B = 256 columns of dy, both MN-major, K
 //             the expert's rows in ascending order.
 // Rows gathered by route come by TMA gather4, four rows a request, straight from
@@ -33,7 +36,7 @@
 // Bounds, of the measured 1916 TFLOP/s: rows in place the tensor pipe (8192 rows
 // of 4096 a expert: 1855 the product, 1900 the gradient in bf16), gathered rows
 // the requests (a gather4 takes some 16 cycles, 32 of them a stage): W2's input
-// gradient of 4096 tokens in the 8-expert layer 608 us for 580 in place.
+// gradient of 4096 tokens in the 8-expert layer 577 us for 559 in place.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 #include <cmath>
@@ -95,8 +98,9 @@ struct Cfg {
 
 struct Maps {
   CUtensorMap a;        // product: W_e [experts][K][F] or [experts][F][K]; gradient: x
-  CUtensorMap b;        // rows of x / dy, full boxes
-  CUtensorMap a_small, b_small;   // kRowBox rows a box (a: gradient)
+  CUtensorMap b;        // gradient: dy, full boxes
+  CUtensorMap b_box[4];   // product: x, 16, 32, 64 and 128 rows a box
+  CUtensorMap a_small, b_small;   // gradient: kRowBox rows a box
   CUtensorMap a_rows, b_rows;     // one row a box: gather4 (a: gradient)
 };
 
@@ -193,8 +197,9 @@ __device__ __forceinline__ Item item_of(const Args& a, const Segments& s, int it
     it.e = lo;
     it.a = 0;
     it.b = grp * G + lin - tile * gsz;
-    it.row0 = s.start[lo] + tile * kTile;
-    it.rows = min(kTile, s.count[lo] - tile * kTile);
+    const int rows = ((s.count[lo] + count - 1) / count + 31) & ~31;   // (at most 256; the last tile has some)
+    it.row0 = s.start[lo] + tile * rows;
+    it.rows = min(rows, s.count[lo] - tile * rows);
   }
   it.e = mx::uniform(it.e);
   it.row0 = mx::uniform(it.row0);
@@ -378,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
   if (warp == 0) {
     if (lane == 0) {
       prefetch_tmap(args.gather_a ? &maps.a_rows : &maps.a);
-      prefetch_tmap(args.gather_b ? &maps.b_rows : &maps.b);
+      prefetch_tmap(args.gather_b ? &maps.b_rows : wgrad(kMode) ? &maps.b : &maps.b_box[3]);
     }
     __syncwarp();
     // The set-up reads nothing an earlier kernel writes: it overlaps the end
@@ -424,6 +429,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
       // product: this CTA's rows of the tile; gradient: this CTA's columns
       const int half = half_rows(it.rows);
       const int brow0 = it.row0 + me * half;
+      // product in place: the largest box that fits, twice (the second one's last
+      // row is the last) if it does not fill the rows (boxes of 16 rows instead: 357
+      // us for 290, W13 of 8192 tokens in the 128-expert layer)
+      const int box = 31 - __clz(max(half, 16)), box_rows = 1 << box, boxes = half == box_rows ? 1 : 2;
       const int acol = it.a * kTile + me * 128, bcol = it.b * kGroups * kTile + me * 128;
       const int first = (part + parts - n0 % parts) % parts;   // this warp's first stage of the item
       int4 next = {};   // gradient: rows of the next stage, x in lanes 0..15, dy in lanes 16..31
@@ -455,7 +464,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
         const int k0 = ks * kBK;
         if (!wgrad(kMode)) {
           if (mx::elect_one()) {
-            const uint32_t tx = kABytes + (uint32_t)half * kBK * 2;
+            const uint32_t tx = kABytes + (uint32_t)(args.gather_b ? half : boxes * box_rows) * kBK * 2;
             s_tx[stage] = tx;
             if (lead) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * tx);
 #pragma unroll
@@ -477,11 +486,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kMode>::kMaxThre
                 const int4 r = rows[i];
                 tma_gather4_pair(sB + i * 512, &maps.b_rows, k0, r.x, r.y, r.z, r.w, fb, pol_x);
               }
-            } else if (half == 128) {
-              tma_load_2d_pair(sB, &maps.b, k0, brow0, fb, pol_x);
             } else {
-              for (int r = 0; r < half; r += kRowBox)
-                tma_load_2d_pair(sB + r * 128, &maps.b_small, k0, brow0 + r, fb, pol_x);
+              const CUtensorMap* m = &maps.b_box[box - 4];
+              tma_load_2d_pair(sB, m, k0, brow0, fb, pol_x);
+              if (boxes == 2) tma_load_2d_pair(sB + (half - box_rows) * 128, m, k0, brow0 + half - box_rows, fb, pol_x);
             }
           }
         } else {
@@ -895,15 +903,18 @@ long long routes_of(const GroupArgs& g) {
 // row tile once for both, but keep one accumulator, whose stores nothing overlaps,
 // and leave the last wave of items emptier.  The time of a wave of double items
 // over that of two waves of single ones was 0.94 for gathered rows (whose requests
-// bound: W2's input gradient of 4096 tokens in the 8-expert layer 659 -> 608 us),
-// 1.03 for rows in place, 0.9 where experts average at most 128 rows; the waves
-// follow from the tiles to be expected, half of an expert's last one filled.
+// bound: W2's input gradient of 4096 tokens in the 8-expert layer 612 -> 577 us),
+// 0.98 for rows in place (W13's product of 8192 tokens in the 128-expert layer 292
+// -> 281; 0.94 to 1.06, the latter in the 8-expert layer), 0.9 where experts average
+// at most 128 rows (W13 of 64 tokens in the 128-expert layer 122 -> 116); the waves
+// follow from the tiles to be expected: at least one an expert, half of its last one
+// filled.
 bool wide_items(const GroupArgs& g, bool gather, int sms) {
   const double routes = (double)routes_of(g), experts = routes < g.N ? routes : g.N;
-  const double tiles = routes / kTile + 0.5 * experts, units = sms / 2;
+  const double tiles = std::fmax(routes / kTile + 0.5 * experts, experts), units = sms / 2;
   const double one = std::ceil(tiles * ((g.F + kTile - 1) / kTile) / units);
   const double two = std::ceil(tiles * ((g.F + 2 * kTile - 1) / (2 * kTile)) / units);
-  return 2.0 * two * (routes <= 128.0 * g.N ? 0.9 : gather ? 0.94 : 1.03) < one;
+  return 2.0 * two * (routes <= 128.0 * g.N ? 0.9 : gather ? 0.94 : 0.98) < one;
 }
 
 }  // namespace
@@ -917,9 +928,10 @@ bool launch_grouped_gemm(const GroupedGemmArgs& in, PFN_cuTensorMapEncodeTiled_v
   if (!(in.transposed ? map_rows(fn, &m.a, in.w, K, F, N, 128)
         : a.wide_a    ? map_wide(fn, &m.a, in.w, F, K, N)
                       : map_rows(fn, &m.a, in.w, F, K, N, kBK)) ||
-      !(in.gather ? map_rows(fn, &m.b_rows, in.x, K, rows, 0, 1)
-                  : map_rows(fn, &m.b, in.x, K, rows, 0, 128) && map_rows(fn, &m.b_small, in.x, K, rows, 0, kRowBox)))
+      (in.gather && !map_rows(fn, &m.b_rows, in.x, K, rows, 0, 1)))
     return false;
+  for (int i = 0; i < 4 && !in.gather; ++i)
+    if (!map_rows(fn, &m.b_box[i], in.x, K, rows, 0, 16 << i)) return false;
   a.g = g;
   a.gather_b = in.gather;
   set_divisor(a, (uint32_t)g.slots);
