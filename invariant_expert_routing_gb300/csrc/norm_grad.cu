@@ -326,10 +326,11 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 4; j += 2) {
         if (!in[h]) break;
-        *reinterpret_cast<F2*>(part + (size_t)blockIdx.x * 2 * H + c[h] + 2 * j) = dw[h][j];
-        if (kSums == kBoth) *reinterpret_cast<F2*>(part + ((size_t)blockIdx.x * 2 + 1) * H + c[h] + 2 * j) = db[h][j];
+        float* to = part + (size_t)blockIdx.x * 2 * H + c[h] + 2 * j;
+        *reinterpret_cast<ulonglong2*>(to) = make_ulonglong2(dw[h][j].v, dw[h][j + 1].v);
+        if (kSums == kBoth) *reinterpret_cast<ulonglong2*>(to + H) = make_ulonglong2(db[h][j].v, db[h][j + 1].v);
       }
   }
 }
@@ -441,18 +442,21 @@ __global__ void __launch_bounds__(128)
   }
   float* at = part + (size_t)blockIdx.y * 2 * H + c;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    *reinterpret_cast<F2*>(at + 2 * j) = dw[j];
-    *reinterpret_cast<F2*>(at + H + 2 * j) = db[j];
+  for (int j = 0; j < 4; j += 2) {
+    *reinterpret_cast<ulonglong2*>(at + 2 * j) = make_ulonglong2(dw[j].v, dw[j + 1].v);
+    *reinterpret_cast<ulonglong2*>(at + H + 2 * j) = make_ulonglong2(db[j].v, db[j + 1].v);
   }
 }
 
-// 32 columns a CTA: 32 slabs in turn a warp lane column, then those by a tree.
-__global__ void __launch_bounds__(1024)
+// 32 columns a CTA: a warp takes every kWarps-th slab in turn, then those by a tree.
+// 16 warps for the 152 slabs of wide rows (all CTAs at once: 2 us less for rows of
+// 7168), 32 for more (rows of 1024: 25 us for 30).
+template <int kWarps>
+__global__ void __launch_bounds__(32 * kWarps)
     norm_columns_sum_kernel(const float* __restrict__ part, int slabs, int H, float* __restrict__ dweight,
                             float* __restrict__ dbias) {
-  __shared__ float s[32][33];
-  const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
+  __shared__ float s[kWarps][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   const float* from = part + (size_t)blockIdx.y * H;   // blockIdx.y: 0 dweight, 1 dbias
   float* out = blockIdx.y ? dbias : dweight;
@@ -462,14 +466,16 @@ __global__ void __launch_bounds__(1024)
   float t = 0.0f;
   if (c < H) {
 #pragma unroll 8
-    for (int i = y; i < slabs; i += 32) t += from[(size_t)i * 2 * H + c];
+    for (int i = warp; i < slabs; i += kWarps) t += from[(size_t)i * 2 * H + c];
   }
-  s[y][lane] = t;
+  s[warp][lane] = t;
   __syncthreads();
-  t = s[lane][y];   // lane: the slab group, y: the column
+  constexpr int kSpan = 32 / kWarps;                        // columns a warp joins at once
+  const int col = warp * kSpan + lane / kWarps;
+  t = s[lane % kWarps][col];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-  if (lane == 0 && blockIdx.x * 32 + y < H) out[blockIdx.x * 32 + y] = t;
+  for (int off = kWarps / 2; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+  if (lane % kWarps == 0 && blockIdx.x * 32 + col < H) out[blockIdx.x * 32 + col] = t;
 }
 
 constexpr int kMaxSlabs = 128;
@@ -567,8 +573,8 @@ void launch_norm_backward(const uint16_t* v, const uint16_t* dout, const uint16_
                  slab_rows, part);
   }
   if (params)
-    launch_pdl(norm_columns_sum_kernel, dim3((H + 31) / 32, 2), dim3(1024), 0, s, (const float*)part, slabs, H, dweight,
-               dbias);
+    launch_pdl(slabs <= 152 ? norm_columns_sum_kernel<16> : norm_columns_sum_kernel<32>, dim3((H + 31) / 32, 2),
+               dim3(slabs <= 152 ? 512 : 1024), 0, s, (const float*)part, slabs, H, dweight, dbias);
 }
 
 }  // namespace moe

@@ -477,3 +477,52 @@ def test_two_streams_share_a_grouped_workspace(moe):
         torch.cuda.synchronize()
         assert torch.equal(y, want_y) and torch.equal(dw, want)
     assert moe.moe_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+def test_two_groups_gathered_and_one_in_place_give_the_same_bits(moe, transposed):
+    """8192 rows of 8 experts, 56 groups of features: about 2016 tiles, for 76 pairs of CTAs 27 waves of single items or 14
+    of double ones, which the gathered form takes (28 x 0.94 < 27) and the form in place does not (28 x 0.98 > 27)."""
+    torch = torch_()
+    from tests import train_ref as R
+    G, K, F, g = R.Groups(4096, 8, 2, 8, seed=6), 72, 14336, _gen(6)
+    x, w = _randn(g, G.T, K), _randn(g, *((8, F, K) if transposed else (8, K, F)), scale=0.1)
+    xp = torch.full((G.rows, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+    xp[G.real] = x[G.ids[G.real].long() // G.k]
+    y, yp = _gemm(moe, G, x, w, True, transposed), _gemm(moe, G, xp, w, False, transposed)
+    assert torch.equal(y, yp)
+
+
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 31, 32, 33, 47, 63, 64, 65, 96, 97, 127, 128, 129, 160, 161, 191, 192, 193,
+                               224, 225, 255, 256, 257, 288, 289, 300, 352, 385, 480, 511, 512, 513, 545, 769])
+def test_every_height_of_a_tile(moe, n):
+    """An expert's rows in tiles of one height, followed by another expert's: in place (overlapping boxes, NaN in the padding)
+    and gathered the same bits, both by the formula, nothing written past the segments."""
+    torch = torch_()
+    from tests import train_ref as R
+    K, F, N, T = 200, 264, 2, n + 5
+    g = _gen(n)
+    cfg = moe.make_config(128, N, 1, 128, 8)
+    rows = moe.moe_max_padded_rows(cfg, T)
+    start = (n + 7) // 8 * 8
+    real = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    real[:n] = real[start:start + 5] = True
+    ids = torch.full((rows,), T, dtype=torch.int32, device="cuda")
+    ids[real] = torch.randperm(T, generator=g, device="cuda").int()
+    counts = torch.tensor([n, 5], dtype=torch.int32, device="cuda")
+    x, w = _randn(g, T, K), _randn(g, N, K, F, scale=0.1)
+    xp = torch.full((rows, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+    xp[real] = x[ids[real].long()]
+    ws = moe.workspace_grouped(cfg, T)
+    ys = [torch.full((rows, F), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    moe.moe_grouped_gemm(cfg, T, x, w, ids, counts, ys[0], ws, gather=True)
+    moe.moe_grouped_gemm(cfg, T, xp, w, None, counts, ys[1], ws)
+    moe.moe_grouped_gemm(cfg, T, xp, w.transpose(1, 2).contiguous(), None, counts, ys[2], ws, transposed=True)
+    assert moe.moe_get_device_status(ws) == 0
+    a, b = xp[:n].double(), xp[start:start + 5].double()
+    want = torch.cat([a @ w[0].double(), b @ w[1].double()])
+    mag = torch.cat([a.abs() @ w[0].double().abs(), b.abs() @ w[1].double().abs()])
+    assert torch.equal(ys[0], ys[1])
+    for y in ys:
+        assert (y[~real] == 7).all()
+        R.check(y[real], want, R.BF * want.abs() + R.sum_tol(K) * mag)
