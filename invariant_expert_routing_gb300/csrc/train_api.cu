@@ -175,6 +175,9 @@ moe_status moe_swiglu_backward(const moe_config* cfg, int32_t T, const uint16_t*
   if ((dgu != gu && overlap(dgu, 2 * one, gu, 2 * one)) || overlap(dgu, 2 * one, da, one) ||
       (a != da && overlap(a, one, da, one)) || overlap(a, one, gu, 2 * one) || overlap(a, one, dgu, 2 * one))
     return MOE_ERR_INVALID_ARG;
+  const size_t gates = sizeof(float) * (size_t)T * api::slots(cfg);
+  if (overlap(dgate, gates, topk_gate, gates) || overlap(dgate, gates, dgu, 2 * one) || overlap(dgate, gates, a, one))
+    return MOE_ERR_INVALID_ARG;
   moe::launch_swiglu_backward(gu, topk_gate, da, sorted_route_ids, num_padded, rows, T * api::slots(cfg), I, dgu, dgate,
                               a, static_cast<cudaStream_t>(stream));
   return api::last_error();
@@ -229,6 +232,10 @@ moe_status moe_norm_backward(int32_t T, int32_t H, int32_t centre, const uint16_
   const size_t n = 2 * (size_t)T * H;
   if (overlap(dx, n, v, n) || overlap(dx, n, dout, n) || (dx != dresidual && overlap(dx, n, dresidual, n)))
     return MOE_ERR_INVALID_ARG;
+  const size_t sum_bytes = sizeof(float) * (size_t)H;
+  if (overlap(dweight, sum_bytes, dbias, sum_bytes)) return MOE_ERR_INVALID_ARG;
+  for (const float* p : {dweight, dbias})
+    if (overlap(p, sum_bytes, dx, n) || overlap(p, sum_bytes, ws, ws_bytes)) return MOE_ERR_INVALID_ARG;
   moe::launch_norm_backward(v, dout, dresidual, weight, eps, T, H, centre != 0, dx, dweight, dbias, ws, s);
   return api::last_error();
 }

@@ -141,3 +141,15 @@ def test_rows_of_the_binding_and_the_library(moe):
         for T in (0, 1, 7, 1000):
             c = moe.make_config(**CFG, **kw)
             assert moe._rows(c, T) == moe.moe_max_padded_rows(c, T)
+
+
+@pytest.mark.parametrize("dw,db", [(DA, DA), (DA, DA + 128 * 4 - 16), (Y + 16, DG), (DA, Y), (WSP, DG), (None, WSP)])
+def test_norm_backward_refuses_sums_over_one_another(moe, dw, db):
+    n = moe.moe_workspace_bytes_norm_backward(4, 128)
+    assert moe._lib.moe_norm_backward(4, 128, 1, X, W, A, IDS, 1e-5, Y, dw, db, WSP, n, None) == INVALID
+
+
+@pytest.mark.parametrize("dgate", [W, W + 64 * 2 * 4 - 16, DGU + 16, A])
+def test_swiglu_backward_refuses_gates_over_other_tensors(moe, dgate):
+    c = moe.make_config(**CFG)
+    assert moe._lib.moe_swiglu_backward(ctypes.byref(c), 64, X, W, DA, IDS, COUNTS, DGU, dgate, A, None) == INVALID
