@@ -616,11 +616,13 @@ def _rows(c, T):
 
 def _want_rows(name, t, rows):
     """The address and the columns of a [rows, columns] bf16 tensor."""
-    if t is None or t.dim() != 2:
+    shape = () if t is None else t.shape   # (each look at a tensor's attributes takes about a tenth of a microsecond)
+    if len(shape) != 2:
         raise ValueError(f"{name}: a 2-D tensor is needed")
-    shape = t.shape
     columns = shape[1]
-    return _want(name, t, "bfloat16", (rows, columns)), columns
+    if shape[0] != rows or t.dtype is not _dtypes["bfloat16"] or not t.is_cuda or not t.is_contiguous():
+        _want(name, t, "bfloat16", (rows, columns))
+    return t.data_ptr(), columns
 
 
 def _want_groups(c, rows, sorted_route_ids, expert_counts, ws, gathered):
