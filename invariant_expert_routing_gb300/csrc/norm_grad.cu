@@ -335,6 +335,145 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads)
   }
 }
 
+// ---- rows up to 16384 wide: a CTA an SM, four pieces of eight columns a thread
+// whose sums stay in registers, the row in shared memory (read there by the thread
+// that copied it) with one or two behind it, and a barrier for each pair of
+// moments.  8192 rows of 12288: 171 us, of 16384: 194 (4.7 and
+// 5.5 TB/s; dv and slabs of rows, as below: 351 and 411).
+constexpr int kWideMaxChunks = 64, kWideThreads = 512;
+
+template <bool kCentre, Sums kSums>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    norm_backward_wide_kernel(const uint16_t* v_in, const uint16_t* dout, const uint16_t* dresidual,
+                              const uint16_t* __restrict__ weight, float eps, int T, int H, int slots, uint16_t* dx,
+                              float* __restrict__ part) {
+  extern __shared__ __align__(16) uint8_t ring[];   // [slots][3][H] bf16
+  __shared__ float s_sum[2][2][4][kFusedMaxWarps];  // by the parity of the row and the moments
+  constexpr int kPieces = 4, kStep = 8 * kWideThreads, kWarps = kWideThreads / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c0 = (int)threadIdx.x * 8;
+  const int rows = (int)blockIdx.x < T ? (T - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+  const size_t stride = (size_t)gridDim.x * H;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  size_t ahead = (size_t)blockIdx.x * H;   // the row to request next
+  int asked = 0;
+  auto request = [&](int slot) {
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int c = c0 + k * kStep;
+      if (c >= H || asked >= rows) continue;
+      const uint32_t dst = smem_u32(ring) + ((uint32_t)slot * 3 * H + c) * 2;
+      cp_async16(dst, v_in + ahead + c, 16);
+      cp_async16(dst + 2 * H, dout + ahead + c, 16);
+      if (dresidual) cp_async16(dst + 4 * H, dresidual + ahead + c, 16);
+    }
+    cp_async_commit();
+    ahead += stride;
+    ++asked;
+  };
+  auto piece = [&](int slot, int tensor, int k, F2 (&v)[4]) {
+    const int c = c0 + k * kStep;
+    uint4 got = zero;
+    if (c < H) got = *reinterpret_cast<const uint4*>(ring + ((size_t)(slot * 3 + tensor) * H + c) * 2);
+    unpack(got, v);
+  };
+  pdl_wait();
+  pdl_trigger();
+  for (int i = 0; i < slots; ++i) request(i);
+  const float per = 1.0f / (float)H;
+  uint4 wv[kPieces];
+  F2 dw[kPieces][4] = {}, db[kPieces][4] = {};
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k) {
+    wv[k] = zero;
+    if (c0 + k * kStep < H) wv[k] = __ldg(reinterpret_cast<const uint4*>(weight + c0 + k * kStep));
+  }
+  int slot = 0;
+  size_t at = (size_t)blockIdx.x * H;
+  for (int i = 0; i < rows; ++i) {
+    if (slots == 3)
+      cp_async_wait<2>();
+    else
+      cp_async_wait<1>();
+    float mean = 0.0f, mean_g = 0.0f, q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (kCentre) {
+      F2 tv = both(0.0f), tg = both(0.0f);
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        F2 v[4], o[4], w[4];
+        piece(slot, 0, k, v);
+        piece(slot, 1, k, o);
+        unpack(wv[k], w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          tv = add(tv, v[j]);
+          tg = fma(o[j], w[j], tg);
+        }
+      }
+      q[0] = total(tv);
+      q[1] = total(tg);
+      block_sum4(q, warp, lane, kWarps, s_sum[i & 1][0]);
+      mean = q[0] * per;
+      mean_g = q[1] * per;
+    }
+    F2 dd = both(0.0f), dg = both(0.0f);
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      F2 v[4], o[4], w[4];
+      piece(slot, 0, k, v);
+      piece(slot, 1, k, o);
+      unpack(wv[k], w);
+      const F2 minus = both(c0 + k * kStep < H ? -mean : 0.0f);   // (past H everything stays zero)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const F2 d = kCentre ? add(v[j], minus) : v[j];
+        dd = fma(d, d, dd);
+        dg = fma(d, mul(o[j], w[j]), dg);
+      }
+    }
+    q[0] = total(dd);
+    q[1] = total(dg);
+    q[2] = q[3] = 0.0f;
+    block_sum4(q, warp, lane, kWarps, s_sum[i & 1][1]);
+    const float inv = 1.0f / sqrtf(q[0] * per + eps);
+    const float slope = q[1] * per * inv * inv;   // mean(g n) / root
+    const F2 inv2 = both(inv), slope2 = both(-slope), minus_g = both(-mean_g), minus = both(-mean);
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      if (c0 + k * kStep >= H) continue;
+      F2 v[4], o[4], w[4], r[4] = {};
+      piece(slot, 0, k, v);
+      piece(slot, 1, k, o);
+      unpack(wv[k], w);
+      if (dresidual) piece(slot, 2, k, r);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const F2 d = kCentre ? add(v[j], minus) : v[j];
+        if (kSums != kNone) dw[k][j] = fma(o[j], mul(d, inv2), dw[k][j]);
+        if (kSums == kBoth) db[k][j] = add(db[k][j], o[j]);
+        const F2 g = kCentre ? fma(o[j], w[j], minus_g) : mul(o[j], w[j]);
+        r[j] = fma(fma(d, slope2, g), inv2, r[j]);
+      }
+      __stcs(reinterpret_cast<uint4*>(dx + at + c0 + k * kStep), pack(r));
+    }
+    __syncwarp();
+    request(slot);   // into this row's slot, by the threads that have read it
+    slot = slot + 1 == slots ? 0 : slot + 1;
+    at += stride;
+  }
+  cp_async_wait<0>();
+  if (kSums != kNone) {
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        if (c0 + k * kStep >= H) break;
+        float* to = part + (size_t)blockIdx.x * 2 * H + c0 + k * kStep + 2 * j;
+        *reinterpret_cast<ulonglong2*>(to) = make_ulonglong2(dw[k][j].v, dw[k][j + 1].v);
+        if (kSums == kBoth) *reinterpret_cast<ulonglong2*>(to + H) = make_ulonglong2(db[k][j].v, db[k][j + 1].v);
+      }
+  }
+}
+
 // ---- wider rows: dv, then the columns' sums in slabs of rows (12 bytes an
 // element instead of 8)
 // dv of one row a CTA, and the row's (mean, 1 / root) for the weight's gradient.
@@ -507,14 +646,31 @@ int fused_threads(int H) { return 32 * ((H + 2 * kChunk - 1) / (2 * kChunk)); }
 // Short rows take at least eight a CTA where there are many, so that the sums of
 // the CTAs stay few.
 int fused_ctas(int H, int T) {
+  if ((H + kChunk - 1) / kChunk > kFusedMaxChunks) return T < 152 ? T : 152;   // (the wide kernel)
   const int most = 152 * (512 / fused_threads(H)), eighth = T / 8 > 152 ? T / 8 : 152;
   const int ctas = most < eighth ? most : eighth;
   return T < ctas ? T : ctas;
 }
 
 size_t norm_backward_scratch_bytes(int T, int H) {
-  if ((H + kChunk - 1) / kChunk <= kFusedMaxChunks) return sizeof(float) * 2 * (size_t)H * fused_ctas(H, T);
+  if ((H + kChunk - 1) / kChunk <= kWideMaxChunks) return sizeof(float) * 2 * (size_t)H * fused_ctas(H, T);
   return sizeof(float2) * (size_t)T + sizeof(float) * 2 * (size_t)H * kMaxSlabs;
+}
+
+template <bool kCentre, Sums kSums>
+void launch_wide(const uint16_t* v, const uint16_t* dout, const uint16_t* dresidual, const uint16_t* weight, float eps,
+                 int T, int H, uint16_t* dx, float* part, int ctas, cudaStream_t s) {
+  auto kernel = norm_backward_wide_kernel<kCentre, kSums>;
+  constexpr int kMost = 3 * 6 * 12288;   // bytes of three rows, more than two of 16384
+  const int slots = H <= 12288 ? 3 : 2;
+  static bool attr_set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  launch_pdl(kernel, dim3(ctas), dim3(kWideThreads), slots * 6 * H, s, v, dout, dresidual, weight, eps, T, H, slots, dx, part);
 }
 
 template <bool kCentre, Sums kSums, int kThreads, int kRing>
@@ -539,7 +695,7 @@ void launch_norm_backward(const uint16_t* v, const uint16_t* dout, const uint16_
   const bool params = dweight || dbias;
   float* part = static_cast<float*>(scratch);
   int slabs;
-  if (chunks <= kFusedMaxChunks) {
+  if (chunks <= kWideMaxChunks) {
     slabs = fused_ctas(H, T);
     auto go = [&](auto kernel) { kernel(v, dout, dresidual, weight, eps, T, H, dx, part, slabs, s); };
     // rows in shared memory: what 227 KB hold, of the CTAs on an SM together
@@ -550,8 +706,10 @@ void launch_norm_backward(const uint16_t* v, const uint16_t* dout, const uint16_
         go(launch_fused<kCentre, kSums, 256, 4>);
       else if (chunks <= 28)
         go(launch_fused<kCentre, kSums, 448, 5>);
-      else
+      else if (chunks <= kFusedMaxChunks)
         go(launch_fused<kCentre, kSums, 512, 4>);
+      else
+        go(launch_wide<kCentre, kSums>);
     };
     using No = std::integral_constant<Sums, kNone>;
     using W = std::integral_constant<Sums, kWeight>;
@@ -564,8 +722,8 @@ void launch_norm_backward(const uint16_t* v, const uint16_t* dout, const uint16_
       dweight ? sized(std::false_type{}, W{}) : sized(std::false_type{}, No{});
   } else {
     float2* stats = reinterpret_cast<float2*>(part + 2 * (size_t)H * kMaxSlabs);
-    launch_pdl(chunks <= 64 ? norm_dx_kernel<4, 512> : norm_dx_kernel<4, 1024>, dim3((unsigned)T), dim3(32 * ((chunks + 3) / 4)), 0, s, v, dout, dresidual, weight, eps,
-               H, (int)centre, dx, stats);
+    launch_pdl(norm_dx_kernel<4, 1024>, dim3((unsigned)T), dim3(32 * ((chunks + 3) / 4)), 0, s, v, dout, dresidual, weight,
+               eps, H, (int)centre, dx, stats);
     const int slab_rows = (T + kMaxSlabs - 1) / kMaxSlabs;
     slabs = (T + slab_rows - 1) / slab_rows;
     if (params)

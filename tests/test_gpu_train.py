@@ -526,3 +526,9 @@ def test_every_height_of_a_tile(moe, n):
     for y in ys:
         assert (y[~real] == 7).all()
         R.check(y[real], want, R.BF * want.abs() + R.sum_tol(K) * mag)
+
+
+@pytest.mark.parametrize("T,H", [(1, 8200), (400, 12288), (310, 12296), (333, 16384), (153, 10240), (1000, 8968)])
+@pytest.mark.parametrize("centre", [True, False])
+def test_norm_backward_of_wide_rows(moe, T, H, centre):
+    test_norm_backward(moe, T, H, centre, 30.0)
