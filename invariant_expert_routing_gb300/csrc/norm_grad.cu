@@ -8,8 +8,9 @@
 // from v: the row is read anyway.  Variances come from the deviations, so a
 // mean far from zero costs no digits.
 //
-// Sums over a row have one order for every batch: eight elements in turn, the
-// 32 groups of a 256-element chunk by a fixed tree, the chunks by another.
+// Sums over a row have one order for a given H, whatever the batch.  The forward's:
+// eight elements in turn, the 32 groups of a 256-element chunk by a fixed tree, the
+// chunks by another.
 #include <cuda_bf16.h>
 #include <cstdint>
 #include <type_traits>
