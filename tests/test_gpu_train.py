@@ -401,7 +401,7 @@ def test_long_segments_keep_fp32_sums(moe, n, add):
 @pytest.mark.parametrize("F", [2048, 2056, 1800])
 @pytest.mark.parametrize("transposed", [False, True])
 def test_one_and_two_groups_of_features_give_the_same_bits(moe, transposed, F):
-    """4000 tokens, 2 of 4 experts, F about 2048: items of two groups for gathered rows, of one for rows in place."""
+    """4000 tokens, 2 of 4 experts, F about 2048: items of two groups where F fills them, of one where it does not."""
     torch = torch_()
     from tests import train_ref as R
     G, K, g = R.Groups(4000, 4, 2, 8, seed=5), 136, _gen(F)
