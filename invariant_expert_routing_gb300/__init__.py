@@ -424,9 +424,10 @@ class _Dtypes(dict):
 _dtypes = _Dtypes()
 
 
-def _want(name, t, dtype, shape, optional=False):
+def _want(name, t, dtype, shape, optional=False, device=None):
     """The address of a contiguous CUDA tensor of this type and shape (the C entry points see
-    pointers only); None for an optional one that is absent."""
+    pointers only); None for an optional one that is absent.  device: the current one, where a
+    tensor of another is refused."""
     if t is None:
         if optional:
             return None
@@ -434,13 +435,17 @@ def _want(name, t, dtype, shape, optional=False):
     if t.dtype is not _dtypes[dtype] or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous CUDA tensor of {dtype} {tuple(shape)} is needed, got "
                          f"{t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'} on {t.device}")
+    if device is not None and t.get_device() != device:
+        _here(name, t)
     return t.data_ptr()
 
 
-def _want_at_least(name, t, dtype, n):
+def _want_at_least(name, t, dtype, n, device=None):
     """The address of a contiguous CUDA tensor of this type with at least n elements."""
     if t is None or t.dtype is not _dtypes[dtype] or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: a contiguous CUDA tensor of at least {n} {dtype} is needed")
+    if device is not None and t.get_device() != device:
+        _here(name, t)
     return t.data_ptr()
 
 
@@ -598,9 +603,12 @@ def workspace_grouped(cfg, max_tokens: int, device="cuda"):
 
 
 def _here(name, t):
-    """The kernels run on the current device: a tensor of another one is refused."""
-    if t.get_device() != _device():
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{_device()}")
+    """The current device, on which the kernels run: a tensor of another one is refused.  An entry
+    point asks with its first tensor and has the others compared with the number it gets."""
+    device = _device()
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{device}")
+    return device
 
 
 def _slots(c):
@@ -614,7 +622,7 @@ def _rows(c, T):
     return moe_max_padded_rows(c, T)
 
 
-def _want_rows(name, t, rows):
+def _want_rows(name, t, rows, device=None):
     """The address and the columns of a [rows, columns] bf16 tensor."""
     shape = () if t is None else t.shape   # (each look at a tensor's attributes takes about a tenth of a microsecond)
     if len(shape) != 2:
@@ -622,15 +630,17 @@ def _want_rows(name, t, rows):
     columns = shape[1]
     if shape[0] != rows or t.dtype is not _dtypes["bfloat16"] or not t.is_cuda or not t.is_contiguous():
         _want(name, t, "bfloat16", (rows, columns))
+    if device is not None and t.get_device() != device:
+        _here(name, t)
     return t.data_ptr(), columns
 
 
-def _want_groups(c, rows, sorted_route_ids, expert_counts, ws, gathered):
+def _want_groups(c, rows, sorted_route_ids, expert_counts, ws, gathered, device):
     ids = None
     if gathered or sorted_route_ids is not None:
-        ids = _want_at_least("sorted_route_ids", sorted_route_ids, "int32", rows)
-    return (ids, _want("expert_counts", expert_counts, "int32", (c.num_experts,)),
-            _want_at_least("ws", ws, "uint8", 1))
+        ids = _want_at_least("sorted_route_ids", sorted_route_ids, "int32", rows, device)
+    return (ids, _want("expert_counts", expert_counts, "int32", (c.num_experts,), device=device),
+            _want_at_least("ws", ws, "uint8", 1, device))
 
 
 def moe_grouped_gemm(cfg, T, x, w, sorted_route_ids, expert_counts, y_perm, ws, gather=False, transposed=False,
@@ -640,10 +650,10 @@ def moe_grouped_gemm(cfg, T, x, w, sorted_route_ids, expert_counts, y_perm, ws, 
     c = _cfg(cfg)
     rows = _rows(c, T)
     px, K = _want_rows("x", x, T if gather else rows)
-    py, F = _want_rows("y_perm", y_perm, rows)
-    pw = _want("w", w, "bfloat16", (c.num_experts, F, K) if transposed else (c.num_experts, K, F))
-    ids, counts, pws = _want_groups(c, rows, sorted_route_ids, expert_counts, ws, gather)
-    _here("x", x)
+    dev = _here("x", x)
+    py, F = _want_rows("y_perm", y_perm, rows, dev)
+    pw = _want("w", w, "bfloat16", (c.num_experts, F, K) if transposed else (c.num_experts, K, F), device=dev)
+    ids, counts, pws = _want_groups(c, rows, sorted_route_ids, expert_counts, ws, gather, dev)
     flags = (MOE_GROUPED_GATHER if gather else 0) | (MOE_GROUPED_TRANSPOSED if transposed else 0)
     _check("moe_grouped_gemm", _lib.moe_grouped_gemm(ctypes.byref(c), T, K, F, flags, px, pw, ids, counts, py, pws,
                                                      ws.numel(), _stream(stream)))
@@ -656,13 +666,13 @@ def moe_grouped_wgrad(cfg, T, x, dy, sorted_route_ids, expert_counts, dw, ws, dw
     c = _cfg(cfg)
     rows = _rows(c, T)
     px, K = _want_rows("x", x, T if gather_x else rows)
-    pdy, F = _want_rows("dy", dy, T if gather_dy else rows)
+    dev = _here("x", x)
+    pdy, F = _want_rows("dy", dy, T if gather_dy else rows, dev)
     shape = (c.num_experts, K, F)
     bf16 = dw is not None and dw.dtype is _dtypes["bfloat16"]
-    pdw = _want("dw", dw, "bfloat16" if bf16 else "float32", shape)
-    padd = _want("dw_add", dw_add, "float32", shape, optional=True)
-    ids, counts, pws = _want_groups(c, rows, sorted_route_ids, expert_counts, ws, gather_x or gather_dy)
-    _here("x", x)
+    pdw = _want("dw", dw, "bfloat16" if bf16 else "float32", shape, device=dev)
+    padd = _want("dw_add", dw_add, "float32", shape, optional=True, device=dev)
+    ids, counts, pws = _want_groups(c, rows, sorted_route_ids, expert_counts, ws, gather_x or gather_dy, dev)
     flags = ((MOE_WGRAD_GATHER_X if gather_x else 0) | (MOE_WGRAD_GATHER_DY if gather_dy else 0)
              | (MOE_WGRAD_BF16 if bf16 else 0))
     _check("moe_grouped_wgrad", _lib.moe_grouped_wgrad(ctypes.byref(c), T, K, F, flags, px, pdy, ids, counts, padd,
@@ -671,31 +681,32 @@ def moe_grouped_wgrad(cfg, T, x, dy, sorted_route_ids, expert_counts, dw, ws, dw
 
 def _want_swiglu(c, T, gu, topk_gate, sorted_route_ids, num_padded):
     rows = _rows(c, T)
-    return (rows, _want("gu", gu, "bfloat16", (rows, 2 * c.intermediate)),
-            _want("topk_gate", topk_gate, "float32", (T, _slots(c)), True),
-            _want_at_least("sorted_route_ids", sorted_route_ids, "int32", rows),
-            _want_at_least("num_padded", num_padded, "int32", 1))
+    pgu = _want("gu", gu, "bfloat16", (rows, 2 * c.intermediate))
+    dev = _here("gu", gu)
+    return (rows, dev, pgu, _want("topk_gate", topk_gate, "float32", (T, _slots(c)), True, dev),
+            _want_at_least("sorted_route_ids", sorted_route_ids, "int32", rows, dev),
+            _want_at_least("num_padded", num_padded, "int32", 1, dev))
 
 
 def moe_swiglu(cfg, T, gu, topk_gate, sorted_route_ids, num_padded, a, stream=None):
     """a [rows, I] = gate * silu(g) * u from gu [rows, 2I]; topk_gate [T, S] or None."""
     c = _cfg(cfg)
-    rows, pgu, gate, ids, npad = _want_swiglu(c, T, gu, topk_gate, sorted_route_ids, num_padded)
-    _here("gu", gu)
+    rows, dev, pgu, gate, ids, npad = _want_swiglu(c, T, gu, topk_gate, sorted_route_ids, num_padded)
     _check("moe_swiglu", _lib.moe_swiglu(ctypes.byref(c), T, pgu, gate, ids, npad,
-                                         _want("a", a, "bfloat16", (rows, c.intermediate)), _stream(stream)))
+                                         _want("a", a, "bfloat16", (rows, c.intermediate), device=dev),
+                                         _stream(stream)))
 
 
 def moe_swiglu_backward(cfg, T, gu, topk_gate, da, sorted_route_ids, num_padded, dgu, dgate=None, a=None, stream=None):
     """dgu [rows, 2I], dgate [T, S] fp32 and the activation a from da [rows, I]; dgate and a may be None."""
     c = _cfg(cfg)
-    rows, pgu, gate, ids, npad = _want_swiglu(c, T, gu, topk_gate, sorted_route_ids, num_padded)
-    _here("gu", gu)
+    rows, dev, pgu, gate, ids, npad = _want_swiglu(c, T, gu, topk_gate, sorted_route_ids, num_padded)
     one = (rows, c.intermediate)
     _check("moe_swiglu_backward", _lib.moe_swiglu_backward(
-        ctypes.byref(c), T, pgu, gate, _want("da", da, "bfloat16", one), ids, npad,
-        _want("dgu", dgu, "bfloat16", (rows, 2 * c.intermediate)),
-        _want("dgate", dgate, "float32", (T, _slots(c)), True), _want("a", a, "bfloat16", one, True), _stream(stream)))
+        ctypes.byref(c), T, pgu, gate, _want("da", da, "bfloat16", one, device=dev), ids, npad,
+        _want("dgu", dgu, "bfloat16", (rows, 2 * c.intermediate), device=dev),
+        _want("dgate", dgate, "float32", (T, _slots(c)), True, dev), _want("a", a, "bfloat16", one, True, dev),
+        _stream(stream)))
 
 
 def moe_add_layer_norm(x, residual, weight, bias, eps, residual_out, out, stream=None):
@@ -703,12 +714,12 @@ def moe_add_layer_norm(x, residual, weight, bias, eps, residual_out, out, stream
     and residual_out may be None."""
     shape = T, H = x.shape
     px = _want("x", x, "bfloat16", shape)
-    _here("x", x)
+    dev = _here("x", x)
     _check("moe_add_layer_norm", _lib.moe_add_layer_norm(
-        T, H, px, _want("residual", residual, "bfloat16", shape, True),
-        _want("weight", weight, "bfloat16", (H,)), _want("bias", bias, "bfloat16", (H,), True), eps,
-        _want("residual_out", residual_out, "bfloat16", shape, True), _want("out", out, "bfloat16", shape),
-        _stream(stream)))
+        T, H, px, _want("residual", residual, "bfloat16", shape, True, dev),
+        _want("weight", weight, "bfloat16", (H,), device=dev), _want("bias", bias, "bfloat16", (H,), True, dev), eps,
+        _want("residual_out", residual_out, "bfloat16", shape, True, dev),
+        _want("out", out, "bfloat16", shape, device=dev), _stream(stream)))
 
 
 def moe_workspace_bytes_norm_backward(max_tokens: int, H: int) -> int:
@@ -729,10 +740,10 @@ def moe_norm_backward(v, dout, dresidual, weight, eps, dx, dweight, dbias, ws, c
     dbias [H] fp32; dresidual, dweight and dbias may be None."""
     shape = T, H = v.shape
     pv = _want("v", v, "bfloat16", shape)
-    _here("v", v)
+    dev = _here("v", v)
     _check("moe_norm_backward", _lib.moe_norm_backward(
-        T, H, int(centre), pv, _want("dout", dout, "bfloat16", shape),
-        _want("dresidual", dresidual, "bfloat16", shape, True), _want("weight", weight, "bfloat16", (H,)), eps,
-        _want("dx", dx, "bfloat16", shape), _want("dweight", dweight, "float32", (H,), True),
-        _want("dbias", dbias, "float32", (H,), True), _want_at_least("ws", ws, "uint8", 1), ws.numel(),
-        _stream(stream)))
+        T, H, int(centre), pv, _want("dout", dout, "bfloat16", shape, device=dev),
+        _want("dresidual", dresidual, "bfloat16", shape, True, dev),
+        _want("weight", weight, "bfloat16", (H,), device=dev), eps, _want("dx", dx, "bfloat16", shape, device=dev),
+        _want("dweight", dweight, "float32", (H,), True, dev), _want("dbias", dbias, "float32", (H,), True, dev),
+        _want_at_least("ws", ws, "uint8", 1, dev), ws.numel(), _stream(stream)))
