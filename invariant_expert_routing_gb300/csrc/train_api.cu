@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 
 #include "api_internal.h"
 #include "grouped.h"
@@ -19,6 +20,26 @@ constexpr size_t kGroupedWorkspace = 256;
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a && b && x < y + bn && y < x + an;
+}
+
+// Whether an output lies over an input or over another output.  An input that an
+// output may be in place of is left out (null) where it is that output.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool clash(std::initializer_list<Span> out, std::initializer_list<Span> in) {
+  for (const Span* o = out.begin(); o != out.end(); ++o) {
+    for (const Span& i : in)
+      if (overlap(o->p, o->bytes, i.p, i.bytes)) return true;
+    for (const Span* q = o + 1; q != out.end(); ++q)
+      if (overlap(o->p, o->bytes, q->p, q->bytes)) return true;
+  }
+  return false;
+}
+template <class T>
+const T* unless(const void* same, const T* p) {
+  return p == same ? nullptr : p;
 }
 
 moe_status check_width(int32_t n) {
@@ -149,7 +170,12 @@ moe_status moe_swiglu(const moe_config* cfg, int32_t T, const uint16_t* gu, cons
   MOE_TRY(api::need(a));
   const int64_t rows = api::max_rows(cfg, T);
   const int I = cfg->intermediate;
-  if (overlap(a, 2 * (size_t)rows * I, gu, 4 * (size_t)rows * I)) return MOE_ERR_INVALID_ARG;
+  const size_t gates = sizeof(float) * (size_t)T * api::slots(cfg);
+  if (clash({{a, 2 * (size_t)rows * I}}, {{gu, 4 * (size_t)rows * I},
+                                          {topk_gate, gates},
+                                          {sorted_route_ids, sizeof(int32_t) * (size_t)rows},
+                                          {num_padded, sizeof(int32_t)}}))
+    return MOE_ERR_INVALID_ARG;
   moe::launch_swiglu(gu, topk_gate, sorted_route_ids, num_padded, rows, T * api::slots(cfg), I, a,
                      static_cast<cudaStream_t>(stream));
   return api::last_error();
@@ -171,12 +197,13 @@ moe_status moe_swiglu_backward(const moe_config* cfg, int32_t T, const uint16_t*
   MOE_TRY(api::optional(a));
   const int64_t rows = api::max_rows(cfg, T);
   const int I = cfg->intermediate;
-  const size_t one = 2 * (size_t)rows * I;
-  if ((dgu != gu && overlap(dgu, 2 * one, gu, 2 * one)) || overlap(dgu, 2 * one, da, one) ||
-      (a != da && overlap(a, one, da, one)) || overlap(a, one, gu, 2 * one) || overlap(a, one, dgu, 2 * one))
-    return MOE_ERR_INVALID_ARG;
-  const size_t gates = sizeof(float) * (size_t)T * api::slots(cfg);
-  if (overlap(dgate, gates, topk_gate, gates) || overlap(dgate, gates, dgu, 2 * one) || overlap(dgate, gates, a, one))
+  const size_t one = 2 * (size_t)rows * I, gates = sizeof(float) * (size_t)T * api::slots(cfg);
+  // (a CTA stores its row's entry of dgate while others still read gu and da)
+  if (clash({{dgu, 2 * one}, {a, one}, {dgate, gates}}, {{unless(dgu, gu), 2 * one},
+                                                         {unless(a, da), one},
+                                                         {topk_gate, gates},
+                                                         {sorted_route_ids, sizeof(int32_t) * (size_t)rows},
+                                                         {num_padded, sizeof(int32_t)}}))
     return MOE_ERR_INVALID_ARG;
   moe::launch_swiglu_backward(gu, topk_gate, da, sorted_route_ids, num_padded, rows, T * api::slots(cfg), I, dgu, dgate,
                               a, static_cast<cudaStream_t>(stream));

@@ -1,0 +1,57 @@
+"""Outputs of the training step's entry points that lie over an input, the workspace or another output are refused
+before any launch (no GPU needed)."""
+import ctypes
+
+import pytest
+
+from tests.test_abi import moe  # noqa: F401
+
+T, H, I, N, S, B, K, F = 64, 128, 256, 8, 2, 8, 128, 512
+ROWS = T * S + N * (B - 1)
+CFG = dict(hidden=H, num_experts=N, top_k=S, intermediate=I, block_size=B)
+INVALID = 1
+# addresses far enough apart for every tensor of these sizes
+(GU, GATE, DA, IDS, PADDED, DGU, DGATE, A, X, R, W, BIAS, OUT, V, DOUT, DX, DW, DB, WS, COUNTS, Y) = (
+    0x100000000 * i for i in range(1, 22))
+
+
+def over(start, size, n):
+    """Addresses of n bytes that share 16 with [start, start + size): at its start, at its end, and (n larger) from before it."""
+    return [start, start + size - 16] + ([start - n + 16] if start >= n else [])
+
+
+def swiglu(moe, **kw):  # noqa: F811
+    t = dict(dict(gu=GU, gate=GATE, ids=IDS, padded=PADDED, a=A), **kw)
+    return moe._lib.moe_swiglu(ctypes.byref(moe.make_config(**CFG)), T, t["gu"], t["gate"], t["ids"], t["padded"], t["a"],
+                               None)
+
+
+def swiglu_backward(moe, **kw):  # noqa: F811
+    t = dict(dict(gu=GU, gate=GATE, da=DA, ids=IDS, padded=PADDED, dgu=DGU, dgate=DGATE, a=A), **kw)
+    return moe._lib.moe_swiglu_backward(ctypes.byref(moe.make_config(**CFG)), T, t["gu"], t["gate"], t["da"], t["ids"],
+                                        t["padded"], t["dgu"], t["dgate"], t["a"], None)
+
+
+SWIGLU = dict(gu=(GU, ROWS * 2 * I * 2), gate=(GATE, T * S * 4), da=(DA, ROWS * I * 2), ids=(IDS, ROWS * 4),
+              padded=(PADDED, 16), dgu=(DGU, ROWS * 2 * I * 2), dgate=(DGATE, T * S * 4), a=(A, ROWS * I * 2))
+
+
+@pytest.mark.parametrize("under", ["gu", "gate", "ids", "padded"])
+def test_swiglu(moe, under):  # noqa: F811
+    for p in over(*SWIGLU[under], SWIGLU["a"][1]):
+        assert swiglu(moe, a=p) == INVALID
+
+
+@pytest.mark.parametrize("out,under", [(o, u) for o in ("dgu", "dgate", "a") for u in SWIGLU if u != o])
+def test_swiglu_backward(moe, out, under):  # noqa: F811
+    in_place = {("dgu", "gu"), ("a", "da")}
+    for p in over(*SWIGLU[under], SWIGLU[out][1]):
+        if (out, under) not in in_place or p != SWIGLU[under][0]:
+            assert swiglu_backward(moe, **{out: p}) == INVALID
+
+
+@pytest.mark.parametrize("out,under", [("dgate", "gu"), ("dgate", "da"), ("dgate", "ids")])
+def test_swiglu_backward_in_place(moe, out, under):  # noqa: F811
+    """What is in place of an input is an output all the same."""
+    for p in over(*SWIGLU[under], SWIGLU[out][1]):
+        assert swiglu_backward(moe, dgu=GU, a=DA, **{out: p}) == INVALID
