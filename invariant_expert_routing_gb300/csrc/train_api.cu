@@ -221,9 +221,9 @@ moe_status moe_add_layer_norm(int32_t T, int32_t H, const uint16_t* x, const uin
   MOE_TRY(api::optional(residual_out));
   MOE_TRY(api::need(out));
   const size_t n = 2 * (size_t)T * H;
-  for (const uint16_t* in : {x, residual})
-    for (const uint16_t* o : {(const uint16_t*)residual_out, (const uint16_t*)out})
-      if (o != in && overlap(o, n, in, n)) return MOE_ERR_INVALID_ARG;
+  for (const uint16_t* o : {(const uint16_t*)residual_out, (const uint16_t*)out})
+    if (clash({{o, n}}, {{unless(o, x), n}, {unless(o, residual), n}, {weight, 2 * (size_t)H}, {bias, 2 * (size_t)H}}))
+      return MOE_ERR_INVALID_ARG;
   if (overlap(out, n, residual_out, n)) return MOE_ERR_INVALID_ARG;
   const int sms = api::sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
@@ -255,14 +255,13 @@ moe_status moe_norm_backward(int32_t T, int32_t H, int32_t centre, const uint16_
   MOE_TRY(api::need(weight));
   MOE_TRY(api::need(dx));
   MOE_TRY(api::need(ws));
-  if (ws_bytes < moe::norm_backward_scratch_bytes(T, H)) return MOE_ERR_WORKSPACE;
-  const size_t n = 2 * (size_t)T * H;
-  if (overlap(dx, n, v, n) || overlap(dx, n, dout, n) || (dx != dresidual && overlap(dx, n, dresidual, n)))
+  const size_t scratch = moe::norm_backward_scratch_bytes(T, H);
+  if (ws_bytes < scratch) return MOE_ERR_WORKSPACE;
+  const size_t n = 2 * (size_t)T * H, sum_bytes = sizeof(float) * (size_t)H;
+  // (the CTAs store their columns' sums into ws while others read rows and write dx)
+  if (clash({{dx, n}, {dweight, sum_bytes}, {dbias, sum_bytes}, {ws, scratch}},
+            {{v, n}, {dout, n}, {unless(dx, dresidual), n}, {weight, 2 * (size_t)H}}))
     return MOE_ERR_INVALID_ARG;
-  const size_t sum_bytes = sizeof(float) * (size_t)H;
-  if (overlap(dweight, sum_bytes, dbias, sum_bytes)) return MOE_ERR_INVALID_ARG;
-  for (const float* p : {dweight, dbias})
-    if (overlap(p, sum_bytes, dx, n) || overlap(p, sum_bytes, ws, ws_bytes)) return MOE_ERR_INVALID_ARG;
   moe::launch_norm_backward(v, dout, dresidual, weight, eps, T, H, centre != 0, dx, dweight, dbias, ws, s);
   return api::last_error();
 }

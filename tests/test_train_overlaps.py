@@ -55,3 +55,37 @@ def test_swiglu_backward_in_place(moe, out, under):  # noqa: F811
     """What is in place of an input is an output all the same."""
     for p in over(*SWIGLU[under], SWIGLU[out][1]):
         assert swiglu_backward(moe, dgu=GU, a=DA, **{out: p}) == INVALID
+
+
+def layer_norm(moe, **kw):  # noqa: F811
+    t = dict(dict(x=X, r=R, w=W, b=BIAS, ro=V, out=OUT), **kw)
+    return moe._lib.moe_add_layer_norm(T, H, t["x"], t["r"], t["w"], t["b"], 1e-5, t["ro"], t["out"], None)
+
+
+NORM = dict(x=(X, T * H * 2), r=(R, T * H * 2), w=(W, H * 2), b=(BIAS, H * 2), ro=(V, T * H * 2), out=(OUT, T * H * 2))
+
+
+@pytest.mark.parametrize("out,under", [(o, u) for o in ("ro", "out") for u in NORM if u != o])
+def test_add_layer_norm(moe, out, under):  # noqa: F811
+    for p in over(*NORM[under], NORM[out][1]):
+        if under not in ("x", "r") or p != NORM[under][0]:   # in place
+            assert layer_norm(moe, **{out: p}) == INVALID
+
+
+def norm_backward(moe, n, **kw):  # noqa: F811
+    t = dict(dict(v=V, dout=DOUT, r=R, w=W, dx=DX, dw=DW, db=DB, ws=WS), **kw)
+    return moe._lib.moe_norm_backward(T, H, 1, t["v"], t["dout"], t["r"], t["w"], 1e-5, t["dx"], t["dw"], t["db"], t["ws"],
+                                      n, None)
+
+
+@pytest.mark.parametrize("out", ["dx", "dw", "db", "ws"])
+@pytest.mark.parametrize("under", ["v", "dout", "r", "w", "dx", "dw", "db", "ws"])
+def test_norm_backward(moe, out, under):  # noqa: F811
+    if out == under:
+        return
+    n = moe.moe_workspace_bytes_norm_backward(T, H)
+    at = dict(v=(V, T * H * 2), dout=(DOUT, T * H * 2), r=(R, T * H * 2), w=(W, H * 2), dx=(DX, T * H * 2), dw=(DW, H * 4),
+              db=(DB, H * 4), ws=(WS, n))
+    for p in over(*at[under], at[out][1]):
+        if (out, under) != ("dx", "r") or p != R:   # in place
+            assert norm_backward(moe, n, **{out: p}) == INVALID
