@@ -101,9 +101,12 @@ moe_status moe_grouped_gemm(const moe_config* cfg, int32_t T, int32_t K, int32_t
   if (ws_bytes < kGroupedWorkspace) return MOE_ERR_WORKSPACE;
   moe::GroupedGemmArgs a{};
   a.g = group_args(cfg, T, K, F, sorted_route_ids, expert_counts, ws);
-  const size_t rows = (size_t)a.g.max_rows, y_bytes = 2 * rows * F;
-  if (overlap(y_perm, y_bytes, x, 2 * (gather ? (size_t)T : rows) * K) ||
-      overlap(y_perm, y_bytes, w, 2 * (size_t)a.g.N * K * F))
+  const size_t rows = (size_t)a.g.max_rows;
+  if (clash({{y_perm, 2 * rows * F}, {ws, kGroupedWorkspace}},
+            {{x, 2 * (gather ? (size_t)T : rows) * K},
+             {w, 2 * (size_t)a.g.N * K * F},
+             {gather ? sorted_route_ids : nullptr, sizeof(int32_t) * rows},
+             {expert_counts, sizeof(int32_t) * (size_t)a.g.N}}))
     return MOE_ERR_INVALID_ARG;
   a.x = x;
   a.w = w;
@@ -143,8 +146,12 @@ moe_status moe_grouped_wgrad(const moe_config* cfg, int32_t T, int32_t K, int32_
   moe::GroupedWgradArgs a{};
   a.g = group_args(cfg, T, K, F, sorted_route_ids, expert_counts, ws);
   const size_t rows = (size_t)a.g.max_rows;
-  if (overlap(dw, dw_bytes, x, 2 * (gx ? (size_t)T : rows) * K) ||
-      overlap(dw, dw_bytes, dy, 2 * (gd ? (size_t)T : rows) * F))
+  if (clash({{dw, dw_bytes}, {ws, kGroupedWorkspace}},
+            {{x, 2 * (gx ? (size_t)T : rows) * K},
+             {dy, 2 * (gd ? (size_t)T : rows) * F},
+             {unless(dw, dw_add), dw_bytes},
+             {gx || gd ? sorted_route_ids : nullptr, sizeof(int32_t) * rows},
+             {expert_counts, sizeof(int32_t) * (size_t)a.g.N}}))
     return MOE_ERR_INVALID_ARG;
   a.x = x;
   a.dy = dy;

@@ -89,3 +89,27 @@ def test_norm_backward(moe, out, under):  # noqa: F811
     for p in over(*at[under], at[out][1]):
         if (out, under) != ("dx", "r") or p != R:   # in place
             assert norm_backward(moe, n, **{out: p}) == INVALID
+
+
+def grouped(moe, op, **kw):  # noqa: F811
+    c = moe.make_config(**CFG)
+    t = dict(dict(x=X, w=W, dy=DOUT, ids=IDS, counts=COUNTS, y=Y, dw=DW, add=None, ws=WS), **kw)
+    if op == "gemm":
+        return moe._lib.moe_grouped_gemm(ctypes.byref(c), T, K, F, 1, t["x"], t["w"], t["ids"], t["counts"], t["y"],
+                                         t["ws"], 256, None)
+    return moe._lib.moe_grouped_wgrad(ctypes.byref(c), T, K, F, 1, t["x"], t["dy"], t["ids"], t["counts"], t["add"],
+                                      t["dw"], t["ws"], 256, None)
+
+
+GROUPED = dict(x=(X, T * K * 2), w=(W, N * K * F * 2), dy=(DOUT, ROWS * F * 2), ids=(IDS, ROWS * 4), counts=(COUNTS, N * 4),
+               ws=(WS, 256), y=(Y, ROWS * F * 2), dw=(DW, N * K * F * 4), add=(GU, N * K * F * 4))
+
+
+@pytest.mark.parametrize("op,out,under", [("gemm", o, u) for o in ("y", "ws") for u in ("x", "w", "ids", "counts", "ws", "y")
+                                          if u != o] +
+                         [("wgrad", o, u) for o in ("dw", "ws") for u in ("x", "dy", "ids", "counts", "add", "ws", "dw")
+                          if u != o])
+def test_grouped(moe, op, out, under):  # noqa: F811
+    for p in over(*GROUPED[under], GROUPED[out][1]):
+        if (out, under) != ("dw", "add") or p != GU:   # in place
+            assert grouped(moe, op, **{out: p}, **({"add": GU} if op == "wgrad" else {})) == INVALID
