@@ -240,7 +240,8 @@ moe_status moe_add_layer_norm(int32_t T, int32_t H, const uint16_t* x, const uin
 }
 
 size_t moe_workspace_bytes_norm_backward(int32_t max_tokens, int32_t H) {
-  return check_norm(max_tokens, H, 0.0f) == MOE_OK ? moe::norm_backward_scratch_bytes(max_tokens, H) : 0;
+  // (no tokens are as valid as any number, and need a workspace of no more than one)
+  return check_norm(max_tokens, H, 0.0f) == MOE_OK ? moe::norm_backward_scratch_bytes(max_tokens ? max_tokens : 1, H) : 0;
 }
 
 moe_status moe_norm_backward(int32_t T, int32_t H, int32_t centre, const uint16_t* v, const uint16_t* dout,
