@@ -120,12 +120,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 // A warp holds two chunks of a row, and its columns' sums over all rows of the
 // CTA, in registers; the rows behind it are on their way into shared memory
 // (cp.async: a thread copies what it reads itself, so no barrier is needed for
-// them), as many as fit: two rows at a time with two behind them left memory idle
+// them): two rows at a time with two behind them left memory idle
 // (192 us for 16448 rows of 7168).  One barrier a row: it carries the row's
 // second moments together with the next row's sums, whose values stay in
 // registers (one chunk a warp, read twice: 173 us, by instruction issue).  Each
 // byte moves once.
 constexpr int kFusedMaxChunks = 32, kFusedMaxWarps = 16;
+// Rows in shared memory: 192 KB with 512 threads on the SM, in one CTA or in two.  Five,
+// which 480 threads leave room for, were no faster (16448 rows of 7168: 153.5 us for
+// 154.5, of 5120 and 7680 the same; the RMS norm with dbias 202 for 189).
+constexpr int kRing = 4;
 
 // Sums of four values over the CTA, known to every thread: lane halves and
 // quarters exchange values, so that each eighth lane group ends with one of the
@@ -210,7 +214,7 @@ enum Sums { kNone, kWeight, kBoth };
 // part [grid][2][H]: each CTA's sums over its rows (blockIdx.x + i gridDim.x) of
 // dout n and dout.  dx may be dresidual (no __restrict__): a row is copied
 // before it is written, by the same thread.
-template <bool kCentre, Sums kSums, int kThreads, int kRing>
+template <bool kCentre, Sums kSums, int kThreads>
 __global__ void __launch_bounds__(kThreads, 512 / kThreads)
     norm_backward_kernel(const uint16_t* v_in, const uint16_t* dout, const uint16_t* dresidual,
                          const uint16_t* __restrict__ weight, float eps, int T, int H, uint16_t* dx,
@@ -674,10 +678,10 @@ void launch_wide(const uint16_t* v, const uint16_t* dout, const uint16_t* dresid
   launch_pdl(kernel, dim3(ctas), dim3(kWideThreads), slots * 6 * H, s, v, dout, dresidual, weight, eps, T, H, slots, dx, part);
 }
 
-template <bool kCentre, Sums kSums, int kThreads, int kRing>
+template <bool kCentre, Sums kSums, int kThreads>
 void launch_fused(const uint16_t* v, const uint16_t* dout, const uint16_t* dresidual, const uint16_t* weight, float eps,
                   int T, int H, uint16_t* dx, float* part, int ctas, cudaStream_t s) {
-  auto kernel = norm_backward_kernel<kCentre, kSums, kThreads, kRing>;
+  auto kernel = norm_backward_kernel<kCentre, kSums, kThreads>;
   const int threads = fused_threads(H), smem = kRing * 6 * 16 * threads;
   static bool attr_set[64] = {false};
   int dev = 0;
@@ -699,16 +703,13 @@ void launch_norm_backward(const uint16_t* v, const uint16_t* dout, const uint16_
   if (chunks <= kWideMaxChunks) {
     slabs = fused_ctas(H, T);
     auto go = [&](auto kernel) { kernel(v, dout, dresidual, weight, eps, T, H, dx, part, slabs, s); };
-    // rows in shared memory: what 227 KB hold, of the CTAs on an SM together
     auto sized = [&](auto c, auto n) {
       constexpr bool kCentre = decltype(c)::value;
       constexpr Sums kSums = decltype(n)::value;
       if (chunks <= 16)
-        go(launch_fused<kCentre, kSums, 256, 4>);
-      else if (chunks <= 28)
-        go(launch_fused<kCentre, kSums, 448, 5>);
+        go(launch_fused<kCentre, kSums, 256>);
       else if (chunks <= kFusedMaxChunks)
-        go(launch_fused<kCentre, kSums, 512, 4>);
+        go(launch_fused<kCentre, kSums, 512>);
       else
         go(launch_wide<kCentre, kSums>);
     };
