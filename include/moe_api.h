@@ -593,14 +593,18 @@ moe_status moe_forward_mx(const moe_config* cfg, const moe_scoring* scoring, int
  *   dw13  = moe_grouped_wgrad(h, dgu, GATHER_X)
  *   dx    = moe_grouped_gemm(dgu, w13, TRANSPOSED)        [rows, H]
  *   dh    = moe_combine(dout, gates of 1, dx)
+ * The step starts and ends at the gates: the gradient from dgate through the
+ * (renormalised) scores into w_gate, the router's bias and the layer's input is
+ * the caller's to compute and to add to dh, and so is a shared expert's.
  *
  * Rows are grouped as the dispatch lays them out: expert e's segment starts
  * at the sum of the earlier experts' expert_counts, each rounded up to a
  * multiple of B, and holds expert_counts[e] rows.  A gathered operand is
  * [T, columns]: row p of the segment reads its row sorted_route_ids[p] / S (an
  * id outside [0, T*S) reads zeros).  An operand in place is [rows, columns],
- * rows = moe_max_padded_rows(cfg, T).  Rows of the padding are neither read
- * nor written, whatever they hold.  Counts that are negative or need more than
+ * rows = moe_max_padded_rows(cfg, T).  Rows of the padding are not written
+ * and change no result, whatever they hold (a product in place may load them with
+ * the rows before them).  Counts that are negative or need more than
  * rows rows set MOE_DEV_ERR_BAD_BLOCKS and nothing is computed.
  * cfg gives N, B, the slots and the bound on the rows; K and F are multiples
  * of 8 up to 65536, free of cfg's hidden and intermediate.
@@ -617,8 +621,11 @@ size_t moe_workspace_bytes_grouped(const moe_config* cfg, int32_t max_tokens);
  *   x [T, K] (GATHER) or [rows, K] bf16;  y_perm [rows, F] bf16 out
  *   w [N, K, F] bf16, with TRANSPOSED [N, F, K] (the product with W_e^T: the
  *   gradient of the input of a product with w [N, F, K])
- * sorted_route_ids may be NULL without GATHER.  y_perm may not overlap x or w.
- * One K order for every T, no split-K: a row does not depend on the batch. */
+ * sorted_route_ids may be NULL without GATHER.  y_perm and ws overlap nothing
+ * else that the call is given.  One K order for every T, no split-K: a row does not
+ * depend on the batch.  The tensor cores add 16 products of K at a time and
+ * truncate the sum to fp32: off by at most K / 16 steps of 2^-23 of the sum so
+ * far, before the one rounding to bf16 (2^-8 of the result). */
 #define MOE_GROUPED_GATHER 0x1u
 #define MOE_GROUPED_TRANSPOSED 0x2u
 moe_status moe_grouped_gemm(const moe_config* cfg, int32_t T, int32_t K, int32_t F, uint32_t flags, const uint16_t* x,
@@ -630,8 +637,8 @@ moe_status moe_grouped_gemm(const moe_config* cfg, int32_t T, int32_t K, int32_t
  * same bits on every run).  An expert without rows gets dw_add or zeros.
  *   x  [T, K] (GATHER_X) or [rows, K] bf16, dy [T, F] (GATHER_DY) or [rows, F]
  *   dw [N, K, F] fp32 out, with BF16 bf16 (rounded once)
- *   dw_add [N, K, F] fp32 or NULL, may be dw itself (no other overlap); not
- *   with BF16
+ *   dw_add [N, K, F] fp32 or NULL, may be dw itself (no other overlap of dw or
+ *   ws with what the call is given); not with BF16
  * T = 0 writes dw too: dw_add or zeros. */
 #define MOE_WGRAD_GATHER_X 0x1u
 #define MOE_WGRAD_GATHER_DY 0x2u
@@ -646,6 +653,9 @@ moe_status moe_grouped_wgrad(const moe_config* cfg, int32_t T, int32_t K, int32_
  * are not written.
  *   gu [rows, 2I] bf16 (I = cfg->intermediate; the output of moe_grouped_gemm
  *   with w13), topk_gate [T, S] fp32 or NULL, a [rows, I] bf16 out, no overlap.
+ * 1 / (1 + e^-g) is formed with the hardware's exponential and division, off by at
+ * most (6 + 1.2 |g|) 2^-23 of it for g >= -87.3; below, where silu(g) is less than
+ * 2^-119, it is 0 instead.
  * With the gate here the second product needs none: moe_combine then runs
  * with gates of 1. */
 moe_status moe_swiglu(const moe_config* cfg, int32_t T, const uint16_t* gu, const float* topk_gate,
@@ -653,7 +663,8 @@ moe_status moe_swiglu(const moe_config* cfg, int32_t T, const uint16_t* gu, cons
 
 /* The gradient of moe_swiglu: with s = 1 / (1 + e^-g), per row
  *   dgu = bf16[ w da u s (1 + g (1 - s)) | w da silu(g) ]
- *   dgate[r] = sum over I of da silu(g) u   (fp32, one order for every T)
+ *   dgate[r] = sum over I of da silu(g) u   (fp32, one order for every T; each
+ *   silu(g) as far off as in moe_swiglu)
  *   a as in moe_swiglu (the activation need not be kept for the weight gradient)
  *   da [rows, I] bf16, dgu [rows, 2I] bf16 out, dgate [T, S] fp32 out or NULL
  *   (entries of routes that are in no row are not written), a [rows, I] bf16
@@ -670,8 +681,9 @@ moe_status moe_swiglu_backward(const moe_config* cfg, int32_t T, const uint16_t*
  *   bf16 or NULL, residual_out [T, H] bf16 or NULL, out [T, H] bf16.
  * var is the mean square of the deviations from the mean, computed from them.
  * residual_out may be x or residual itself, and so may out; no other overlap.
- * H % 8 == 0, H <= 32768.  Sums are fp32 in one order for every T; with eps = 0
- * a row of equal values gives NaN. */
+ * H % 8 == 0, H <= 32768.  Sums are fp32 in one order for every T.  With eps = 0
+ * a row of equal values has no norm: NaN where the sum of its values is exact,
+ * otherwise what the mean's rounding leaves. */
 moe_status moe_add_layer_norm(int32_t T, int32_t H, const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
                               const uint16_t* bias, float eps, uint16_t* residual_out, uint16_t* out, void* stream);
 
@@ -691,7 +703,11 @@ size_t moe_workspace_bytes_norm_backward(int32_t max_tokens, int32_t H);
  *   weight [H] bf16, dx [T, H] bf16 out, dweight, dbias [H] fp32 out or NULL.
  * The statistics are computed again from v.  dx may be dresidual; no other
  * overlap.  The sums over rows have one order for a given T and H, without
- * atomics.  T = 0 sets dweight and dbias to zero.  H as above. */
+ * atomics.  T = 0 sets dweight and dbias to zero.  H as above.
+ * moe_add_layer_norm and moe_add_norm normalise x + residual in fp32; this takes
+ * the statistics and n from v, which was rounded: in a row whose mean is m
+ * deviations n is up to about m 2^-8 off.  With eps = 0 one row without deviation
+ * makes all of dweight NaN, beside its row of dx. */
 moe_status moe_norm_backward(int32_t T, int32_t H, int32_t centre, const uint16_t* v, const uint16_t* dout,
                              const uint16_t* dresidual, const uint16_t* weight, float eps, uint16_t* dx, float* dweight,
                              float* dbias, void* ws, size_t ws_bytes, void* stream);

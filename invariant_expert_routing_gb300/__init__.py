@@ -432,20 +432,22 @@ def _want(name, t, dtype, shape, optional=False, device=None):
         if optional:
             return None
         raise ValueError(f"{name}: a tensor is needed")
-    if t.dtype is not _dtypes[dtype] or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+    if (t.dtype is not _dtypes[dtype] or t.shape != shape
+            or (not t.is_cuda if device is None else t.get_device() != device) or not t.is_contiguous()):
+        if device is not None and t.is_cuda:
+            _here(name, t)
         raise ValueError(f"{name}: a contiguous CUDA tensor of {dtype} {tuple(shape)} is needed, got "
                          f"{t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'} on {t.device}")
-    if device is not None and t.get_device() != device:
-        _here(name, t)
     return t.data_ptr()
 
 
 def _want_at_least(name, t, dtype, n, device=None):
     """The address of a contiguous CUDA tensor of this type with at least n elements."""
-    if t is None or t.dtype is not _dtypes[dtype] or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
+    if (t is None or t.dtype is not _dtypes[dtype] or t.numel() < n or not t.is_contiguous()
+            or (not t.is_cuda if device is None else t.get_device() != device)):
+        if t is not None and device is not None and t.is_cuda:
+            _here(name, t)
         raise ValueError(f"{name}: a contiguous CUDA tensor of at least {n} {dtype} is needed")
-    if device is not None and t.get_device() != device:
-        _here(name, t)
     return t.data_ptr()
 
 
@@ -628,10 +630,9 @@ def _want_rows(name, t, rows, device=None):
     if len(shape) != 2:
         raise ValueError(f"{name}: a 2-D tensor is needed")
     columns = shape[1]
-    if shape[0] != rows or t.dtype is not _dtypes["bfloat16"] or not t.is_cuda or not t.is_contiguous():
-        _want(name, t, "bfloat16", (rows, columns))
-    if device is not None and t.get_device() != device:
-        _here(name, t)
+    if (shape[0] != rows or t.dtype is not _dtypes["bfloat16"]
+            or (not t.is_cuda if device is None else t.get_device() != device) or not t.is_contiguous()):
+        _want(name, t, "bfloat16", (rows, columns), False, device)
     return t.data_ptr(), columns
 
 
@@ -639,7 +640,7 @@ def _want_groups(c, rows, sorted_route_ids, expert_counts, ws, gathered, device)
     ids = None
     if gathered or sorted_route_ids is not None:
         ids = _want_at_least("sorted_route_ids", sorted_route_ids, "int32", rows, device)
-    return (ids, _want("expert_counts", expert_counts, "int32", (c.num_experts,), device=device),
+    return (ids, _want("expert_counts", expert_counts, "int32", (c.num_experts,), False, device),
             _want_at_least("ws", ws, "uint8", 1, device))
 
 
@@ -652,7 +653,7 @@ def moe_grouped_gemm(cfg, T, x, w, sorted_route_ids, expert_counts, y_perm, ws, 
     px, K = _want_rows("x", x, T if gather else rows)
     dev = _here("x", x)
     py, F = _want_rows("y_perm", y_perm, rows, dev)
-    pw = _want("w", w, "bfloat16", (c.num_experts, F, K) if transposed else (c.num_experts, K, F), device=dev)
+    pw = _want("w", w, "bfloat16", (c.num_experts, F, K) if transposed else (c.num_experts, K, F), False, dev)
     ids, counts, pws = _want_groups(c, rows, sorted_route_ids, expert_counts, ws, gather, dev)
     flags = (MOE_GROUPED_GATHER if gather else 0) | (MOE_GROUPED_TRANSPOSED if transposed else 0)
     _check("moe_grouped_gemm", _lib.moe_grouped_gemm(ctypes.byref(c), T, K, F, flags, px, pw, ids, counts, py, pws,
@@ -670,8 +671,8 @@ def moe_grouped_wgrad(cfg, T, x, dy, sorted_route_ids, expert_counts, dw, ws, dw
     pdy, F = _want_rows("dy", dy, T if gather_dy else rows, dev)
     shape = (c.num_experts, K, F)
     bf16 = dw is not None and dw.dtype is _dtypes["bfloat16"]
-    pdw = _want("dw", dw, "bfloat16" if bf16 else "float32", shape, device=dev)
-    padd = _want("dw_add", dw_add, "float32", shape, optional=True, device=dev)
+    pdw = _want("dw", dw, "bfloat16" if bf16 else "float32", shape, False, dev)
+    padd = _want("dw_add", dw_add, "float32", shape, True, dev)
     ids, counts, pws = _want_groups(c, rows, sorted_route_ids, expert_counts, ws, gather_x or gather_dy, dev)
     flags = ((MOE_WGRAD_GATHER_X if gather_x else 0) | (MOE_WGRAD_GATHER_DY if gather_dy else 0)
              | (MOE_WGRAD_BF16 if bf16 else 0))
@@ -693,7 +694,7 @@ def moe_swiglu(cfg, T, gu, topk_gate, sorted_route_ids, num_padded, a, stream=No
     c = _cfg(cfg)
     rows, dev, pgu, gate, ids, npad = _want_swiglu(c, T, gu, topk_gate, sorted_route_ids, num_padded)
     _check("moe_swiglu", _lib.moe_swiglu(ctypes.byref(c), T, pgu, gate, ids, npad,
-                                         _want("a", a, "bfloat16", (rows, c.intermediate), device=dev),
+                                         _want("a", a, "bfloat16", (rows, c.intermediate), False, dev),
                                          _stream(stream)))
 
 
@@ -703,8 +704,8 @@ def moe_swiglu_backward(cfg, T, gu, topk_gate, da, sorted_route_ids, num_padded,
     rows, dev, pgu, gate, ids, npad = _want_swiglu(c, T, gu, topk_gate, sorted_route_ids, num_padded)
     one = (rows, c.intermediate)
     _check("moe_swiglu_backward", _lib.moe_swiglu_backward(
-        ctypes.byref(c), T, pgu, gate, _want("da", da, "bfloat16", one, device=dev), ids, npad,
-        _want("dgu", dgu, "bfloat16", (rows, 2 * c.intermediate), device=dev),
+        ctypes.byref(c), T, pgu, gate, _want("da", da, "bfloat16", one, False, dev), ids, npad,
+        _want("dgu", dgu, "bfloat16", (rows, 2 * c.intermediate), False, dev),
         _want("dgate", dgate, "float32", (T, _slots(c)), True, dev), _want("a", a, "bfloat16", one, True, dev),
         _stream(stream)))
 
@@ -717,9 +718,9 @@ def moe_add_layer_norm(x, residual, weight, bias, eps, residual_out, out, stream
     dev = _here("x", x)
     _check("moe_add_layer_norm", _lib.moe_add_layer_norm(
         T, H, px, _want("residual", residual, "bfloat16", shape, True, dev),
-        _want("weight", weight, "bfloat16", (H,), device=dev), _want("bias", bias, "bfloat16", (H,), True, dev), eps,
+        _want("weight", weight, "bfloat16", (H,), False, dev), _want("bias", bias, "bfloat16", (H,), True, dev), eps,
         _want("residual_out", residual_out, "bfloat16", shape, True, dev),
-        _want("out", out, "bfloat16", shape, device=dev), _stream(stream)))
+        _want("out", out, "bfloat16", shape, False, dev), _stream(stream)))
 
 
 def moe_workspace_bytes_norm_backward(max_tokens: int, H: int) -> int:
@@ -742,8 +743,8 @@ def moe_norm_backward(v, dout, dresidual, weight, eps, dx, dweight, dbias, ws, c
     pv = _want("v", v, "bfloat16", shape)
     dev = _here("v", v)
     _check("moe_norm_backward", _lib.moe_norm_backward(
-        T, H, int(centre), pv, _want("dout", dout, "bfloat16", shape, device=dev),
+        T, H, int(centre), pv, _want("dout", dout, "bfloat16", shape, False, dev),
         _want("dresidual", dresidual, "bfloat16", shape, True, dev),
-        _want("weight", weight, "bfloat16", (H,), device=dev), eps, _want("dx", dx, "bfloat16", shape, device=dev),
+        _want("weight", weight, "bfloat16", (H,), False, dev), eps, _want("dx", dx, "bfloat16", shape, False, dev),
         _want("dweight", dweight, "float32", (H,), True, dev), _want("dbias", dbias, "float32", (H,), True, dev),
         _want_at_least("ws", ws, "uint8", 1, dev), ws.numel(), _stream(stream)))

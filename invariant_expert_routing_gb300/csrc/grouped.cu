@@ -33,10 +33,18 @@
 // overlap the next one's MMAs.  Segments are found from the counts by every CTA,
 // so a product is one launch and no list lives in memory.
 //
-// Bounds, of the measured 1916 TFLOP/s: rows in place the tensor pipe (8192 rows
-// of 4096 a expert: 1855 the product, 1900 the gradient in bf16), gathered rows
-// the requests (a gather4 takes some 16 cycles, 32 of them a stage): W2's input
-// gradient of 4096 tokens in the 8-expert layer 577 us for 559 in place.
+// Times here are of one of the first 50 calls unless they are called sustained: a
+// loop of large products runs into the power cap, which takes the clock from 2070 to
+// some 1400 to 1700 MHz and a call up to 15 % longer.
+//
+// Bounds.  Two experts of about 4096 rows, 4096 x 14336 in place: 1840 TFLOP/s of the
+// measured 1916 the product, 1600 the bf16 gradient.  Sustained, in cycles of the
+// clock that was seen, the tensor pipe is busy 85 % in the 8-expert layer's input
+// gradient of W2 (4096 tokens) in place and 76 % gathered (658 and 670 us): the
+// requests of gathered rows, some 16 cycles a gather4 and 32 of them a stage, are the
+// difference.  In the 128-expert layer's W13 (8192 tokens) it is 67 % in place and
+// 62 % gathered (327 and 328 us): items of unequal height are handed out by number,
+// a two-group item's stores overlap no MMAs, and rows are rounded up to 32.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 #include <cmath>
@@ -72,7 +80,10 @@ __host__ __device__ constexpr bool wgrad(Mode m) { return m >= kWgrad; }
 // 1024 rows, 1e-5 for 8192 (2-norms; rounded sums would stay at 3e-7).  Longer
 // segments are summed part by part, the parts added (rounded to nearest) in the
 // other accumulator's columns, and the MMAs wait for that.  For bf16 results 1e-5
-// is nothing.
+// is nothing, and products, always bf16, are summed in one part whatever K: with K
+// 2048 and 4096 one result in 850 and in 420 rounds to the other neighbour than a
+// sum rounded at every step, and the error against 64 bits (1.66e-3 in the 2-norm,
+// the rounding to bf16) is the same in six digits.
 constexpr int kPartStagesFp32 = 12, kPartStagesBf16 = 128;
 
 // kWgradAdd reads and writes fp32 gradients at the rate of memory: four stages
