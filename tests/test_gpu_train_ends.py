@@ -59,6 +59,29 @@ def test_weight_gradients_keep_nan_and_infinities_in_their_columns(moe, add):
     assert torch.equal(dw[~hit], clean[~hit]) and not torch.isfinite(dw[hit]).any()
 
 
+def test_silu_of_every_bf16_value(moe):
+    """dgate of rows with one element whose da and u are 1 is silu(g) itself.  The exponential is off by (2 + 1.173 |g|) 2^-23,
+    the division by 2^-22 and the addition and the product with g by 2^-24 each: within (6 + 1.2 |g|) 2^-23."""
+    torch = torch_()
+    from tests import train_ref as R
+    bits = torch.arange(1 << 16, device="cuda", dtype=torch.int32).to(torch.int16)
+    v = bits.view(torch.bfloat16)
+    v = v[torch.isfinite(v)]
+    G = R.Groups(v.numel(), 1, 1, 8)
+    gu, da = (torch.zeros(G.rows, n, dtype=torch.bfloat16, device="cuda") for n in (256, 128))
+    token = G.ids[G.real].long()
+    gu[G.real, 5], gu[:, 128 + 5], da[:, 5] = v[token], 1, 1
+    dgu, dgate = torch.empty_like(gu), torch.empty(v.numel(), 1, device="cuda")
+    cfg = moe.make_config(128, 1, 1, 128, 8)
+    moe.moe_swiglu_backward(cfg, v.numel(), gu, None, da, G.ids, G.num_padded, dgu, dgate)
+    g, got = v.double(), dgate.flatten().double()
+    want = g * torch.sigmoid(g)
+    near = g >= -87.3
+    # (results below 2^-126 have no 24 bits)
+    R.check(got[near], want[near], (6 + 1.2 * g[near].abs().clamp(max=200)) * 2.0 ** -23 * want[near].abs() + 2.0 ** -149)
+    assert (got[g < -87.4] == 0).all() and want[g < -87.3].abs().max() < 2.0 ** -119
+
+
 WIDTHS = [264, 4096, 7168, 12288, 16392]           # a form of the norms each
 
 
